@@ -13,6 +13,11 @@ fallback: without the built library every call raises.
     v, xs = in_projection(u, bp)          # u [B, L, D] -> v, x_n [B, D, L]
     out   = out_projection(y, bp)         # [B, D, L] -> [B, L, D]
     out   = block_forward(u, bp, spec)    # all three in one call
+
+    # the state-space block (see ssm.py): norm, 8-bit projection, short convolution, selective scan
+    y, s  = rms_norm(x, weight, residual=s)
+    y     = short_conv(x, w, bias, silu=True)
+    y     = selective_scan(u, delta, A, Bm, Cm, z=z)
 """
 from __future__ import annotations
 
@@ -26,7 +31,11 @@ __all__ = ["HyenaError", "lib", "plan", "filter_gen", "filter_spectrum", "spectr
            "in_projection", "out_projection", "block_forward", "block_workspace_bytes", "PreparedCall",
            "prepare_in_projection", "prepare_out_projection", "prepare_block_forward", "backward",
            "backward_workspace_bytes", "filter_gen_li", "filter_gen_mr", "forward_fir", "nd_plan",
-           "nd_spectrum_bytes", "nd_workspace_bytes", "nd_filter_spectrum", "prepare_nd_forward", "nd_forward"]
+           "nd_spectrum_bytes", "nd_workspace_bytes", "nd_filter_spectrum", "prepare_nd_forward", "nd_forward",
+           "short_conv", "short_conv_step", "short_conv_backward", "short_conv_backward_workspace_bytes",
+           "selective_scan", "selective_scan_step", "selective_scan_backward", "selective_scan_workspace_bytes",
+           "selective_scan_backward_workspace_bytes", "rms_norm", "rms_norm_quantized", "rms_norm_backward",
+           "rms_norm_backward_workspace_bytes", "quantize", "scaled_matmul"]
 
 # HYENA_LIB names another build of the same library (tuning variants, the
 # host-sanitized build of the argument checks); the in-tree build otherwise.
@@ -166,6 +175,7 @@ def lib() -> ctypes.CDLL:
     L.hyena_nd_forward.argtypes = [vp, ctypes.POINTER(vp), vp, vp, i64, i32, i32, i32, i64p, i32, i32, i32, vp, i64,
                                    vp]
     L.hyena_nd_forward.restype = i32
+    ssm.declare(L)
     L.hyena_status_str.argtypes = [i32]
     L.hyena_status_str.restype = ctypes.c_char_p
     _lib = L
@@ -649,3 +659,12 @@ def prepare_nd_forward(v, xs, spec, circular: bool | None = None, per_sample: bo
 def nd_forward(v, xs, spec, circular: bool | None = None, per_sample: bool = False, out=None, workspace=None):
     """y = z_{N+1} of the order-N recurrence with grid convolutions."""
     return prepare_nd_forward(v, xs, spec, circular, per_sample, out, workspace)()
+
+
+# ----------------------------------------------------- the state-space block
+
+from . import ssm  # noqa: E402
+from .ssm import (quantize, rms_norm, rms_norm_backward, rms_norm_backward_workspace_bytes,  # noqa: E402
+                  rms_norm_quantized, scaled_matmul, selective_scan, selective_scan_backward,
+                  selective_scan_backward_workspace_bytes, selective_scan_step, selective_scan_workspace_bytes,
+                  short_conv, short_conv_backward, short_conv_backward_workspace_bytes, short_conv_step)

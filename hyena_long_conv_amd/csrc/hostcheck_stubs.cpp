@@ -1,11 +1,12 @@
 // hostcheck_stubs.cpp -- stand-ins for the kernel launchers, linked with
-// api.cpp into a host-only build of the C ABI (g++, AddressSanitizer and
+// api.cpp and api_ssm.cpp into a host-only build of the C ABI (g++, AddressSanitizer and
 // UndefinedBehaviorSanitizer; no GPU code).  That build exercises argument
 // validation, planning and the size queries on the CPU.  A call with bad
 // arguments must return its status before it reaches a launcher; a call
 // that gets this far receives hipErrorNoDevice, which the entry points
 // report as HYENA_ERR_HIP, the status a GPU-less host would see anyway.
 #include "launch.hpp"
+#include "ssm.hpp"
 
 namespace hyena {
 
@@ -37,5 +38,16 @@ hipError_t static_scratch(void**, int64_t*) { return kNoKernels; }
 hipError_t spectrum_to_fourstep(const void*, int, const PlanInfo&, const PlanInfo&, void*, hipStream_t) {
   return kNoKernels;
 }
+
+hipError_t short_conv(const ConvArgs&, hipStream_t) { return kNoKernels; }
+hipError_t short_conv_step(const ConvArgs&, hipStream_t) { return kNoKernels; }
+hipError_t short_conv_backward(const ConvArgs&, hipStream_t) { return kNoKernels; }
+hipError_t selective_scan(const ScanArgs&, hipStream_t) { return kNoKernels; }
+hipError_t selective_scan_step(const ScanArgs&, hipStream_t) { return kNoKernels; }
+hipError_t selective_scan_backward(const ScanArgs&, hipStream_t) { return kNoKernels; }
+hipError_t rms_norm(const NormArgs&, hipStream_t) { return kNoKernels; }
+hipError_t rms_norm_backward(const NormArgs&, hipStream_t) { return kNoKernels; }
+hipError_t quantize(const NormArgs&, hipStream_t) { return kNoKernels; }
+hipError_t scaled_matmul(const ScaledArgs&, hipStream_t) { return kNoKernels; }
 
 }  // namespace hyena

@@ -1,0 +1,320 @@
+// kernels_conv.hip -- the short causal depthwise convolution as an operator
+// of its own, forward, for single tokens, and backward.
+//
+//   p[t] = bias + sum_{j<T} w[j] x[t-j],   y = p  or  p * sigmoid(p)
+//
+// per channel; x[-1], x[-2], .. come from a carried state (zeros without
+// one), and the last T-1 inputs are what the next call carries.  Taps are
+// rounded up to TT = 4, 8 or 16 with zero weights.  A thread holds 8
+// consecutive outputs of a row and reads the TT values before them again,
+// from the cache that its neighbours' loads have filled: the bytes of x and y
+// bound the call.
+#include <hip/hip_runtime.h>
+
+#include "ssm.hpp"
+#include "ssm_device.hpp"
+
+namespace hyena {
+namespace {
+
+__device__ __forceinline__ int conv_length(const ConvArgs& a, int64_t b) {
+  if (!a.lengths) return (int)a.L;
+  const int n = a.lengths[b];
+  return n < 0 ? 0 : (n > a.L ? (int)a.L : n);
+}
+
+// The input at t of row r, from the state before the row's start.
+template <int IOT>
+__device__ __forceinline__ float conv_at(const ConvArgs& a, int64_t r, int64_t t) {
+  if (t >= 0) return ld1<IOT>(a.x, r * a.L + t);
+  const int64_t i = t + a.T - 1;
+  return a.state && i >= 0 ? ld1<IOT>(a.state, r * (a.T - 1) + i) : 0.f;
+}
+
+// v[0..n) = inputs t .. t+n of row r (n a multiple of 4, t possibly negative
+// or its end behind len; zeros there).
+template <int IOT, int N>
+__device__ __forceinline__ void conv_window(const ConvArgs& a, int64_t r, int t, int len, float (&v)[N]) {
+  if (t >= 0 && t + N <= len) {
+    const int64_t i = r * a.L + t;
+#pragma unroll
+    for (int k = 0; k < N; k += 4) {
+      if constexpr (IOT == 0) {
+        const f32x4v w = *reinterpret_cast<const f32x4_e4*>(static_cast<const float*>(a.x) + i + k);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[k + e] = w[e];
+      } else {
+        typedef uint32_t u2 __attribute__((ext_vector_type(2), aligned(2)));
+        const u2 w = *reinterpret_cast<const u2*>(static_cast<const uint16_t*>(a.x) + i + k);
+        v[k] = __uint_as_float(w.x << 16);
+        v[k + 1] = __uint_as_float(w.x & 0xffff0000u);
+        v[k + 2] = __uint_as_float(w.y << 16);
+        v[k + 3] = __uint_as_float(w.y & 0xffff0000u);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] = t + k < len ? conv_at<IOT>(a, r, t + k) : 0.f;
+  }
+}
+
+template <int TT>
+__device__ __forceinline__ void conv_taps(const ConvArgs& a, int d, float (&w)[TT]) {
+#pragma unroll
+  for (int j = 0; j < TT; ++j) w[j] = j < a.T ? a.w[(int64_t)d * a.T + j] : 0.f;
+}
+
+template <int IOT, int TT>
+__global__ __launch_bounds__(256) void k_conv(ConvArgs a, int per, int lper, int blocks) {
+  const int tid = threadIdx.x;
+  const int64_t rb = blockIdx.x / blocks;
+  const int xb = (int)(blockIdx.x - rb * blocks);
+  const int64_t r = rb * (256 >> lper) + (tid >> lper);
+  if (r >= (int64_t)a.B * a.D) return;
+  const int64_t b = r / a.D;
+  const int d = (int)(r - b * a.D), len = conv_length(a, b);
+  const int i = xb * per + (tid & (per - 1)), t = 8 * i;
+  if (a.state_out)
+    for (int k = i; k < a.T - 1; k += blocks * per)
+      st1<IOT>(a.state_out, r * (a.T - 1) + k, conv_at<IOT>(a, r, (int64_t)len - (a.T - 1) + k));
+  if (t >= a.L) return;
+  float x[TT + 8], w[TT], y[8];
+  conv_taps<TT>(a, d, w);
+  if (t < len) {
+    conv_window<IOT, TT + 8>(a, r, t - TT, len, x);
+    const float bias = a.bias ? a.bias[d] : 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      float p = bias;
+#pragma unroll
+      for (int j = 0; j < TT; ++j) p = fmaf(w[j], x[TT + e - j], p);
+      y[e] = t + e < len ? (a.silu ? p * sigmoid_f(p) : p) : 0.f;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = 0.f;
+  }
+  st8n<IOT>(a.y, r * a.L + t, y, (int)min(a.L - t, (int64_t)8));
+}
+
+// One token for each of B sequences: a thread to a channel.
+template <int IOT, int TT>
+__global__ __launch_bounds__(256) void k_conv_step(ConvArgs a) {
+  const int64_t r = blockIdx.x * (int64_t)256 + threadIdx.x;
+  if (r >= (int64_t)a.B * a.D) return;
+  const int d = (int)(r % a.D), S = a.T - 1;
+  float w[TT], x[TT];
+  conv_taps<TT>(a, d, w);
+  x[0] = ld1<IOT>(a.x, r);
+#pragma unroll
+  for (int j = 1; j < TT; ++j) x[j] = j <= S ? ld1<IOT>(a.state_out, r * S + S - j) : 0.f;
+  float p = a.bias ? a.bias[d] : 0.f;
+#pragma unroll
+  for (int j = 0; j < TT; ++j) p = fmaf(w[j], x[j], p);
+  st1<IOT>(a.y, r, a.silu ? p * sigmoid_f(p) : p);
+#pragma unroll
+  for (int j = 0; j < TT - 1; ++j)
+    if (j < S) st1<IOT>(a.state_out, r * S + S - 1 - j, x[j]);
+}
+
+// Backward.  With gp = gy act'(p),
+//   gx[t] = sum_j w[j] gp[t+j],  gw[j] = sum_t gp[t] x[t-j],  gbias = sum_t gp[t],
+// and the carried inputs' gradients are gx at negative t; a gradient of the
+// state that the call left behind adds to the last T-1 inputs'.  p is
+// computed again, for a lane's 8 steps and the TT-1 behind them.  Sums over
+// time: a workgroup covers kConvSpan steps of a row and leaves one partial
+// for each tap, which k_conv_sum adds up in a fixed order.
+template <int IOT, int TT>
+__device__ __forceinline__ void conv_gp(const ConvArgs& a, int64_t r, int t, int len, const float (&w)[TT], float bias,
+                                        float (&x)[2 * TT + 8], float (&gp)[TT + 8]) {
+  // x: inputs t - TT .. t + TT + 8
+  conv_window<IOT, 2 * TT + 8>(a, r, t - TT, len, x);
+#pragma unroll
+  for (int e = 0; e < TT + 8; ++e) gp[e] = 0.f;
+  if (t >= 0 && t + TT + 8 <= len) {
+#pragma unroll
+    for (int e = 0; e < TT + 8; e += 8) {
+      if (e + 8 <= TT + 8) {
+        float v[8];
+        widen8<IOT>(ld8<IOT>(a.gy, r * a.L + t + e), v);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) gp[e + k] = v[k];
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) gp[e + k] = ld1<IOT>(a.gy, r * a.L + t + e + k);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < TT + 8; ++e)
+      if (t + e >= 0 && t + e < len) gp[e] = ld1<IOT>(a.gy, r * a.L + t + e);
+  }
+  if (a.silu) {
+#pragma unroll
+    for (int e = 0; e < TT + 7; ++e) {
+      float p = bias;
+#pragma unroll
+      for (int j = 0; j < TT; ++j) p = fmaf(w[j], x[TT + e - j], p);
+      const float s = sigmoid_f(p);
+      gp[e] = t + e >= 0 && t + e < len ? gp[e] * (s * fmaf(p, 1.f - s, 1.f)) : 0.f;
+    }
+  }
+}
+
+template <int IOT, int TT>
+__global__ __launch_bounds__(256) void k_conv_bwd(ConvArgs a, int per, int lper, int blocks) {
+  __shared__ float part[4][TT + 1];
+  const int tid = threadIdx.x;
+  const int64_t rb = blockIdx.x / blocks;
+  const int xb = (int)(blockIdx.x - rb * blocks);
+  const int64_t rows = (int64_t)a.B * a.D, r = rb * (256 >> lper) + (tid >> lper);
+  const bool live = r < rows;
+  const int64_t rr = live ? r : rows - 1;
+  const int64_t b = rr / a.D;
+  const int d = (int)(rr - b * a.D), len = live ? conv_length(a, b) : 0, S = a.T - 1;
+  float w[TT], sum[TT + 1];
+  conv_taps<TT>(a, d, w);
+  const float bias = a.bias ? a.bias[d] : 0.f;
+#pragma unroll
+  for (int j = 0; j <= TT; ++j) sum[j] = 0.f;
+  const int64_t t_end = min(a.L, (xb + 1) * kConvSpan);
+  for (int64_t t = xb * kConvSpan + 8 * (tid & (per - 1)); t < t_end && live; t += 8 * per) {
+    float gx[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (t < len) {
+      float x[2 * TT + 8], gp[TT + 8];
+      conv_gp<IOT, TT>(a, r, (int)t, len, w, bias, x, gp);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+#pragma unroll
+        for (int j = 0; j < TT; ++j) gx[e] = fmaf(w[j], gp[e + j], gx[e]);
+        sum[TT] += gp[e];
+#pragma unroll
+        for (int j = 0; j < TT; ++j) sum[j] = fmaf(gp[e], x[TT + e - j], sum[j]);
+      }
+      if (a.gstate_out) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int64_t i = t + e - (len - S);
+          if (i >= 0 && i < S) gx[e] += ld1<IOT>(a.gstate_out, r * S + i);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) gx[e] = t + e < len ? gx[e] : 0.f;
+    }
+    st8n<IOT>(a.gx, r * a.L + t, gx, (int)min(a.L - t, (int64_t)8));
+  }
+  // the carried inputs: one thread to a row walks over its T-1 values
+  if (a.gstate && live && xb == 0 && (tid & (per - 1)) == 0) {
+    for (int i = 0; i < S; ++i) {
+      const int t = i - S;                                // gx[t] = sum_j w[j] gp[t+j], t + j in [0, len)
+      float v = 0.f;
+      for (int j = -t; j <= S && t + j < len; ++j) {
+        const int s = t + j;
+        float gp = ld1<IOT>(a.gy, r * a.L + s);
+        if (a.silu) {
+          float p = bias;
+          for (int k = 0; k <= S; ++k) p = fmaf(a.w[(int64_t)d * a.T + k], conv_at<IOT>(a, r, s - k), p);
+          const float sg = sigmoid_f(p);
+          gp *= sg * fmaf(p, 1.f - sg, 1.f);
+        }
+        v = fmaf(a.w[(int64_t)d * a.T + j], gp, v);
+      }
+      // the state left behind still holds this carried input when len < T-1
+      if (a.gstate_out && i >= len) v += ld1<IOT>(a.gstate_out, r * S + i - len);
+      st1<IOT>(a.gstate, r * S + i, v);
+    }
+  }
+  // the row's sums over its threads: within a wave, then over the waves
+#pragma unroll
+  for (int j = 0; j <= TT; ++j) {
+    for (int o = min(per, 64) >> 1; o > 0; o >>= 1) sum[j] += __shfl_xor(sum[j], o);
+  }
+  if (per > 64) {
+    if ((tid & 63) == 0) {
+#pragma unroll
+      for (int j = 0; j <= TT; ++j) part[tid >> 6][j] = sum[j];
+    }
+    __syncthreads();
+    if ((tid & (per - 1)) == 0) {
+#pragma unroll
+      for (int j = 0; j <= TT; ++j)
+        for (int k = 1; k < per / 64; ++k) sum[j] += part[(tid >> 6) + k][j];
+    }
+  }
+  if (live && (tid & (per - 1)) == 0) {
+    float* o = a.partial + ((b * blocks + xb) * a.D + d) * (a.T + 1);
+#pragma unroll
+    for (int j = 0; j < TT; ++j)
+      if (j < a.T) o[j] = sum[j];
+    o[a.T] = sum[TT];
+  }
+}
+
+__global__ __launch_bounds__(256) void k_conv_sum(ConvArgs a, int64_t parts) {
+  __shared__ float s[8][33];
+  const int c = threadIdx.x & 31, k = threadIdx.x >> 5;
+  const int64_t W = (int64_t)a.D * (a.T + 1), i = blockIdx.x * (int64_t)32 + c;
+  float v = 0.f;
+  if (i < W)
+    for (int64_t p = k; p < parts; p += 8) v += a.partial[p * W + i];
+  s[k][c] = v;
+  __syncthreads();
+  if (k == 0 && i < W) {
+#pragma unroll
+    for (int j = 1; j < 8; ++j) v += s[j][c];
+    const int64_t d = i / (a.T + 1);
+    const int j = (int)(i - d * (a.T + 1));
+    if (j < a.T) a.gw[d * a.T + j] = v;
+    else if (a.gbias) a.gbias[d] = v;
+  }
+}
+
+template <int TT>
+void conv_forward_tt(const ConvArgs& a, const ConvGrid& g, hipStream_t s) {
+  if (a.io) k_conv<1, TT><<<(unsigned)g.groups, 256, 0, s>>>(a, g.per, g.lper, (int)g.blocks);
+  else k_conv<0, TT><<<(unsigned)g.groups, 256, 0, s>>>(a, g.per, g.lper, (int)g.blocks);
+}
+
+template <int TT>
+void conv_step_tt(const ConvArgs& a, hipStream_t s) {
+  const unsigned n = (unsigned)(((int64_t)a.B * a.D + 255) / 256);
+  if (a.io) k_conv_step<1, TT><<<n, 256, 0, s>>>(a);
+  else k_conv_step<0, TT><<<n, 256, 0, s>>>(a);
+}
+
+template <int TT>
+void conv_backward_tt(const ConvArgs& a, const ConvGrid& g, hipStream_t s) {
+  if (a.io) k_conv_bwd<1, TT><<<(unsigned)g.groups, 256, 0, s>>>(a, g.per, g.lper, (int)g.blocks);
+  else k_conv_bwd<0, TT><<<(unsigned)g.groups, 256, 0, s>>>(a, g.per, g.lper, (int)g.blocks);
+}
+
+}  // namespace
+
+hipError_t short_conv(const ConvArgs& a, hipStream_t s) {
+  const ConvGrid g = conv_grid(a.B, a.D, a.L, kConvStep);
+  if (a.T <= 4) conv_forward_tt<4>(a, g, s);
+  else if (a.T <= 8) conv_forward_tt<8>(a, g, s);
+  else conv_forward_tt<16>(a, g, s);
+  return hipGetLastError();
+}
+
+hipError_t short_conv_step(const ConvArgs& a, hipStream_t s) {
+  if (a.T <= 4) conv_step_tt<4>(a, s);
+  else if (a.T <= 8) conv_step_tt<8>(a, s);
+  else conv_step_tt<16>(a, s);
+  return hipGetLastError();
+}
+
+hipError_t short_conv_backward(const ConvArgs& a, hipStream_t s) {
+  const ConvGrid g = conv_grid(a.B, a.D, a.L, kConvSpan);
+  if (a.T <= 4) conv_backward_tt<4>(a, g, s);
+  else if (a.T <= 8) conv_backward_tt<8>(a, g, s);
+  else conv_backward_tt<16>(a, g, s);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int64_t W = (int64_t)a.D * (a.T + 1);
+  k_conv_sum<<<(unsigned)((W + 31) / 32), 256, 0, s>>>(a, conv_backward_parts(a.B, a.L));
+  return hipGetLastError();
+}
+
+}  // namespace hyena

@@ -1,0 +1,694 @@
+// kernels_scan.hip -- the selective state-space scan, forward, for single
+// tokens, and backward.
+//
+//   dt = softplus(delta + delta_bias),  a[t][n] = exp(dt[t] A[n]),
+//   h[t][n] = a[t][n] h[t-1][n] + dt[t] u[t] B[t][n],
+//   y[t] = (sum_n C[t][n] h[t][n] + skip u[t]) * silu(z[t])
+//
+// per channel d of each sequence; B and C are shared by the channels of a
+// group.  Steps behind a sequence's length count as dt = u = B = C = 0: the
+// state stays as it is, and the values stored there may be anything.
+//
+// The recurrence is a scan of the maps h -> a h + b, whose composition is
+// (a2 a1, a2 b1 + b2).  16 lanes (one DPP row) hold 128 steps of one channel,
+// 8 consecutive ones each: a lane composes its 8 steps, the row scans the 16
+// results in 4 steps of 2 instructions, and the lane runs its 8 steps again
+// from the right start.  A wave holds 4 channels, a workgroup 16, which share
+// B and C in LDS as fp32.
+#include <hip/hip_runtime.h>
+
+#include "ssm.hpp"
+#include "ssm_device.hpp"
+
+namespace hyena {
+namespace {
+
+constexpr int CH = kScanChunk, TILE = kScanTile, SCAN_THREADS = 256;
+
+// Inclusive scan of the maps (P, H) over a row, lane 0 first.
+__device__ __forceinline__ void row_scan(float P, float& H) {
+  H = fmaf(P, row_shr<1>(0.f, H), H);
+  P *= row_shr<1>(1.f, P);
+  H = fmaf(P, row_shr<2>(0.f, H), H);
+  P *= row_shr<2>(1.f, P);
+  H = fmaf(P, row_shr<4>(0.f, H), H);
+  P *= row_shr<4>(1.f, P);
+  H = fmaf(P, row_shr<8>(0.f, H), H);
+}
+
+// The same, lane 15 first.
+__device__ __forceinline__ void row_scan_back(float P, float& H) {
+  H = fmaf(P, row_shl<1>(0.f, H), H);
+  P *= row_shl<1>(1.f, P);
+  H = fmaf(P, row_shl<2>(0.f, H), H);
+  P *= row_shl<2>(1.f, P);
+  H = fmaf(P, row_shl<4>(0.f, H), H);
+  P *= row_shl<4>(1.f, P);
+  H = fmaf(P, row_shl<8>(0.f, H), H);
+}
+
+// LDS place of step t's value among a state's 128: lanes read their 8 steps
+// as two 16-byte words, the first halves of all lanes side by side, so that
+// neither read has bank conflicts.
+__device__ __forceinline__ void stage8(float* s, int l, const float (&v)[8]) {
+  *reinterpret_cast<f32x4v*>(s + 4 * l) = f32x4v{v[0], v[1], v[2], v[3]};
+  *reinterpret_cast<f32x4v*>(s + 64 + 4 * l) = f32x4v{v[4], v[5], v[6], v[7]};
+}
+__device__ __forceinline__ void fetch8(const float* s, int l, float (&v)[8]) {
+  const f32x4v x = *reinterpret_cast<const f32x4v*>(s + 4 * l);
+  const f32x4v y = *reinterpret_cast<const f32x4v*>(s + 64 + 4 * l);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) { v[e] = x[e]; v[e + 4] = y[e]; }
+}
+
+__device__ __forceinline__ int seq_length(const ScanArgs& a, int b) {
+  if (!a.lengths) return (int)a.L;
+  const int n = a.lengths[b];
+  return n < 0 ? 0 : (n > a.L ? (int)a.L : n);
+}
+
+// dt and u of a lane's 8 steps (zeros behind the length).
+template <int IOT>
+__device__ __forceinline__ void steps8(const ScanArgs& a, const Raw8<IOT>& ru, const Raw8<IOT>& rd, float bias, int n,
+                                       float (&u)[8], float (&dt)[8]) {
+  widen8<IOT>(ru, u);
+  widen8<IOT>(rd, dt);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float x = dt[i] + bias;
+    dt[i] = i < n ? (a.softplus ? softplus_f(x) : x) : 0.f;
+  }
+}
+
+// ---------------------------------------------------------------- forward
+//
+// One workgroup: 16 channels of a group over one time segment, chunk after
+// chunk.  END: only the state at the segment's end from a zero start, and the
+// sum of dt, for the segments behind it (all but the last run this first
+// when the time axis is split); a segment's decay is exp(A sum dt), so the
+// start of segment s is a short recurrence over the ones before it, which
+// each workgroup does for its own channels.
+template <int IOT, int NV, bool END>
+__global__ __launch_bounds__(SCAN_THREADS) void k_scan(ScanArgs a) {
+  extern __shared__ float lds[];
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, row = lane >> 4, l = lane & 15;
+  const int N = a.N, Dg = a.D / a.G, tiles = (Dg + TILE - 1) / TILE;
+  const int nseg = END ? a.segs - 1 : a.segs;
+  int id = blockIdx.x;
+  const int tile = id % tiles; id /= tiles;
+  const int g = id % a.G; id /= a.G;
+  const int seg = id % nseg;
+  const int b = id / nseg;
+  const int cw = wave * 4 + row, dg = tile * TILE + cw;
+  const bool live = dg < Dg;
+  const int d = g * Dg + (live ? dg : Dg - 1);
+  const int64_t L = a.L;
+  const int len = seq_length(a, b);
+  const int64_t base = ((int64_t)b * a.D + d) * L;
+  const int64_t bc = ((int64_t)b * a.G + g) * N * L;
+  const int t_begin = (int)(seg * a.seg);
+  const int t_end = (int)min(L, (int64_t)t_begin + a.seg);
+
+  float* sB = lds;                                   // [N][128]
+  float* sC = END ? lds : lds + N * CH;              // [N][128]
+  float2* sS = reinterpret_cast<float2*>((END ? lds : sC) + N * CH);   // [16][N]: A log2(e), the state at the chunk's start
+
+  for (int i = tid; i < TILE * N; i += SCAN_THREADS) {
+    const int c = i / N, n = i - c * N, dc = tile * TILE + c;
+    float A2 = 0.f, h = 0.f;
+    if (dc < Dg) {
+      const int ch = g * Dg + dc;
+      A2 = a.A[(int64_t)ch * N + n] * kLog2e;
+      if constexpr (!END) {
+        if (a.state) h = a.state[((int64_t)b * a.D + ch) * N + n];
+        for (int s = 0; s < seg; ++s) {
+          const int64_t r = ((int64_t)b * a.segs + s) * a.D + ch;
+          h = fmaf(exp2_fast(A2 * a.sdt[r]), h, a.hend[r * N + n]);
+        }
+      }
+    }
+    sS[i] = make_float2(A2, h);
+  }
+  const float bias = a.dbias ? a.dbias[d] : 0.f;
+  const float skip = !END && a.skip ? a.skip[d] : 0.f;
+  float dt_total = 0.f;
+
+  // B and C of a chunk: 16 words of 8 steps for each state, NV for a thread
+  constexpr int NW = END ? (NV + 1) / 2 : NV;
+  const int words = (END ? N : 2 * N) * 16;
+  Raw8<IOT> rbc[NW], ru, rd, rz;
+  auto load = [&](int t0) {
+#pragma unroll
+    for (int k = 0; k < NW; ++k) {
+      const int i = tid + SCAN_THREADS * k, v = i & 15, n = i >> 4;
+      rbc[k] = zero8<IOT>();
+      if (i < words) {
+        const bool isC = n >= N;
+        rbc[k] = ld8n<IOT>(isC ? a.Cm : a.Bm, bc + (int64_t)(isC ? n - N : n) * L + t0 + 8 * v, len - t0 - 8 * v);
+      }
+    }
+    const int t = t0 + 8 * l, m = live ? len - t : 0;
+    ru = ld8n<IOT>(a.u, base + t, m);
+    rd = ld8n<IOT>(a.delta, base + t, m);
+    if constexpr (!END)
+      if (a.z) rz = ld8n<IOT>(a.z, base + t, m);
+  };
+  if (t_begin < len) load(t_begin);
+
+  for (int t0 = t_begin; t0 < t_end; t0 += CH) {
+    const int t = t0 + 8 * l, m = len - t;
+    if (t0 >= len) {                                  // behind the sequence: zeros
+      if constexpr (!END) {
+        float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (live && t < L) st8n<IOT>(a.y, base + t, y, (int)min(L - t, (int64_t)8));
+      }
+      continue;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < NW; ++k) {
+      const int i = tid + SCAN_THREADS * k;
+      if (i < words) {
+        float v[8];
+        widen8<IOT>(rbc[k], v);
+        stage8(lds + (i >> 4) * CH, i & 15, v);
+      }
+    }
+    float u[8], dt[8], z[8], y[8];
+    steps8<IOT>(a, ru, rd, bias, live ? m : 0, u, dt);
+    if constexpr (!END)
+      if (a.z) widen8<IOT>(rz, z);
+    __syncthreads();
+    if (t0 + CH < t_end && t0 + CH < len) load(t0 + CH);   // in flight over this chunk's scan
+
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      y[i] = skip * u[i];
+      u[i] *= dt[i];
+      sum += dt[i];
+    }
+    dt_total += sum;
+    for (int n = 0; n < N; ++n) {
+      const float2 sc = sS[cw * N + n];
+      const float A2 = sc.x, h0 = sc.y;
+      float x[8], al[8];
+      fetch8(sB + n * CH, l, x);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        al[i] = exp2_fast(dt[i] * A2);
+        x[i] *= u[i];
+      }
+      float H = x[0];
+#pragma unroll
+      for (int i = 1; i < 8; ++i) H = fmaf(al[i], H, x[i]);
+      const float P = exp2_fast(A2 * sum);
+      H = fmaf(P, l == 0 ? h0 : 0.f, H);
+      row_scan(P, H);
+      const float r = row_ror<1>(H);                  // lane 0: the state at the chunk's end
+      if (l == 0) sS[cw * N + n].y = r;
+      if constexpr (!END) {
+        float c[8];
+        fetch8(sC + n * CH, l, c);
+        float h = l == 0 ? h0 : r;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          h = fmaf(al[i], h, x[i]);
+          y[i] = fmaf(h, c[i], y[i]);
+        }
+      }
+    }
+    if constexpr (!END) {
+      if (a.z) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] *= z[i] * sigmoid_f(z[i]);
+      }
+      if (m < 8) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = i < m ? y[i] : 0.f;
+      }
+      if (live && t < L) st8n<IOT>(a.y, base + t, y, (int)min(L - t, (int64_t)8));
+    }
+  }
+
+  if constexpr (END) {
+    dt_total = row_sum(dt_total);
+    if (live && l == 0) a.sdt[((int64_t)b * a.segs + seg) * a.D + d] = dt_total;
+  } else if (!a.state_out || seg != a.segs - 1) {
+    return;
+  }
+  __syncthreads();
+  for (int i = tid; i < TILE * N; i += SCAN_THREADS) {
+    const int c = i / N, n = i - c * N, dc = tile * TILE + c;
+    if (dc >= Dg) continue;
+    const int ch = g * Dg + dc;
+    if constexpr (END) a.hend[(((int64_t)b * a.segs + seg) * a.D + ch) * N + n] = sS[i].y;
+    else a.state_out[((int64_t)b * a.D + ch) * N + n] = sS[i].y;
+  }
+}
+
+template <int IOT, int NV>
+hipError_t launch_scan(const ScanArgs& a, hipStream_t s) {
+  const int64_t tiles = (a.D / a.G + TILE - 1) / TILE, wgs = tiles * a.G * a.B;
+  const size_t state = (size_t)TILE * a.N * 8, bc = (size_t)a.N * CH * 4;
+  if (a.segs > 1) {
+    k_scan<IOT, NV, true><<<dim3((unsigned)(wgs * (a.segs - 1))), SCAN_THREADS, bc + state, s>>>(a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  k_scan<IOT, NV, false><<<dim3((unsigned)(wgs * a.segs)), SCAN_THREADS, 2 * bc + state, s>>>(a);
+  return hipGetLastError();
+}
+
+// ------------------------------------------------------------ single tokens
+//
+// 4 states to a lane, W lanes (a power of two, W * 4 >= N) to a channel of a
+// sequence; the state's read and write are the call's traffic.
+template <int IOT>
+__global__ __launch_bounds__(256) void k_scan_step(ScanArgs a, int W, int lw, float* __restrict__ state) {
+  const int64_t idx = blockIdx.x * (int64_t)256 + threadIdx.x, r = idx >> lw;
+  const int l = (int)(idx & (W - 1)), N = a.N, n0 = 4 * l;
+  const bool live = r < (int64_t)a.B * a.D;
+  float part = 0.f, u = 0.f, z = 0.f, skip = 0.f;
+  if (live) {
+    const int64_t b = r / a.D;
+    const int d = (int)(r - b * a.D), g = d / (a.D / a.G);
+    u = ld1<IOT>(a.u, r);
+    float dt = ld1<IOT>(a.delta, r) + (a.dbias ? a.dbias[d] : 0.f);
+    if (a.z) z = ld1<IOT>(a.z, r);
+    if (a.skip) skip = a.skip[d];
+    const float* A = a.A + (int64_t)d * N + n0;
+    float* h = state + r * N + n0;
+    const int64_t bc = (b * a.G + g) * N + n0;
+    float Av[4], hv[4], Bv[4], Cv[4];
+    if ((N & 3) == 0) {
+      if (n0 < N) {
+        const f32x4v x = *reinterpret_cast<const f32x4v*>(A), y = *reinterpret_cast<const f32x4v*>(h);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) { Av[e] = x[e]; hv[e] = y[e]; }
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (n0 + e < N) { Av[e] = A[e]; hv[e] = h[e]; }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const bool in = n0 + e < N;
+      Bv[e] = in ? ld1<IOT>(a.Bm, bc + e) : 0.f;
+      Cv[e] = in ? ld1<IOT>(a.Cm, bc + e) : 0.f;
+    }
+    if (a.softplus) dt = softplus_f(dt);
+    const float du = dt * u;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (n0 + e < N) {
+        hv[e] = fmaf(exp2_fast(dt * (Av[e] * kLog2e)), hv[e], du * Bv[e]);
+        part = fmaf(hv[e], Cv[e], part);
+      }
+    if ((N & 3) == 0) {
+      if (n0 < N) *reinterpret_cast<f32x4v*>(h) = f32x4v{hv[0], hv[1], hv[2], hv[3]};
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (n0 + e < N) h[e] = hv[e];
+    }
+  }
+  for (int o = W >> 1; o > 0; o >>= 1) part += __shfl_xor(part, o);
+  if (live && l == 0) {
+    float y = fmaf(skip, u, part);
+    if (a.z) y *= z * sigmoid_f(z);
+    st1<IOT>(a.y, r, y);
+  }
+}
+
+// --------------------------------------------------------------- backward
+//
+// With g[t] the gradient of h[t], q[t] = a[t] g[t] what it hands to h[t-1],
+// gy' = gy silu(z) and g[t] = C[t] gy'[t] + q[t+1]:
+//   gB[t] = sum_d g dt u,  gC[t] = sum_d h gy',  gA = sum_t q[t] h[t-1] dt[t],
+//   gu = dt sum_n g B + skip gy',
+//   gdt = u sum_n g B + sum_n q[t] h[t-1] A,  gdelta = gdt sigmoid(delta + bias),
+//   gz = gy (sum_n C h + skip u) silu'(z).
+// Three passes.  The first leaves each chunk's end state from a zero start
+// and the carry q at its start from a zero end (and the sum of dt); the
+// second joins them along time, both ways, into the state at each chunk's
+// start and the carry at its end; the third then does all chunks at once.
+// Its workgroup stays at one chunk and walks over channels, so that B and C
+// are staged once and the sums over channels stay on the chip.
+
+// Chunk sums: H, Q [N] and sum dt of 4 channels to a wave.
+template <int IOT>
+__global__ __launch_bounds__(SCAN_THREADS) void k_scan_bwd_ends(ScanArgs a) {
+  extern __shared__ float lds[];
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, row = lane >> 4, l = lane & 15;
+  const int N = a.N, Dg = a.D / a.G, tiles = (Dg + TILE - 1) / TILE, per = (tiles + a.splits - 1) / a.splits;
+  int id = blockIdx.x;
+  const int split = id % a.splits; id /= a.splits;
+  const int c = id % a.chunks; id /= a.chunks;
+  const int g = id % a.G, b = id / a.G;
+  const int64_t L = a.L;
+  const int len = seq_length(a, b), t0 = c * CH, t = t0 + 8 * l, m = len - t;
+  const int64_t bc = ((int64_t)b * a.G + g) * N * L;
+  float* sB = lds;
+  float* sC = lds + N * CH;
+  for (int i = tid; i < 2 * N * 16; i += SCAN_THREADS) {
+    const int v = i & 15, n = i >> 4;
+    const bool isC = n >= N;
+    float x[8];
+    widen8<IOT>(ld8n<IOT>(isC ? a.Cm : a.Bm, bc + (int64_t)(isC ? n - N : n) * L + t0 + 8 * v, len - t0 - 8 * v), x);
+    stage8(lds + n * CH, v, x);
+  }
+  __syncthreads();
+  const int tile_end = min(tiles, (split + 1) * per);
+  for (int tile = split * per; tile < tile_end; ++tile) {
+    const int dg = tile * TILE + wave * 4 + row;
+    const bool live = dg < Dg;
+    const int d = g * Dg + (live ? dg : Dg - 1), mm = live ? m : 0;
+    const int64_t at = ((int64_t)b * a.D + d) * L + t;
+    float u[8], dt[8], gy[8];
+    const Raw8<IOT> rg = ld8n<IOT>(a.gy, at, mm);
+    Raw8<IOT> rz;
+    if (a.z) rz = ld8n<IOT>(a.z, at, mm);
+    steps8<IOT>(a, ld8n<IOT>(a.u, at, mm), ld8n<IOT>(a.delta, at, mm), a.dbias ? a.dbias[d] : 0.f, mm, u, dt);
+    widen8<IOT>(rg, gy);
+    if (a.z) {
+      float z[8];
+      widen8<IOT>(rz, z);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) gy[i] *= z[i] * sigmoid_f(z[i]);
+    }
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      u[i] *= dt[i];
+      sum += dt[i];
+    }
+    const int64_t r = ((int64_t)b * a.chunks + c) * a.D + d;
+    const float* A = a.A + (int64_t)d * N;
+    for (int n = 0; n < N; ++n) {
+      const float A2 = A[n] * kLog2e;
+      float x[8], al[8], cc[8];
+      fetch8(sB + n * CH, l, x);
+      fetch8(sC + n * CH, l, cc);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        al[i] = exp2_fast(dt[i] * A2);
+        x[i] *= u[i];
+      }
+      float H = x[0], Q = al[7] * (cc[7] * gy[7]);
+#pragma unroll
+      for (int i = 1; i < 8; ++i) {
+        H = fmaf(al[i], H, x[i]);
+        Q = al[7 - i] * fmaf(cc[7 - i], gy[7 - i], Q);
+      }
+      const float P = exp2_fast(A2 * sum);
+      row_scan(P, H);
+      row_scan_back(P, Q);
+      if (live && l == 15) a.hc[r * N + n] = H;
+      if (live && l == 0) a.qc[r * N + n] = Q;
+    }
+    sum = row_sum(sum);
+    if (live && l == 0) a.dts[r] = sum;
+  }
+}
+
+// Joins the chunks along time: hc becomes the state at each chunk's start,
+// qc the carry that comes in behind its end.  One thread to a state.
+__global__ __launch_bounds__(256) void k_scan_bwd_join(ScanArgs a) {
+  const int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x, DN = (int64_t)a.D * a.N;
+  if (i >= a.B * DN) return;
+  const int64_t b = i / DN, dn = i - b * DN;
+  const int d = (int)(dn / a.N);
+  const float A2 = a.A[dn] * kLog2e;
+  float* hc = a.hc + b * a.chunks * DN + dn;
+  float* qc = a.qc + b * a.chunks * DN + dn;
+  const float* dts = a.dts + b * a.chunks * (int64_t)a.D + d;
+  float h = a.state ? a.state[i] : 0.f;
+#pragma unroll 4
+  for (int c = 0; c < a.chunks; ++c) {
+    const float e = hc[c * DN];
+    hc[c * DN] = h;
+    h = fmaf(exp2_fast(A2 * dts[(int64_t)c * a.D]), h, e);
+  }
+  float q = a.gstate_out ? a.gstate_out[i] : 0.f;
+#pragma unroll 4
+  for (int c = a.chunks - 1; c >= 0; --c) {
+    const float e = qc[c * DN];
+    qc[c * DN] = q;
+    q = fmaf(exp2_fast(A2 * dts[(int64_t)c * a.D]), q, e);
+  }
+  if (a.gstate) a.gstate[i] = q;
+}
+
+// x + its partner across the wave's halves, for two values at once: the lower
+// half holds x's sums, the upper half y's.
+__device__ __forceinline__ float fold_halves(float x, float y) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(y), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+// The same across neighbouring rows: even rows hold x's sums, odd rows y's.
+__device__ __forceinline__ float fold_rows(float x, float y) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(y), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+template <int IOT>
+__global__ __launch_bounds__(SCAN_THREADS) void k_scan_bwd(ScanArgs a) {
+  extern __shared__ float lds[];
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, row = lane >> 4, l = lane & 15;
+  const int N = a.N, Dg = a.D / a.G, tiles = (Dg + TILE - 1) / TILE, per = (tiles + a.splits - 1) / a.splits;
+  int id = blockIdx.x;
+  const int split = id % a.splits; id /= a.splits;
+  const int c = id % a.chunks; id /= a.chunks;
+  const int g = id % a.G, b = id / a.G;
+  const int64_t L = a.L;
+  const int len = seq_length(a, b), t0 = c * CH, t = t0 + 8 * l, m = len - t;
+  const int room = (int)min(L - t, (int64_t)8);      // this lane's steps in the array (<= 0: none)
+  const int64_t bc = ((int64_t)b * a.G + g) * N * L;
+  float* sB = lds;                                             // [N][128]
+  float* sC = sB + N * CH;                                     // [N][128]
+  f32x4v* sG = reinterpret_cast<f32x4v*>(sC + N * CH);         // [N][64 lanes]: sums over channels
+  f32x4v* sS = sG + N * 64;                                    // [16][N]: A log2(e), start state, end carry, gA's part
+  for (int i = tid; i < 2 * N * 16; i += SCAN_THREADS) {
+    const int v = i & 15, n = i >> 4;
+    const bool isC = n >= N;
+    float x[8];
+    widen8<IOT>(ld8n<IOT>(isC ? a.Cm : a.Bm, bc + (int64_t)(isC ? n - N : n) * L + t0 + 8 * v, len - t0 - 8 * v), x);
+    stage8(lds + n * CH, v, x);
+  }
+  for (int i = tid; i < N * 64; i += SCAN_THREADS) sG[i] = f32x4v{0.f, 0.f, 0.f, 0.f};
+
+  const int quarter = (N + 3) / 4;
+  const int tile_end = min(tiles, (split + 1) * per);
+  for (int tile = split * per; tile < tile_end; ++tile) {
+    const int cw = wave * 4 + row, dg = tile * TILE + cw;
+    const bool live = dg < Dg;
+    const int d = g * Dg + (live ? dg : Dg - 1), mm = live ? m : 0;
+    const int64_t at = ((int64_t)b * a.D + d) * L + t, r = ((int64_t)b * a.chunks + c) * a.D + d;
+    const Raw8<IOT> ru = ld8n<IOT>(a.u, at, mm), rd = ld8n<IOT>(a.delta, at, mm), rg = ld8n<IOT>(a.gy, at, mm);
+    Raw8<IOT> rz = zero8<IOT>();
+    if (a.z) rz = ld8n<IOT>(a.z, at, mm);
+    // this wave's channels only: no other wave reads or writes these words
+    for (int n = l; n < N; n += 16) {
+      const float A = a.A[(int64_t)d * N + n];
+      sS[cw * N + n] = f32x4v{A, live ? a.hc[r * N + n] : 0.f, live ? a.qc[r * N + n] : 0.f, 0.f};
+    }
+    const float bias = a.dbias ? a.dbias[d] : 0.f, skip = a.skip ? a.skip[d] : 0.f;
+    float u[8], dt[8], du[8], gy[8], y[8], s1[8], s2[8];
+    steps8<IOT>(a, ru, rd, bias, mm, u, dt);
+    widen8<IOT>(rg, gy);
+    if (a.z) {
+      float z[8];
+      widen8<IOT>(rz, z);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) gy[i] *= z[i] * sigmoid_f(z[i]);
+    }
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      y[i] = skip * u[i];
+      du[i] = u[i] * dt[i];
+      sum += dt[i];
+      s1[i] = s2[i] = 0.f;
+    }
+    __syncthreads();
+    // the four waves take the states in turn, so that each sum over channels
+    // has one writer at a time and one order
+    for (int turn = 0; turn < 4; ++turn) {
+      const int first = ((turn + wave) & 3) * quarter, last = min(N, first + quarter);
+      for (int n = first; n < last; ++n) {
+        const f32x4v sc = sS[cw * N + n];
+        const float A = sc[0], A2 = A * kLog2e;
+        float x[8], al[8], cc[8], h[8];
+        fetch8(sB + n * CH, l, x);
+        fetch8(sC + n * CH, l, cc);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) al[i] = exp2_fast(dt[i] * A2);
+        float H = du[0] * x[0], Q = al[7] * (cc[7] * gy[7]);
+#pragma unroll
+        for (int i = 1; i < 8; ++i) {
+          H = fmaf(al[i], H, du[i] * x[i]);
+          Q = al[7 - i] * fmaf(cc[7 - i], gy[7 - i], Q);
+        }
+        const float P = exp2_fast(A2 * sum);
+        H = fmaf(P, l == 0 ? sc[1] : 0.f, H);
+        Q = fmaf(P, l == 15 ? sc[2] : 0.f, Q);
+        row_scan(P, H);
+        row_scan_back(P, Q);
+        const float hb = row_shr<1>(sc[1], H);        // the state before this lane's steps
+        float q = row_shl<1>(sc[2], Q);               // the carry from behind them
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          h[i] = fmaf(al[i], i ? h[i - 1] : hb, du[i] * x[i]);
+          y[i] = fmaf(h[i], cc[i], y[i]);
+        }
+        float gA = 0.f;
+#pragma unroll
+        for (int i = 7; i >= 0; --i) {
+          const float gh = fmaf(cc[i], gy[i], q);
+          q = al[i] * gh;
+          s1[i] = fmaf(gh, x[i], s1[i]);
+          const float w = q * (i ? h[i - 1] : hb);
+          s2[i] = fmaf(w, A, s2[i]);
+          gA = fmaf(w, dt[i], gA);
+          cc[i] = fold_halves(gh * du[i], h[i] * gy[i]);
+        }
+        f32x4v acc = sG[n * 64 + lane];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[k] += fold_rows(cc[2 * k], cc[2 * k + 1]);
+        sG[n * 64 + lane] = acc;
+        gA = row_sum(gA);
+        if (l == 0) sS[cw * N + n][3] = gA;
+      }
+      __syncthreads();
+    }
+    // the chunk's parts of the sums over time, and the lane's own gradients
+    for (int n = l; n < N; n += 16)
+      if (live) a.hc[r * N + n] = sS[cw * N + n][3];
+    float gz[8], sk = 0.f, sb = 0.f;
+    if (a.z) {
+      float z[8], g0[8];
+      widen8<IOT>(rz, z);
+      widen8<IOT>(rg, g0);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float sg = sigmoid_f(z[i]);
+        gz[i] = g0[i] * y[i] * (sg * fmaf(z[i], 1.f - sg, 1.f));
+      }
+    }
+    float pre[8];
+    widen8<IOT>(rd, pre);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      sk = fmaf(gy[i], u[i], sk);
+      float gd = fmaf(s1[i], u[i], s2[i]);
+      if (a.softplus) gd *= sigmoid_f(pre[i] + bias);
+      gd = i < mm ? gd : 0.f;
+      s2[i] = gd;
+      sb += gd;
+      s1[i] = fmaf(s1[i], dt[i], skip * gy[i]);
+    }
+    sk = row_sum(sk);
+    sb = row_sum(sb);
+    if (live) {
+      if (l == 0) { a.ps[r] = sk; a.pb[r] = sb; }
+      if (room > 0) {
+        if (a.z) st8n<IOT>(a.gz, at, gz, room);
+        st8n<IOT>(a.gu, at, s1, room);
+        st8n<IOT>(a.gdelta, at, s2, room);
+      }
+    }
+  }
+  // sums over channels: lane (row r, column l) of a state holds, in word k,
+  // step 8 l + 2 k + (r & 1) of gB (r < 2) or gC
+  __syncthreads();
+  const float* sg = reinterpret_cast<const float*>(sG);
+  for (int i = tid; i < 2 * N * CH; i += SCAN_THREADS) {
+    const int tt = i & (CH - 1), n = (i >> 7) % N, isC = (i >> 7) / N;
+    if (t0 + tt >= L) continue;
+    const float v = sg[(n * 64 + (isC * 2 + (tt & 1)) * 16 + (tt >> 3)) * 4 + ((tt & 7) >> 1)];
+    const int64_t o = bc + (int64_t)n * L + t0 + tt;
+    if (a.splits > 1) a.gbc[((int64_t)(split * 2 + isC) * a.B * a.G) * N * L + o] = v;
+    else st1<IOT>(isC ? a.gC : a.gB, o, v);
+  }
+}
+
+// gB and gC from the splits' parts.
+template <int IOT>
+__global__ __launch_bounds__(256) void k_scan_bwd_sum_bc(ScanArgs a) {
+  const int64_t n = (int64_t)a.B * a.G * a.N * a.L;
+  for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < 2 * n; i += (int64_t)gridDim.x * 256) {
+    float v = 0.f;
+    for (int s = 0; s < a.splits; ++s) v += a.gbc[s * 2 * n + i];
+    if (i < n) st1<IOT>(a.gB, i, v);
+    else st1<IOT>(a.gC, i - n, v);
+  }
+}
+
+// gA, gskip and gdelta_bias from the chunks' parts: a workgroup sums 32
+// columns, 8 threads to a column.
+__global__ __launch_bounds__(256) void k_scan_bwd_sum_t(ScanArgs a) {
+  __shared__ float s[8][33];
+  const int c = threadIdx.x & 31, k = threadIdx.x >> 5;
+  const int64_t DN = (int64_t)a.D * a.N, rows = (int64_t)a.B * a.chunks;
+  const int64_t i = blockIdx.x * (int64_t)32 + c;    // columns: gA's D*N, then gskip's D, then gdelta_bias's D
+  const float* src = nullptr;
+  int64_t stride = 0;
+  float* dst = nullptr;
+  if (i < DN) { src = a.hc + i; stride = DN; dst = a.gA + i; }
+  else if (i < DN + a.D) { src = a.ps + (i - DN); stride = a.D; dst = a.gskip ? a.gskip + (i - DN) : nullptr; }
+  else if (i < DN + 2 * a.D) { src = a.pb + (i - DN - a.D); stride = a.D; dst = a.gdbias ? a.gdbias + (i - DN - a.D) : nullptr; }
+  float v = 0.f;
+  if (dst) {
+#pragma unroll 4
+    for (int64_t r = k; r < rows; r += 8) v += src[r * stride];
+  }
+  s[k][c] = v;
+  __syncthreads();
+  if (k == 0 && dst) {
+#pragma unroll
+    for (int j = 1; j < 8; ++j) v += s[j][c];
+    *dst = v;
+  }
+}
+
+template <int IOT>
+hipError_t launch_scan_backward(const ScanArgs& a, hipStream_t s) {
+  const unsigned wgs = (unsigned)((int64_t)a.B * a.G * a.chunks * a.splits);
+  const size_t bc = (size_t)2 * a.N * CH * 4;
+  k_scan_bwd_ends<IOT><<<dim3(wgs), SCAN_THREADS, bc, s>>>(a);
+  k_scan_bwd_join<<<dim3((unsigned)(((int64_t)a.B * a.D * a.N + 255) / 256)), 256, 0, s>>>(a);
+  k_scan_bwd<IOT><<<dim3(wgs), SCAN_THREADS, bc + (size_t)a.N * 64 * 16 + (size_t)TILE * a.N * 16, s>>>(a);
+  if (a.splits > 1) {
+    const int64_t n = (int64_t)2 * a.B * a.G * a.N * a.L;
+    k_scan_bwd_sum_bc<IOT><<<dim3((unsigned)min((n + 255) / 256, (int64_t)8192)), 256, 0, s>>>(a);
+  }
+  k_scan_bwd_sum_t<<<dim3((unsigned)(((int64_t)a.D * (a.N + 2) + 31) / 32)), 256, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t selective_scan(const ScanArgs& a, hipStream_t s) {
+  const int nv = (a.N + 7) / 8;
+#define HYENA_SCAN(V) (a.io ? launch_scan<1, V>(a, s) : launch_scan<0, V>(a, s))
+  return nv <= 1 ? HYENA_SCAN(1) : nv <= 2 ? HYENA_SCAN(2) : nv <= 4 ? HYENA_SCAN(4) : HYENA_SCAN(8);
+#undef HYENA_SCAN
+}
+
+hipError_t selective_scan_step(const ScanArgs& a, hipStream_t s) {
+  int lw = 0;
+  while ((4 << lw) < a.N) ++lw;
+  const int64_t threads = ((int64_t)a.B * a.D) << lw;
+  const dim3 grid((unsigned)((threads + 255) / 256));
+  if (a.io) k_scan_step<1><<<grid, 256, 0, s>>>(a, 1 << lw, lw, a.state_out);
+  else k_scan_step<0><<<grid, 256, 0, s>>>(a, 1 << lw, lw, a.state_out);
+  return hipGetLastError();
+}
+
+hipError_t selective_scan_backward(const ScanArgs& a, hipStream_t s) {
+  return a.io ? launch_scan_backward<1>(a, s) : launch_scan_backward<0>(a, s);
+}
+
+}  // namespace hyena

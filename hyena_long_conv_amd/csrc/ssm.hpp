@@ -1,0 +1,179 @@
+// ssm.hpp -- internal launch interface of the state-space block's operators
+// (short convolution, selective scan, residual norm, 8-bit product) between
+// their C ABI (api_ssm.cpp) and the kernel translation units.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace hyena {
+
+// ------------------------------------------------------- short convolution
+struct ConvArgs {
+  const void* x;           // [B][D][L]; [B][D] for the step
+  const float* w;          // [D][T]
+  const float* bias;       // [D] or nullptr
+  const void* state;       // [B][D][T-1] or nullptr
+  const int32_t* lengths;  // [B] or nullptr
+  void* y;
+  void* state_out;         // or nullptr
+  // backward
+  const void* gy;
+  const void* gstate_out;  // or nullptr
+  void* gx;
+  float* gw;               // [D][T]
+  float* gbias;            // [D] or nullptr
+  void* gstate;            // or nullptr
+  float* partial;          // workspace, [conv_backward_parts][D][T+1]
+  int B, D, T, silu, io;
+  int64_t L;
+};
+
+// Samples of one row that a workgroup of the backward covers: its sums over
+// time leave one partial for each.
+constexpr int64_t kConvSpan = 16384;
+inline int64_t conv_backward_parts(int64_t B, int64_t L) { return B * ((L + kConvSpan - 1) / kConvSpan); }
+
+// Rows share a workgroup of 256 threads when they are short: `per` threads
+// (a power of two, 8 steps each) to a row, or `blocks` workgroups of `span`
+// steps along a long one.
+struct ConvGrid {
+  int per, lper;
+  int64_t blocks, groups;
+};
+constexpr int64_t kConvStep = 2048;   // the forward's span: one word of 8 steps to a thread
+inline ConvGrid conv_grid(int64_t B, int64_t D, int64_t L, int64_t span) {
+  ConvGrid g;
+  const int64_t words = ((L < span ? L : span) + 7) / 8;
+  g.lper = 0;
+  while (g.lper < 8 && (1 << g.lper) < words) ++g.lper;
+  g.per = 1 << g.lper;
+  g.blocks = (L + span - 1) / span;
+  const int64_t rows = 256 >> g.lper;
+  g.groups = (B * D + rows - 1) / rows * g.blocks;
+  return g;
+}
+
+hipError_t short_conv(const ConvArgs& a, hipStream_t s);
+hipError_t short_conv_step(const ConvArgs& a, hipStream_t s);
+hipError_t short_conv_backward(const ConvArgs& a, hipStream_t s);
+
+// ---------------------------------------------------------- selective scan
+constexpr int kScanChunk = 128;     // steps that 16 lanes scan at once, 8 each
+constexpr int kScanTile = 16;       // channels of a workgroup: 4 waves of 4
+
+struct ScanArgs {
+  const void *u, *delta, *Bm, *Cm, *z;     // z: or nullptr
+  const float *A, *skip, *dbias, *state;   // skip, dbias, state: or nullptr
+  const int32_t* lengths;                  // or nullptr
+  void* y;
+  float* state_out;                        // or nullptr
+  int B, D, G, N, softplus, io;
+  int64_t L;
+  // time axis split into `segs` segments of `seg` steps (a multiple of the
+  // chunk): end states and sums of dt of all but the last, when segs > 1
+  int segs;
+  int64_t seg;
+  float* hend;                             // [B][segs][D][N]
+  float* sdt;                              // [B][segs][D]
+  // backward
+  const void* gy;
+  const float* gstate_out;                 // or nullptr
+  void *gu, *gdelta, *gB, *gC, *gz;        // gz: or nullptr
+  float *gA, *gskip, *gdbias, *gstate;     // all but gA: or nullptr
+  int chunks;                              // ceil(L / kScanChunk)
+  int splits;                              // workgroups that share a chunk's channels
+  float* hc;                               // [B][chunks][D][N] end states, then states at the chunks' starts, then gA's parts
+  float* qc;                               // [B][chunks][D][N] carries towards the chunks' starts, then from their ends
+  float* dts;                              // [B][chunks][D] sums of dt
+  float* ps;                               // [B][chunks][D] gskip's parts
+  float* pb;                               // [B][chunks][D] gdelta_bias's parts
+  float* gbc;                              // [splits][2][B][G][N][L] parts of gB and gC, when splits > 1
+};
+
+// Segments of the forward scan and their length.  A wave scans 4 channels;
+// with fewer than about two waves for each SIMD of the chip (1024) the time
+// axis is split, which costs a second pass over the decays.
+inline void scan_segments(int64_t B, int64_t D, int64_t L, int* segs, int64_t* seg) {
+  const int64_t waves = B * ((D + kScanTile - 1) / kScanTile) * 4;
+  int64_t s = 1;
+  if (waves < 1024) s = (2048 + waves - 1) / waves;
+  const int64_t chunks = (L + kScanChunk - 1) / kScanChunk;
+  if (s > chunks / 4) s = chunks / 4;      // at least four chunks in a segment
+  if (s < 1) s = 1;
+  const int64_t per = (chunks + s - 1) / s;
+  *seg = per * kScanChunk;
+  *segs = (int)((chunks + per - 1) / per);
+}
+
+struct ScanBackwardLayout {
+  int chunks, splits;
+  int64_t hc, qc, dts, ps, pb, gbc, total;   // byte offsets
+};
+
+inline ScanBackwardLayout scan_backward_layout(int64_t B, int64_t D, int64_t G, int64_t N, int64_t L) {
+  ScanBackwardLayout w;
+  w.chunks = (int)((L + kScanChunk - 1) / kScanChunk);
+  const int64_t tiles = (D / G + kScanTile - 1) / kScanTile;
+  int64_t s = (1024 + B * G * w.chunks - 1) / (B * G * w.chunks);
+  if (s > tiles) s = tiles;
+  const int64_t per = (tiles + s - 1) / s;
+  w.splits = (int)((tiles + per - 1) / per);
+  const auto up = [](int64_t n) { return (n + 255) / 256 * 256; };
+  const int64_t st = up(B * w.chunks * D * N * 4), rows = up(B * w.chunks * D * 4);
+  w.hc = 0;
+  w.qc = st;
+  w.dts = 2 * st;
+  w.ps = w.dts + rows;
+  w.pb = w.ps + rows;
+  w.gbc = w.pb + rows;
+  w.total = w.gbc + (w.splits > 1 ? w.splits * 2 * B * G * N * L * 4 : 0);
+  return w;
+}
+
+hipError_t selective_scan(const ScanArgs& a, hipStream_t s);
+hipError_t selective_scan_step(const ScanArgs& a, hipStream_t s);
+hipError_t selective_scan_backward(const ScanArgs& a, hipStream_t s);
+
+// ------------------------------------------------------------ residual norm
+struct NormArgs {
+  const void *x, *residual;   // residual: or nullptr
+  const float* weight;
+  void* y;                    // I/O dtype, or
+  uint8_t* q;                 // e4m3 codes with
+  float* scales;              // [rows][ceil(D/128)]
+  void* s_out;                // the sum; nullptr without residual
+  int64_t rows;
+  int D, io;
+  float eps;
+  // backward
+  const void *gy, *gs;        // gs: or nullptr
+  void* gx;
+  float* gw;
+  float* partial;             // workspace, [norm_backward_parts][D]
+  // 8-bit cast without a norm: blocks of block_rows x 128
+  int block_rows;
+};
+
+// Row slots of the backward's grid, a multiple of the 4 rows a workgroup may hold.
+inline int64_t norm_backward_parts(int64_t rows) { return rows < 4096 ? (rows + 15) / 16 * 4 : 1024; }
+
+hipError_t rms_norm(const NormArgs& a, hipStream_t s);
+hipError_t rms_norm_backward(const NormArgs& a, hipStream_t s);
+hipError_t quantize(const NormArgs& a, hipStream_t s);
+
+// ------------------------------------------------------------ 8-bit product
+struct ScaledArgs {
+  const uint8_t* q;        // [M][K] e4m3
+  const float* scales;     // [M][ceil(K/128)]
+  const uint8_t* wq;       // [N][K] e4m3
+  const float* wscales;    // [ceil(N/128)][ceil(K/128)]
+  const float* bias;       // [N] or nullptr
+  void* out;               // [M][N], or [M/L][N][L] (channel_major)
+  int64_t M, N, K, L;
+  int io, channel_major;
+};
+
+hipError_t scaled_matmul(const ScaledArgs& a, hipStream_t s);
+
+}  // namespace hyena

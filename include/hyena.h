@@ -378,6 +378,194 @@ hyena_status hyena_nd_forward(const void* v, const void* const* x, const void* s
                               int32_t per_sample, hyena_dtype io, void* workspace, int64_t workspace_bytes,
                               void* stream);
 
+/* ------------------------------------------------------------------------
+ * The state-space block: operators that stand next to the long convolution
+ * in a model of this kind -- a residual addition with a norm, a projection
+ * by an 8-bit matrix product, a short causal convolution, and a selective
+ * state-space scan, each with the form for single tokens of a serving loop
+ * and the backward pass of a training step where it has one.
+ *
+ * Shared by all of them: the conventions at the top of this file; sizes
+ * 1 <= B <= 2^20, 1 <= D <= 2^20, B*D <= 2^30, 1 <= L <= HYENA_MAX_L (SHAPE
+ * outside, UNSUPPORTED beyond a launch's 2^24 workgroups); activations and
+ * carried states 16-byte aligned (ALIGN), fp32 parameter vectors and lengths
+ * 4-byte aligned; an output may overlap no input and no other output (ALIAS).
+ * Arithmetic is fp32, bf16 values are widened exactly and rounded once, to
+ * nearest even, where they are stored.  Sums have a fixed order: equal inputs
+ * give equal bits.
+ *
+ * lengths (device int32 [B], or NULL): sequence b holds min(max(lengths[b],
+ * 0), L) steps.  Whatever stands behind them (NaN included) is not read into
+ * any result; outputs of activation shape are zero there, and the state left
+ * behind is the one at the sequence's own end.
+ * ---------------------------------------------------------------------- */
+
+/*
+ * Short causal depthwise convolution (the block's short filter by itself):
+ *   p[b][c][t] = bias[c] + sum_{j<T} w[c][j] x[b][c][t-j],
+ *   y = p, or p / (1 + exp(-p)) with silu,
+ * x[b][c][-i] = state[b][c][T-1-i] for i = 1..T-1 (oldest first; zeros where
+ * state is NULL).  state_out (NULL: not wanted) is the last T-1 inputs of
+ * state and x together, the state of a call that continues the sequence.
+ * With T = 1 there is no state: both must be NULL (SHAPE).
+ * x, y [B][D][L], state, state_out [B][D][T-1], I/O dtype; w [D][T], bias [D]
+ * (or NULL), fp32; T in 1..HYENA_MAX_SHORT.
+ */
+typedef struct {
+  int64_t B;
+  int64_t L;
+  int32_t D;
+  int32_t T;
+  int32_t silu;            /* 0 or 1                     */
+  int32_t reserved;        /* 0                          */
+  const float* w;
+  const float* bias;       /* or NULL                    */
+  const void* state;       /* or NULL                    */
+  const int32_t* lengths;  /* or NULL                    */
+} hyena_short_conv_params;
+
+hyena_status hyena_short_conv(const void* x, const hyena_short_conv_params* p, void* y, void* state_out,
+                              hyena_dtype io, void* stream);
+
+/* One token for each sequence: x, y [B][D]; state [B][D][T-1] is read and
+ * moved on by one in place (NULL with T = 1).  p->L, p->state and p->lengths
+ * are not used. */
+hyena_status hyena_short_conv_step(const void* x, const hyena_short_conv_params* p, void* state, void* y,
+                                   hyena_dtype io, void* stream);
+
+/* Gradients of a loss with dloss/dy = gy and dloss/dstate_out = gstate_out
+ * (NULL: zero): gx [B][D][L] and gstate [B][D][T-1] (NULL: not wanted) in the
+ * I/O dtype, gw [D][T] and gbias [D] (NULL: not wanted) fp32, summed over
+ * batch and time.  workspace: hyena_short_conv_backward_workspace_bytes(). */
+int64_t hyena_short_conv_backward_workspace_bytes(int64_t B, int32_t D, int32_t T, int64_t L);
+hyena_status hyena_short_conv_backward(const void* x, const hyena_short_conv_params* p, const void* gy,
+                                       const void* gstate_out, void* gx, float* gw, float* gbias, void* gstate,
+                                       hyena_dtype io, void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * Selective state-space scan.  Per sequence b, channel d of group g = d /
+ * (D/G) and state n:
+ *   dt[t]   = softplus(delta[b][d][t] + delta_bias[d])  (or the sum itself),
+ *   h[t][n] = exp(dt[t] A[d][n]) h[t-1][n] + dt[t] u[b][d][t] Bm[b][g][n][t],
+ *   y[t]    = sum_n Cm[b][g][n][t] h[t][n] + skip[d] u[b][d][t],
+ * times z / (1 + exp(-z)) where z is given; h[-1] = state[b][d] (or zeros).
+ * state_out (NULL: not wanted) is h at the sequence's end.
+ * u, delta, z, y [B][D][L], Bm, Cm [B][G][N][L], I/O dtype; A [D][N], skip,
+ * delta_bias [D] (or NULL), state, state_out [B][D][N], fp32.  N in
+ * 1..HYENA_MAX_STATE; G divides D.  A is finite and, for a decaying state,
+ * not positive: the factors exp(dt A) are multiplied up over 128 steps, which
+ * must not overflow.
+ * workspace: hyena_selective_scan_workspace_bytes() (0 where the time axis is
+ * not split).
+ */
+#define HYENA_MAX_STATE 64
+
+typedef struct {
+  int64_t B;
+  int64_t L;
+  int32_t D;
+  int32_t G;
+  int32_t N;
+  int32_t softplus;         /* 0 or 1                    */
+  const void* u;
+  const void* delta;
+  const float* A;
+  const void* Bm;
+  const void* Cm;
+  const float* skip;        /* or NULL                   */
+  const void* z;            /* or NULL                   */
+  const float* delta_bias;  /* or NULL                   */
+  const float* state;       /* or NULL                   */
+  const int32_t* lengths;   /* or NULL                   */
+} hyena_selective_scan_params;
+
+int64_t hyena_selective_scan_workspace_bytes(int64_t B, int32_t D, int32_t N, int64_t L);
+hyena_status hyena_selective_scan(const hyena_selective_scan_params* p, void* y, float* state_out, hyena_dtype io,
+                                  void* workspace, int64_t workspace_bytes, void* stream);
+
+/* One token for each sequence: u, delta, z, y [B][D], Bm, Cm [B][G][N]; state
+ * [B][D][N] fp32 is moved on by one in place.  p->L, p->state and p->lengths
+ * are not used; A is 16-byte aligned as well. */
+hyena_status hyena_selective_scan_step(const hyena_selective_scan_params* p, float* state, void* y, hyena_dtype io,
+                                       void* stream);
+
+/* Gradients of a loss with dloss/dy = gy and dloss/dstate_out = gstate_out
+ * (NULL: zero).  gu, gdelta, gz as u; gB, gC as Bm, summed over the group's
+ * channels; gA [D][N], gskip, gdelta_bias [D] fp32, summed over batch and
+ * time; gstate [B][D][N] fp32.  gz is required with z and NULL without it;
+ * gskip, gdelta_bias and gstate may be NULL (not wanted).  The states are
+ * computed again from p.  workspace:
+ * hyena_selective_scan_backward_workspace_bytes(). */
+typedef struct {
+  void* gu;
+  void* gdelta;
+  float* gA;
+  void* gB;
+  void* gC;
+  float* gskip;
+  void* gz;
+  float* gdelta_bias;
+  float* gstate;
+} hyena_selective_scan_grads;
+
+int64_t hyena_selective_scan_backward_workspace_bytes(int64_t B, int32_t D, int32_t G, int32_t N, int64_t L);
+hyena_status hyena_selective_scan_backward(const hyena_selective_scan_params* p, const void* gy,
+                                           const float* gstate_out, const hyena_selective_scan_grads* g,
+                                           hyena_dtype io, void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * Residual addition and root-mean-square norm along D of `rows` rows:
+ *   s = x + residual (stored in s_out, rounded to the I/O dtype, and normed
+ *   as stored; s = x and s_out NULL where residual is NULL),
+ *   y = s / sqrt(mean(s^2) + eps) * weight.
+ * x, residual, s_out, y [rows][D] I/O dtype, weight [D] fp32; rows <= 2^31,
+ * eps >= 0 (a row of zeros with eps = 0 gives NaN).
+ *
+ * hyena_rms_norm_quantized stores y in 8 bits instead: q [rows][D] e4m3 codes
+ * (OCP, largest value 448) and scales [rows][ceil(D/128)] fp32, one for each
+ * 128 values of a row: scale = max|y| / 448 (1 where all are 0, at least
+ * 2^-126), q = e4m3(y / scale), rounded to nearest even from the fp32 y.  A
+ * block that holds a NaN or an infinity is NaN as a whole.
+ *
+ * hyena_rms_norm_backward: from s (x, or what s_out holds) and gy the
+ * gradient gx of s, and gw [D] fp32 of weight; gs (NULL: zero), the gradient
+ * that reaches s past the norm, is added to gx.  The same gx is the gradient
+ * of x and of residual.
+ */
+hyena_status hyena_rms_norm(const void* x, const void* residual, const float* weight, void* y, void* s_out,
+                            int64_t rows, int32_t D, float eps, hyena_dtype io, void* stream);
+hyena_status hyena_rms_norm_quantized(const void* x, const void* residual, const float* weight, void* q,
+                                      float* scales, void* s_out, int64_t rows, int32_t D, float eps,
+                                      hyena_dtype io, void* stream);
+int64_t hyena_rms_norm_backward_workspace_bytes(int64_t rows, int32_t D);
+hyena_status hyena_rms_norm_backward(const void* s, const float* weight, const void* gy, const void* gs, void* gx,
+                                     float* gw, int64_t rows, int32_t D, float eps, hyena_dtype io, void* workspace,
+                                     int64_t workspace_bytes, void* stream);
+
+/*
+ * Matrix product of 8-bit operands with block scales:
+ *   out[m][n] = sum_k (q[m][k] scales[m][k/128]) (wq[n][k] wscales[n/128][k/128]) + bias[n]
+ * q [M][K], wq [N][K] e4m3, scales [M][ceil(K/128)], wscales [ceil(N/128)]
+ * [ceil(K/128)] fp32, bias [N] fp32 or NULL.  Each block of 128 is summed on
+ * the matrix cores and scaled into an fp32 sum: for an fp32 output in fp32,
+ * for a bf16 output by the 8-bit instructions, whose sums are good to about
+ * 2^-16 of the terms' sizes.  M = B * L rows of
+ * tokens; out is [B][L][N], or with channel_major [B][N][L], the layout of
+ * the operators above, in the I/O dtype.  K a multiple of 16 (UNSUPPORTED
+ * otherwise), K, N <= 2^20, out 16-byte aligned.  It serves a product's
+ * forward, and the gradient of its left operand with the transposed weight's
+ * codes.
+ *
+ * hyena_quantize: codes and scales as above of x [rows][K] (any K): blocks of
+ * block_rows x 128 with block_rows 1 (the left operand) or 128 (the right
+ * one; scales [ceil(rows/128)][ceil(K/128)]).
+ */
+hyena_status hyena_quantize(const void* x, void* q, float* scales, int64_t rows, int32_t K, int32_t block_rows,
+                            hyena_dtype io, void* stream);
+hyena_status hyena_scaled_matmul(const void* q, const float* scales, const void* wq, const float* wscales,
+                                 const float* bias, void* out, int64_t B, int64_t L, int32_t N, int32_t K,
+                                 int32_t channel_major, hyena_dtype io, void* stream);
+
 /* Static description of a status code. */
 const char* hyena_status_str(hyena_status s);
 
