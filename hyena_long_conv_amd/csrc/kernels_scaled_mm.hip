@@ -11,6 +11,8 @@
 namespace hyena {
 namespace {
 
+constexpr int KS = 128;                            // k of a step: one block of scales
+
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
@@ -58,64 +60,290 @@ __device__ __forceinline__ f32x4v mfma128(i32x8 a, i32x8 b) {
   }
 }
 
-// 64 x 64 outputs to a workgroup, 32 x 32 to a wave.
+// ------------------------------------------------------------ tiles in LDS
+//
+// A workgroup of WM x WN waves computes BM = 16 IM WM rows by BN = 16 IN WN
+// columns, one block of 128 along k at a time.  A step's operands go from
+// global memory straight to one of two LDS stages while the other one is
+// multiplied.  An LDS row is 128 bytes, 8 words of 16; word c of row r lies
+// in slot c ^ (r & 7), so that the 8 lanes of a read's turn touch 8 different
+// slots.  The right operand's rows are the matrix instruction's rows: a lane
+// then holds 4 neighbouring n of one m, one scale serves its 4 values, and
+// wscales is one value for a wave, whose n stay in one block of 128.
+
+typedef __attribute__((address_space(3))) void* lds_ptr_t;
+constexpr uint32_t OOB = 0x7ffffff0u;              // behind every buffer: reads as zeros
+
+template <int ROWS, int WAVES>
+struct TileLoads {
+  static constexpr int J = ROWS * 8 / 64 / WAVES;  // instructions of a wave: 8 rows each
+  uint32_t off[J];
+  uint32_t kq[J];
+  __amdgpu_buffer_rsrc_t rs;
+  __device__ __forceinline__ void init(const uint8_t* base, int64_t row0, int64_t rows, int K, int wave, int lane) {
+    const int64_t left = rows - row0;
+    const int have = left > ROWS ? ROWS : (int)left;
+    rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base + row0 * K), (short)0, have * K, 0x00020000);
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const int s = (J * wave + j) * 64 + lane, r = s >> 3, c = (s & 7) ^ (r & 7);
+      kq[j] = 16u * c;
+      off[j] = r < have ? (uint32_t)(r * K) + kq[j] : OOB;
+    }
+  }
+  // The step at k0 into the stage's rows; K a multiple of 16, words behind it are zeros.
+  __device__ __forceinline__ void issue(unsigned char* dst, int wave, int k0, int K) const {
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const uint32_t o = (uint32_t)k0 + kq[j] < (uint32_t)K && off[j] != OOB ? off[j] + (uint32_t)k0 : OOB;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(dst + (J * wave + j) * 1024), 16, (int)o, 0, 0, 0);
+    }
+  }
+};
+
+__device__ __forceinline__ i32x8 tile_operand(const unsigned char* rows, int l, int h) {
+  const unsigned char* r = rows + l * KS;
+  const i32x4 a = *reinterpret_cast<const i32x4*>(r + 16 * ((2 * h) ^ (l & 7)));
+  const i32x4 b = *reinterpret_cast<const i32x4*>(r + 16 * ((2 * h + 1) ^ (l & 7)));
+  return i32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+}
+
+// Eight consecutive outputs of a row or, channel-major, of a channel.
 template <int IOT, bool CM>
-__global__ __launch_bounds__(256) void k_scaled_mm(ScaledArgs a) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l = lane & 15, h = lane >> 4;
-  const int64_t M = a.M, N = a.N, K = a.K, kb = (K + 127) / 128;
-  const int64_t nt = (N + 63) / 64;
-  const int64_t m0 = blockIdx.x / nt * 64 + (wave & 1) * 32, n0 = blockIdx.x % nt * 64 + (wave >> 1) * 32;
-  f32x4v acc[2][2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int j = 0; j < 2; ++j) acc[i][j] = f32x4v{0.f, 0.f, 0.f, 0.f};
-  for (int64_t b = 0; b < kb; ++b) {
-    i32x8 x[2], w[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      x[i] = operand(a.q + min(m0 + 16 * i + l, M - 1) * K, b * 128 + 32 * h, K);
-      w[i] = operand(a.wq + min(n0 + 16 * i + l, N - 1) * K, b * 128 + 32 * h, K);
+__device__ __forceinline__ void put8(const ScaledArgs& a, int64_t m, int64_t n, const float (&v)[8]) {
+  if constexpr (!CM) {
+    if (m < a.M && n < a.N) st8n<IOT>(a.out, m * a.N + n, v, (int)min(a.N - n, (int64_t)8));
+  } else {
+    if (n >= a.N || m >= a.M) return;
+    const uint32_t L = (uint32_t)a.L, b = (uint32_t)m / L, t = (uint32_t)m - b * L;
+    if (t + 8 <= L) {
+      st8n<IOT>(a.out, ((int64_t)b * a.N + n) * a.L + t, v, 8);
+      return;
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int e = 0; e < 8; ++e) {                     // across the end of a sequence
+      const uint32_t me = (uint32_t)m + e, be = me / L;
+      if (me < a.M) st1<IOT>(a.out, ((int64_t)be * a.N + n) * a.L + (me - be * L), v[e]);
+    }
+  }
+}
+
+// Workgroup -> tile: an XCD (workgroup id mod 8) takes a contiguous part of
+// the tiles in an order that goes through panels of 8 tiles along m, so that
+// the workgroups of an XCD share rows of both operands in its L2.
+__device__ __forceinline__ bool tile_of(int64_t tm, int64_t tn, int64_t& m, int64_t& n) {
+  const int64_t per = (tm * tn + 7) / 8, k = blockIdx.x / 8, t = (blockIdx.x & 7) * per + k;
+  if (k >= per || t >= tm * tn) return false;
+  const int64_t panel = t / (8 * tn), left = tm - panel * 8, wide = left < 8 ? left : 8, u = t - panel * 8 * tn;
+  n = u / wide;
+  m = panel * 8 + (u - n * wide);
+  return true;
+}
+
+template <int IOT, bool CM, int IM, int IN, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN) void k_scaled_mm(ScaledArgs a) {
+  constexpr int BM = 16 * IM * WM, BN = 16 * IN * WN, STAGE = (BM + BN) * KS, W = WM * WN;
+  static_assert(128 % (16 * IN) == 0, "a wave's n lie in one block of wscales");
+  extern __shared__ __attribute__((aligned(1024))) unsigned char stage[];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l = lane & 15, h = lane >> 4;
+  const int K = (int)a.K, kb = (K + KS - 1) / KS;
+  int64_t mt, nt;
+  if (!tile_of((a.M + BM - 1) / BM, (a.N + BN - 1) / BN, mt, nt)) return;
+  const int64_t m0 = mt * BM, n0 = nt * BN;
+  const int wm = wave % WM, wn = wave / WM;
+  TileLoads<BM, W> lx;
+  TileLoads<BN, W> lw;
+  lx.init(a.q, m0, a.M, K, wave, lane);
+  lw.init(a.wq, n0, a.N, K, wave, lane);
+  // this lane's rows' scales; the wave's block of wscales
+  const float* sx[IM];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int64_t n = min(n0 + 16 * j + (CM ? l : 4 * h), N - 1);
-        const float sw = a.wscales[n / 128 * kb + b];
-        const f32x4v p = CM ? mfma128<IOT>(x[i], w[j]) : mfma128<IOT>(w[j], x[i]);
+  for (int i = 0; i < IM; ++i) sx[i] = a.scales + min(m0 + (wm * IM + i) * 16 + l, a.M - 1) * kb;
+  const int64_t nw = n0 + wn * IN * 16;
+  const float* sw = a.wscales + min(nw, a.N - 1) / 128 * kb;
+
+  f32x4v acc[IM][IN];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int64_t m = min(m0 + 16 * i + (CM ? 4 * h + e : l), M - 1);
-          acc[i][j][e] = fmaf(p[e], a.scales[m * kb + b] * sw, acc[i][j][e]);
+  for (int i = 0; i < IM; ++i)
+#pragma unroll
+    for (int j = 0; j < IN; ++j) acc[i][j] = f32x4v{0.f, 0.f, 0.f, 0.f};
+  float sn[IM];
+#pragma unroll
+  for (int i = 0; i < IM; ++i) sn[i] = sx[i][0] * sw[0];
+  lx.issue(stage, wave, 0, K);
+  lw.issue(stage + BM * KS, wave, 0, K);
+  for (int b = 0; b < kb; ++b) {
+    float sc[IM];
+#pragma unroll
+    for (int i = 0; i < IM; ++i) sc[i] = sn[i];
+    // this wave's loads of the step are in LDS and its reads of the other
+    // stage are done; the barrier makes both hold for all waves
+    __builtin_amdgcn_s_waitcnt(0x0070);               // vmcnt(0) lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
+    if (b + 1 < kb) {
+      unsigned char* next = stage + ((b + 1) & 1) * STAGE;
+      lx.issue(next, wave, (b + 1) * KS, K);
+      lw.issue(next + BM * KS, wave, (b + 1) * KS, K);
+#pragma unroll
+      for (int i = 0; i < IM; ++i) sn[i] = sx[i][b + 1] * sw[b + 1];
+    }
+    const unsigned char* X = stage + (b & 1) * STAGE + wm * IM * 16 * KS;
+    const unsigned char* Y = stage + (b & 1) * STAGE + BM * KS + wn * IN * 16 * KS;
+    i32x8 w[IN];
+#pragma unroll
+    for (int j = 0; j < IN; ++j) w[j] = tile_operand(Y + j * 16 * KS, l, h);
+#pragma unroll
+    for (int i = 0; i < IM; ++i) {
+      const i32x8 x = tile_operand(X + i * 16 * KS, l, h);
+#pragma unroll
+      for (int j = 0; j < IN; ++j) {
+        const f32x4v p = mfma128<IOT>(w[j], x);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(p[e], sc[i], acc[i][j][e]);
+      }
+    }
+  }
+
+  // Out through LDS, each wave its own part, 16 rows (or 16 IM tokens of 16
+  // channels) at a time, so that global stores are whole words of a row.
+  __syncthreads();
+  float* ep = reinterpret_cast<float*>(stage) + wave * (CM ? 16 * (16 * IM + 4) : 16 * (16 * IN + 4));
+  if constexpr (!CM) {
+    constexpr int LD = 16 * IN + 4;
+#pragma unroll
+    for (int i = 0; i < IM; ++i) {
+#pragma unroll
+      for (int j = 0; j < IN; ++j) *reinterpret_cast<f32x4v*>(ep + l * LD + 16 * j + 4 * h) = acc[i][j];
+      __builtin_amdgcn_wave_barrier();
+      for (int s = lane; s < 16 * 2 * IN; s += 64) {
+        const int r = s / (2 * IN), c = 8 * (s - r * 2 * IN);
+        const int64_t n = nw + c;
+        float v[8], bv[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = ep[r * LD + c + e];
+        if (a.bias) {
+          widen8<0>(ld8n<0>(a.bias, n, (int)min(a.N - n, (int64_t)8)), bv);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] += bv[e];
         }
+        put8<IOT, false>(a, m0 + (wm * IM + i) * 16 + r, n, v);
+      }
+      __builtin_amdgcn_wave_barrier();
+    }
+  } else {
+    constexpr int LD = 16 * IM + 4;
+#pragma unroll
+    for (int j = 0; j < IN; ++j) {
+#pragma unroll
+      for (int i = 0; i < IM; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) ep[(4 * h + e) * LD + 16 * i + l] = acc[i][j][e];
+      __builtin_amdgcn_wave_barrier();
+      for (int s = lane; s < 16 * 2 * IM; s += 64) {
+        const int r = s / (2 * IM), c = 8 * (s - r * 2 * IM);
+        const int64_t n = nw + 16 * j + r;
+        const float bias = a.bias && n < a.N ? a.bias[n] : 0.f;
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = ep[r * LD + c + e] + bias;
+        put8<IOT, true>(a, m0 + wm * IM * 16 + c, n, v);
+      }
+      __builtin_amdgcn_wave_barrier();
+    }
+  }
+}
+
+// ---------------------------------------------------------------- few rows
+//
+// Up to 64 rows: the weights' bytes are the call.  A workgroup takes 16
+// columns and splits k over its 8 waves; a lane loads its operands straight
+// into registers (a row of 128 bytes is one line), and the waves' sums meet
+// in LDS.
+template <int IOT, bool CM, int IM>
+__global__ __launch_bounds__(512) void k_scaled_mm_rows(ScaledArgs a) {
+  __shared__ float part[8][IM][16][17];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l = lane & 15, h = lane >> 4;
+  const int64_t K = a.K, kb = (K + KS - 1) / KS, n0 = blockIdx.x * (int64_t)16;
+  const uint8_t* w = a.wq + min(n0 + l, a.N - 1) * K + 32 * h;
+  const float* sw = a.wscales + n0 / 128 * kb;
+  f32x4v acc[IM];
+#pragma unroll
+  for (int i = 0; i < IM; ++i) acc[i] = f32x4v{0.f, 0.f, 0.f, 0.f};
+  for (int64_t b0 = wave; b0 < kb; b0 += 16) {        // two blocks' loads in flight
+    i32x8 y[2], x[2][IM];
+    float sc[2][IM];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int64_t b = b0 + 8 * u, bs = min(b, kb - 1);    // zeros behind K
+      y[u] = operand(w, b * KS, K - 32 * h);
+#pragma unroll
+      for (int i = 0; i < IM; ++i) {
+        const int64_t m = min((int64_t)(16 * i + l), a.M - 1);
+        x[u][i] = operand(a.q + m * K + 32 * h, b * KS, K - 32 * h);
+        sc[u][i] = a.scales[m * kb + bs] * sw[bs];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int i = 0; i < IM; ++i) {
+        const f32x4v p = mfma128<IOT>(y[u], x[u][i]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][e] = fmaf(p[e], sc[u][i], acc[i][e]);
       }
   }
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < IM; ++i)
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int e = 0; e < 4; ++e) part[wave][i][l][4 * h + e] = acc[i][e];
+  __syncthreads();
+  for (int s = tid; s < IM * 256; s += 512) {
+    // neighbouring threads: neighbouring n, or tokens where those are contiguous
+    const int i = s >> 8, r = CM ? s & 15 : (s >> 4) & 15, c = CM ? (s >> 4) & 15 : s & 15;
+    const int64_t m = 16 * i + r, n = n0 + c;
+    if (m >= a.M || n >= a.N) continue;
+    float v = part[0][i][r][c];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int64_t m = m0 + 16 * i + (CM ? 4 * h + e : l), n = n0 + 16 * j + (CM ? l : 4 * h + e);
-        if (m >= M || n >= N) continue;
-        const float v = acc[i][j][e] + (a.bias ? a.bias[n] : 0.f);
-        st1<IOT>(a.out, CM ? (m / a.L * N + n) * a.L + m % a.L : m * N + n, v);
-      }
+    for (int k = 1; k < 8; ++k) v += part[k][i][r][c];
+    if (a.bias) v += a.bias[n];
+    st1<IOT>(a.out, CM ? (m / a.L * a.N + n) * a.L + m % a.L : m * a.N + n, v);
+  }
+}
+
+template <int IOT, bool CM, int IM, int IN, int WM, int WN>
+hipError_t launch_tiles(const ScaledArgs& a, hipStream_t s) {
+  constexpr int BM = 16 * IM * WM, BN = 16 * IN * WN;
+  constexpr size_t stages = 2 * (BM + BN) * KS, out = (size_t)WM * WN * 16 * (16 * (CM ? IM : IN) + 4) * 4;
+  const int64_t tiles = ((a.M + BM - 1) / BM) * ((a.N + BN - 1) / BN);
+  k_scaled_mm<IOT, CM, IM, IN, WM, WN>
+      <<<dim3((unsigned)((tiles + 7) / 8 * 8)), 64 * WM * WN, stages > out ? stages : out, s>>>(a);
+  return hipGetLastError();
+}
+
+template <int IOT, bool CM>
+hipError_t launch_rows(const ScaledArgs& a, hipStream_t s) {
+  const dim3 grid((unsigned)((a.N + 15) / 16));
+  if (a.M <= 16) k_scaled_mm_rows<IOT, CM, 1><<<grid, 512, 0, s>>>(a);
+  else if (a.M <= 32) k_scaled_mm_rows<IOT, CM, 2><<<grid, 512, 0, s>>>(a);
+  else k_scaled_mm_rows<IOT, CM, 4><<<grid, 512, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+template <int IOT, bool CM>
+hipError_t launch_product(const ScaledArgs& a, hipStream_t s) {
+  const auto tiles = [&](int64_t bm, int64_t bn) { return ((a.M + bm - 1) / bm) * ((a.N + bn - 1) / bn); };
+  if (a.M <= 64) return launch_rows<IOT, CM>(a, s);
+  if (IOT == 1 && tiles(256, 256) >= 192) return launch_tiles<IOT, CM, IOT ? 8 : 4, 4, 2, IOT ? 4 : 2>(a, s);
+  if (tiles(128, 128) >= 192) return launch_tiles<IOT, CM, 4, 4, 2, 2>(a, s);
+  return launch_tiles<IOT, CM, 2, 2, 2, 2>(a, s);
 }
 
 }  // namespace
 
 hipError_t scaled_matmul(const ScaledArgs& a, hipStream_t s) {
-  const unsigned n = (unsigned)(((a.M + 63) / 64) * ((a.N + 63) / 64));
-  if (a.channel_major) {
-    if (a.io) k_scaled_mm<1, true><<<n, 256, 0, s>>>(a);
-    else k_scaled_mm<0, true><<<n, 256, 0, s>>>(a);
-  } else {
-    if (a.io) k_scaled_mm<1, false><<<n, 256, 0, s>>>(a);
-    else k_scaled_mm<0, false><<<n, 256, 0, s>>>(a);
-  }
-  return hipGetLastError();
+  if (a.channel_major) return a.io ? launch_product<1, true>(a, s) : launch_product<0, true>(a, s);
+  return a.io ? launch_product<1, false>(a, s) : launch_product<0, false>(a, s);
 }
 
 }  // namespace hyena

@@ -450,7 +450,9 @@ def test_scaled_matmul_layouts_and_batches():
     off = (cols.transpose(1, 2).double() - rows.double()).abs()
     assert bool((off <= 2 * HALF[torch.bfloat16] * rows.double().abs() + 2.0 ** -14 * rows.double().abs().max()).all())
     one = H.scaled_matmul(q[1].contiguous(), s[1].contiguous(), wq, ws)
-    assert torch.equal(one, rows[1])
+    # few rows are summed in parts along k: each side is within half a step, and 2^-16 of its terms, of the product
+    off = (one.double() - rows[1].double()).abs()
+    assert bool((off <= 2 * HALF[torch.bfloat16] * rows[1].double().abs() + 2.0 ** -14 * rows.double().abs().max()).all())
 
 
 # ------------------------------------------------- streams, graphs, together
