@@ -167,41 +167,69 @@ __global__ __launch_bounds__(64 * WM * WN) void k_scaled_mm(ScaledArgs a) {
   for (int i = 0; i < IM; ++i)
 #pragma unroll
     for (int j = 0; j < IN; ++j) acc[i][j] = f32x4v{0.f, 0.f, 0.f, 0.f};
-  float sn[IM];
+  // the next step's scales, multiplied only after the barrier that waits for them
+  float xn[IM], wn_;
 #pragma unroll
-  for (int i = 0; i < IM; ++i) sn[i] = sx[i][0] * sw[0];
+  for (int i = 0; i < IM; ++i) xn[i] = sx[i][0];
+  wn_ = sw[0];
   lx.issue(stage, wave, 0, K);
   lw.issue(stage + BM * KS, wave, 0, K);
   for (int b = 0; b < kb; ++b) {
-    float sc[IM];
-#pragma unroll
-    for (int i = 0; i < IM; ++i) sc[i] = sn[i];
     // this wave's loads of the step are in LDS and its reads of the other
     // stage are done; the barrier makes both hold for all waves
     __builtin_amdgcn_s_waitcnt(0x0070);               // vmcnt(0) lgkmcnt(0)
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
+    float sc[IM];
+#pragma unroll
+    for (int i = 0; i < IM; ++i) sc[i] = xn[i] * wn_;
     if (b + 1 < kb) {
       unsigned char* next = stage + ((b + 1) & 1) * STAGE;
       lx.issue(next, wave, (b + 1) * KS, K);
       lw.issue(next + BM * KS, wave, (b + 1) * KS, K);
-#pragma unroll
-      for (int i = 0; i < IM; ++i) sn[i] = sx[i][b + 1] * sw[b + 1];
     }
+    const int bn = min(b + 1, kb - 1);
+#pragma unroll
+    for (int i = 0; i < IM; ++i) xn[i] = sx[i][bn];
+    wn_ = sw[bn];
     const unsigned char* X = stage + (b & 1) * STAGE + wm * IM * 16 * KS;
     const unsigned char* Y = stage + (b & 1) * STAGE + BM * KS + wn * IN * 16 * KS;
-    i32x8 w[IN];
+    i32x8 w[IN], x = tile_operand(X, l, h);
 #pragma unroll
     for (int j = 0; j < IN; ++j) w[j] = tile_operand(Y + j * 16 * KS, l, h);
+    // The products of one row of tiles run while the one before is scaled and
+    // added: a product is ready some 16 cycles after it was issued.
+    f32x4v p[2][IN];
 #pragma unroll
     for (int i = 0; i < IM; ++i) {
-      const i32x8 x = tile_operand(X + i * 16 * KS, l, h);
+      i32x8 next = x;
+      if (i + 1 < IM) next = tile_operand(X + (i + 1) * 16 * KS, l, h);
 #pragma unroll
       for (int j = 0; j < IN; ++j) {
-        const f32x4v p = mfma128<IOT>(w[j], x);
+        p[i & 1][j] = mfma128<IOT>(w[j], x);
+        if (i > 0) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(p[e], sc[i], acc[i][j][e]);
+          for (int e = 0; e < 4; ++e) acc[i - 1][j][e] = fmaf(p[(i - 1) & 1][j][e], sc[i - 1], acc[i - 1][j][e]);
+        }
       }
+      x = next;
+    }
+#pragma unroll
+    for (int j = 0; j < IN; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[IM - 1][j][e] = fmaf(p[(IM - 1) & 1][j][e], sc[IM - 1], acc[IM - 1][j][e]);
+    if constexpr (IOT == 1) {                         // that order, for the instruction scheduler
+      __builtin_amdgcn_sched_group_barrier(0x100, 2 * IN + 4, 0);
+#pragma unroll
+      for (int i = 0; i < IM; ++i) {
+#pragma unroll
+        for (int j = 0; j < IN; ++j) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          if (i > 0) __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+        }
+        if (i + 2 < IM) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+      }
+      __builtin_amdgcn_sched_group_barrier(0x002, 4 * IN, 0);
     }
   }
 
