@@ -65,14 +65,22 @@ __device__ __forceinline__ f32x4v mfma128(i32x8 a, i32x8 b) {
 // A workgroup of WM x WN waves computes BM = 16 IM WM rows by BN = 16 IN WN
 // columns, one block of 128 along k at a time.  A step's operands go from
 // global memory straight to one of two LDS stages while the other one is
-// multiplied.  An LDS row is 128 bytes, 8 words of 16; word c of row r lies
-// in slot c ^ (r & 7), so that the 8 lanes of a read's turn touch 8 different
-// slots.  The right operand's rows are the matrix instruction's rows: a lane
+// multiplied, and so do its rows' scales.  An LDS row is 128 bytes, 8 words
+// of 16; word c of row r lies in slot c ^ swizzle(r).  A read takes word 2h or
+// 2h + 1 of 16 rows; two rows span the 64 banks, so the 16 lanes of a turn
+// have to hold all 8 slots of even and of odd rows.  The right operand's rows are the matrix instruction's rows: a lane
 // then holds 4 neighbouring n of one m, one scale serves its 4 values, and
 // wscales is one value for a wave, whose n stay in one block of 128.
 
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
 constexpr uint32_t OOB = 0x7ffffff0u;              // behind every buffer: reads as zeros
+
+// Pairs of rows go through the 8 slots; the order also keeps turns apart that
+// join 8 rows of one h with the 8 others of h + 1 (pairs 0, 1, 6, 7 and
+// 2, 3, 4, 5 hold slot sets that are closed under ^ 2).
+__device__ __forceinline__ int swizzle(int r) {
+  return ((r >> 1) & 1) | ((r >> 2) & 2) | ((((r >> 2) ^ (r >> 3)) & 1) << 2);
+}
 
 template <int ROWS, int WAVES>
 struct TileLoads {
@@ -86,7 +94,7 @@ struct TileLoads {
     rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base + row0 * K), (short)0, have * K, 0x00020000);
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      const int s = (J * wave + j) * 64 + lane, r = s >> 3, c = (s & 7) ^ (r & 7);
+      const int s = (J * wave + j) * 64 + lane, r = s >> 3, c = (s & 7) ^ swizzle(r);
       kq[j] = 16u * c;
       off[j] = r < have ? (uint32_t)(r * K) + kq[j] : OOB;
     }
@@ -103,8 +111,8 @@ struct TileLoads {
 
 __device__ __forceinline__ i32x8 tile_operand(const unsigned char* rows, int l, int h) {
   const unsigned char* r = rows + l * KS;
-  const i32x4 a = *reinterpret_cast<const i32x4*>(r + 16 * ((2 * h) ^ (l & 7)));
-  const i32x4 b = *reinterpret_cast<const i32x4*>(r + 16 * ((2 * h + 1) ^ (l & 7)));
+  const i32x4 a = *reinterpret_cast<const i32x4*>(r + 16 * ((2 * h) ^ swizzle(l)));
+  const i32x4 b = *reinterpret_cast<const i32x4*>(r + 16 * ((2 * h + 1) ^ swizzle(l)));
   return i32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
 }
 
@@ -142,10 +150,10 @@ __device__ __forceinline__ bool tile_of(int64_t tm, int64_t tn, int64_t& m, int6
 
 template <int IOT, bool CM, int IM, int IN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN) void k_scaled_mm(ScaledArgs a) {
-  constexpr int BM = 16 * IM * WM, BN = 16 * IN * WN, STAGE = (BM + BN) * KS, W = WM * WN;
+  constexpr int BM = 16 * IM * WM, BN = 16 * IN * WN, STAGE = (BM + BN) * KS + BM * 4, W = WM * WN;
   static_assert(128 % (16 * IN) == 0, "a wave's n lie in one block of wscales");
   extern __shared__ __attribute__((aligned(1024))) unsigned char stage[];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l = lane & 15, h = lane >> 4;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = lane & 15, h = lane >> 4;
   const int K = (int)a.K, kb = (K + KS - 1) / KS;
   int64_t mt, nt;
   if (!tile_of((a.M + BM - 1) / BM, (a.N + BN - 1) / BN, mt, nt)) return;
@@ -155,45 +163,41 @@ __global__ __launch_bounds__(64 * WM * WN) void k_scaled_mm(ScaledArgs a) {
   TileLoads<BN, W> lw;
   lx.init(a.q, m0, a.M, K, wave, lane);
   lw.init(a.wq, n0, a.N, K, wave, lane);
-  // this lane's rows' scales; the wave's block of wscales
-  const float* sx[IM];
-#pragma unroll
-  for (int i = 0; i < IM; ++i) sx[i] = a.scales + min(m0 + (wm * IM + i) * 16 + l, a.M - 1) * kb;
+  // scales of the tile's rows: waves 0 .. BM / 64 - 1 fetch 64 each; the wave's block of wscales
+  const __amdgpu_buffer_rsrc_t rss = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<float*>(a.scales + m0 * kb), (short)0, (int)min(a.M - m0, (int64_t)BM) * kb * 4, 0x00020000);
+  const uint32_t so = (uint32_t)(wave * 64 + lane) * (uint32_t)kb * 4u;
   const int64_t nw = n0 + wn * IN * 16;
   const float* sw = a.wscales + min(nw, a.N - 1) / 128 * kb;
+  auto issue = [&](int b) {
+    unsigned char* st = stage + (b & 1) * STAGE;
+    lx.issue(st, wave, b * KS, K);
+    lw.issue(st + BM * KS, wave, b * KS, K);
+    if (wave < BM / 64)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rss, (lds_ptr_t)(st + (BM + BN) * KS + wave * 256), 4, (int)so, 4 * b, 0, 0);
+  };
 
   f32x4v acc[IM][IN];
 #pragma unroll
   for (int i = 0; i < IM; ++i)
 #pragma unroll
     for (int j = 0; j < IN; ++j) acc[i][j] = f32x4v{0.f, 0.f, 0.f, 0.f};
-  // the next step's scales, multiplied only after the barrier that waits for them
-  float xn[IM], wn_;
-#pragma unroll
-  for (int i = 0; i < IM; ++i) xn[i] = sx[i][0];
-  wn_ = sw[0];
-  lx.issue(stage, wave, 0, K);
-  lw.issue(stage + BM * KS, wave, 0, K);
+  float swn = sw[0];
+  issue(0);
   for (int b = 0; b < kb; ++b) {
     // this wave's loads of the step are in LDS and its reads of the other
     // stage are done; the barrier makes both hold for all waves
     __builtin_amdgcn_s_waitcnt(0x0070);               // vmcnt(0) lgkmcnt(0)
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
-    float sc[IM];
-#pragma unroll
-    for (int i = 0; i < IM; ++i) sc[i] = xn[i] * wn_;
-    if (b + 1 < kb) {
-      unsigned char* next = stage + ((b + 1) & 1) * STAGE;
-      lx.issue(next, wave, (b + 1) * KS, K);
-      lw.issue(next + BM * KS, wave, (b + 1) * KS, K);
-    }
-    const int bn = min(b + 1, kb - 1);
-#pragma unroll
-    for (int i = 0; i < IM; ++i) xn[i] = sx[i][bn];
-    wn_ = sw[bn];
+    if (b + 1 < kb) issue(b + 1);
     const unsigned char* X = stage + (b & 1) * STAGE + wm * IM * 16 * KS;
     const unsigned char* Y = stage + (b & 1) * STAGE + BM * KS + wn * IN * 16 * KS;
+    const float* S = reinterpret_cast<const float*>(stage + (b & 1) * STAGE + (BM + BN) * KS) + wm * IM * 16 + l;
+    float sc[IM];
+#pragma unroll
+    for (int i = 0; i < IM; ++i) sc[i] = S[16 * i] * swn;
+    swn = sw[min(b + 1, kb - 1)];
     i32x8 w[IN], x = tile_operand(X, l, h);
 #pragma unroll
     for (int j = 0; j < IN; ++j) w[j] = tile_operand(Y + j * 16 * KS, l, h);
@@ -219,7 +223,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_scaled_mm(ScaledArgs a) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[IM - 1][j][e] = fmaf(p[(IM - 1) & 1][j][e], sc[IM - 1], acc[IM - 1][j][e]);
     if constexpr (IOT == 1) {                         // that order, for the instruction scheduler
-      __builtin_amdgcn_sched_group_barrier(0x100, 2 * IN + 4, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 2 * IN + 4 + IM, 0);
 #pragma unroll
       for (int i = 0; i < IM; ++i) {
 #pragma unroll
@@ -342,7 +346,7 @@ __global__ __launch_bounds__(512) void k_scaled_mm_rows(ScaledArgs a) {
 template <int IOT, bool CM, int IM, int IN, int WM, int WN>
 hipError_t launch_tiles(const ScaledArgs& a, hipStream_t s) {
   constexpr int BM = 16 * IM * WM, BN = 16 * IN * WN;
-  constexpr size_t stages = 2 * (BM + BN) * KS, out = (size_t)WM * WN * 16 * (16 * (CM ? IM : IN) + 4) * 4;
+  constexpr size_t stages = 2 * ((BM + BN) * KS + BM * 4), out = (size_t)WM * WN * 16 * (16 * (CM ? IM : IN) + 4) * 4;
   const int64_t tiles = ((a.M + BM - 1) / BM) * ((a.N + BN - 1) / BN);
   k_scaled_mm<IOT, CM, IM, IN, WM, WN>
       <<<dim3((unsigned)((tiles + 7) / 8 * 8)), 64 * WM * WN, stages > out ? stages : out, s>>>(a);
