@@ -31,26 +31,41 @@ __device__ __forceinline__ float conv_at(const ConvArgs& a, int64_t r, int64_t t
   return a.state && i >= 0 ? ld1<IOT>(a.state, r * (a.T - 1) + i) : 0.f;
 }
 
+template <int IOT>
+__device__ __forceinline__ void ld4(const void* p, int64_t i, float (&v)[4]) {
+  if constexpr (IOT == 0) {
+    const f32x4v w = *reinterpret_cast<const f32x4_e4*>(static_cast<const float*>(p) + i);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = w[e];
+  } else {
+    typedef uint32_t u2 __attribute__((ext_vector_type(2), aligned(2)));
+    const u2 w = *reinterpret_cast<const u2*>(static_cast<const uint16_t*>(p) + i);
+    v[0] = __uint_as_float(w.x << 16);
+    v[1] = __uint_as_float(w.x & 0xffff0000u);
+    v[2] = __uint_as_float(w.y << 16);
+    v[3] = __uint_as_float(w.y & 0xffff0000u);
+  }
+}
+
 // v[0..n) = inputs t .. t+n of row r (n a multiple of 4, t possibly negative
 // or its end behind len; zeros there).
 template <int IOT, int N>
 __device__ __forceinline__ void conv_window(const ConvArgs& a, int64_t r, int t, int len, float (&v)[N]) {
   if (t >= 0 && t + N <= len) {
     const int64_t i = r * a.L + t;
+    // where N is no multiple of 8, the odd four values come first
+    if constexpr (N % 8) {
+      float o[4];
+      ld4<IOT>(a.x, i, o);
 #pragma unroll
-    for (int k = 0; k < N; k += 4) {
-      if constexpr (IOT == 0) {
-        const f32x4v w = *reinterpret_cast<const f32x4_e4*>(static_cast<const float*>(a.x) + i + k);
+      for (int e = 0; e < 4; ++e) v[e] = o[e];
+    }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[k + e] = w[e];
-      } else {
-        typedef uint32_t u2 __attribute__((ext_vector_type(2), aligned(2)));
-        const u2 w = *reinterpret_cast<const u2*>(static_cast<const uint16_t*>(a.x) + i + k);
-        v[k] = __uint_as_float(w.x << 16);
-        v[k + 1] = __uint_as_float(w.x & 0xffff0000u);
-        v[k + 2] = __uint_as_float(w.y << 16);
-        v[k + 3] = __uint_as_float(w.y & 0xffff0000u);
-      }
+    for (int k = N % 8; k < N; k += 8) {
+      float o[8];
+      widen8<IOT>(ld8<IOT>(a.x, i + k), o);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[k + e] = o[e];
     }
   } else {
 #pragma unroll
@@ -121,9 +136,9 @@ __global__ __launch_bounds__(256) void k_conv_step(ConvArgs a) {
 //   gx[t] = sum_j w[j] gp[t+j],  gw[j] = sum_t gp[t] x[t-j],  gbias = sum_t gp[t],
 // and the carried inputs' gradients are gx at negative t; a gradient of the
 // state that the call left behind adds to the last T-1 inputs'.  p is
-// computed again, for a lane's 8 steps and the TT-1 behind them.  Sums over
-// time: a workgroup covers kConvSpan steps of a row and leaves one partial
-// for each tap, which k_conv_sum adds up in a fixed order.
+// computed again, for a lane's 8 steps and the TT-1 behind them.  A workgroup
+// sums over its sequences and steps in registers and leaves one partial for
+// each tap, which k_conv_sum adds up in a fixed order.
 template <int IOT, int TT>
 __device__ __forceinline__ void conv_gp(const ConvArgs& a, int64_t r, int t, int len, const float (&w)[TT], float bias,
                                         float (&x)[2 * TT + 8], float (&gp)[TT + 8]) {
@@ -140,8 +155,10 @@ __device__ __forceinline__ void conv_gp(const ConvArgs& a, int64_t r, int t, int
 #pragma unroll
         for (int k = 0; k < 8; ++k) gp[e + k] = v[k];
       } else {
+        float v[4];
+        ld4<IOT>(a.gy, r * a.L + t + e, v);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) gp[e + k] = ld1<IOT>(a.gy, r * a.L + t + e + k);
+        for (int k = 0; k < 4; ++k) gp[e + k] = v[k];
       }
     }
   } else {
@@ -162,106 +179,90 @@ __device__ __forceinline__ void conv_gp(const ConvArgs& a, int64_t r, int t, int
 }
 
 template <int IOT, int TT>
-__global__ __launch_bounds__(256) void k_conv_bwd(ConvArgs a, int per, int lper, int blocks) {
+__global__ __launch_bounds__(256) void k_conv_bwd(ConvArgs a, ConvBackwardGrid g) {
   __shared__ float part[4][TT + 1];
-  const int tid = threadIdx.x;
-  const int64_t rb = blockIdx.x / blocks;
-  const int xb = (int)(blockIdx.x - rb * blocks);
-  const int64_t rows = (int64_t)a.B * a.D, r = rb * (256 >> lper) + (tid >> lper);
-  const bool live = r < rows;
-  const int64_t rr = live ? r : rows - 1;
-  const int64_t b = rr / a.D;
-  const int d = (int)(rr - b * a.D), len = live ? conv_length(a, b) : 0, S = a.T - 1;
+  const int tid = threadIdx.x, per = g.per, at_once = 256 >> g.lper, S = a.T - 1;
+  const int d = (int)(blockIdx.x % a.D);
+  const int64_t id = blockIdx.x / a.D, grp = id / g.blocks, xb = id - grp * g.blocks;
   float w[TT], sum[TT + 1];
   conv_taps<TT>(a, d, w);
   const float bias = a.bias ? a.bias[d] : 0.f;
 #pragma unroll
   for (int j = 0; j <= TT; ++j) sum[j] = 0.f;
-  const int64_t t_end = min(a.L, (xb + 1) * kConvSpan);
-  for (int64_t t = xb * kConvSpan + 8 * (tid & (per - 1)); t < t_end && live; t += 8 * per) {
-    float gx[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (t < len) {
-      float x[2 * TT + 8], gp[TT + 8];
-      conv_gp<IOT, TT>(a, r, (int)t, len, w, bias, x, gp);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-#pragma unroll
-        for (int j = 0; j < TT; ++j) gx[e] = fmaf(w[j], gp[e + j], gx[e]);
-        sum[TT] += gp[e];
-#pragma unroll
-        for (int j = 0; j < TT; ++j) sum[j] = fmaf(gp[e], x[TT + e - j], sum[j]);
-      }
-      if (a.gstate_out) {
+  const int64_t t_end = min(a.L, (xb + 1) * kConvSpan), b_end = min((int64_t)a.B, (grp + 1) * g.seqs);
+  for (int64_t b = grp * g.seqs + (tid >> g.lper); b < b_end; b += at_once) {
+    const int64_t r = b * a.D + d;
+    const int len = conv_length(a, b);
+    for (int64_t t = xb * kConvSpan + 8 * (tid & (per - 1)); t < t_end; t += 8 * per) {
+      float gx[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (t < len) {
+        float x[2 * TT + 8], gp[TT + 8];
+        conv_gp<IOT, TT>(a, r, (int)t, len, w, bias, x, gp);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const int64_t i = t + e - (len - S);
-          if (i >= 0 && i < S) gx[e] += ld1<IOT>(a.gstate_out, r * S + i);
-        }
-      }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) gx[e] = t + e < len ? gx[e] : 0.f;
-    }
-    st8n<IOT>(a.gx, r * a.L + t, gx, (int)min(a.L - t, (int64_t)8));
-  }
-  // the carried inputs: one thread to a row walks over its T-1 values
-  if (a.gstate && live && xb == 0 && (tid & (per - 1)) == 0) {
-    for (int i = 0; i < S; ++i) {
-      const int t = i - S;                                // gx[t] = sum_j w[j] gp[t+j], t + j in [0, len)
-      float v = 0.f;
-      for (int j = -t; j <= S && t + j < len; ++j) {
-        const int s = t + j;
-        float gp = ld1<IOT>(a.gy, r * a.L + s);
-        if (a.silu) {
-          float p = bias;
-          for (int k = 0; k <= S; ++k) p = fmaf(a.w[(int64_t)d * a.T + k], conv_at<IOT>(a, r, s - k), p);
-          const float sg = sigmoid_f(p);
-          gp *= sg * fmaf(p, 1.f - sg, 1.f);
+          for (int j = 0; j < TT; ++j) gx[e] = fmaf(w[j], gp[e + j], gx[e]);
+          sum[TT] += gp[e];
+#pragma unroll
+          for (int j = 0; j < TT; ++j) sum[j] = fmaf(gp[e], x[TT + e - j], sum[j]);
         }
-        v = fmaf(a.w[(int64_t)d * a.T + j], gp, v);
+        if (a.gstate_out && t + 8 > len - S) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int64_t i = t + e - (len - S);
+            if (i >= 0 && i < S) gx[e] += ld1<IOT>(a.gstate_out, r * S + i);
+          }
+        }
+        if (t + 8 > len) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) gx[e] = t + e < len ? gx[e] : 0.f;
+        }
       }
-      // the state left behind still holds this carried input when len < T-1
-      if (a.gstate_out && i >= len) v += ld1<IOT>(a.gstate_out, r * S + i - len);
-      st1<IOT>(a.gstate, r * S + i, v);
+      st8n<IOT>(a.gx, r * a.L + t, gx, (int)min(a.L - t, (int64_t)8));
+    }
+    // the carried inputs: one thread to a row walks over its T-1 values
+    if (a.gstate && xb == 0 && (tid & (per - 1)) == 0) {
+      for (int i = 0; i < S; ++i) {
+        const int t = i - S;                              // gx[t] = sum_j w[j] gp[t+j], t + j in [0, len)
+        float v = 0.f;
+        for (int j = -t; j <= S && t + j < len; ++j) {
+          const int s = t + j;
+          float gp = ld1<IOT>(a.gy, r * a.L + s);
+          if (a.silu) {
+            float p = bias;
+            for (int k = 0; k <= S; ++k) p = fmaf(a.w[(int64_t)d * a.T + k], conv_at<IOT>(a, r, s - k), p);
+            const float sg = sigmoid_f(p);
+            gp *= sg * fmaf(p, 1.f - sg, 1.f);
+          }
+          v = fmaf(a.w[(int64_t)d * a.T + j], gp, v);
+        }
+        // the state left behind still holds this carried input when len < T-1
+        if (a.gstate_out && i >= len) v += ld1<IOT>(a.gstate_out, r * S + i - len);
+        st1<IOT>(a.gstate, r * S + i, v);
+      }
     }
   }
-  // the row's sums over its threads: within a wave, then over the waves
+  // the workgroup's sums: within a wave, then over the waves
 #pragma unroll
   for (int j = 0; j <= TT; ++j) {
-    for (int o = min(per, 64) >> 1; o > 0; o >>= 1) sum[j] += __shfl_xor(sum[j], o);
+    float v = row_sum(sum[j]);
+    v += __shfl_xor(v, 16);
+    v += __shfl_xor(v, 32);
+    if ((tid & 63) == 0) part[tid >> 6][j] = v;
   }
-  if (per > 64) {
-    if ((tid & 63) == 0) {
-#pragma unroll
-      for (int j = 0; j <= TT; ++j) part[tid >> 6][j] = sum[j];
-    }
-    __syncthreads();
-    if ((tid & (per - 1)) == 0) {
-#pragma unroll
-      for (int j = 0; j <= TT; ++j)
-        for (int k = 1; k < per / 64; ++k) sum[j] += part[(tid >> 6) + k][j];
-    }
-  }
-  if (live && (tid & (per - 1)) == 0) {
-    float* o = a.partial + ((b * blocks + xb) * a.D + d) * (a.T + 1);
-#pragma unroll
-    for (int j = 0; j < TT; ++j)
-      if (j < a.T) o[j] = sum[j];
-    o[a.T] = sum[TT];
+  __syncthreads();
+  if (tid <= TT) {
+    const float v = (part[0][tid] + part[1][tid]) + (part[2][tid] + part[3][tid]);
+    const int j = tid < TT ? tid : a.T;
+    if (tid == TT || tid < a.T) a.partial[(id * a.D + d) * (a.T + 1) + j] = v;
   }
 }
 
-__global__ __launch_bounds__(256) void k_conv_sum(ConvArgs a, int64_t parts) {
-  __shared__ float s[8][33];
-  const int c = threadIdx.x & 31, k = threadIdx.x >> 5;
-  const int64_t W = (int64_t)a.D * (a.T + 1), i = blockIdx.x * (int64_t)32 + c;
-  float v = 0.f;
-  if (i < W)
-    for (int64_t p = k; p < parts; p += 8) v += a.partial[p * W + i];
-  s[k][c] = v;
-  __syncthreads();
-  if (k == 0 && i < W) {
-#pragma unroll
-    for (int j = 1; j < 8; ++j) v += s[j][c];
+__global__ __launch_bounds__(SUM_THREADS) void k_conv_sum(ConvArgs a, int64_t parts) {
+  __shared__ float lds[32][33];
+  const int64_t W = (int64_t)a.D * (a.T + 1), i = blockIdx.x * (int64_t)32 + (threadIdx.x & 31);
+  const float v = column_sum(i < W ? a.partial + i : nullptr, parts, W, lds);
+  if (threadIdx.x < 32 && i < W) {
     const int64_t d = i / (a.T + 1);
     const int j = (int)(i - d * (a.T + 1));
     if (j < a.T) a.gw[d * a.T + j] = v;
@@ -283,9 +284,10 @@ void conv_step_tt(const ConvArgs& a, hipStream_t s) {
 }
 
 template <int TT>
-void conv_backward_tt(const ConvArgs& a, const ConvGrid& g, hipStream_t s) {
-  if (a.io) k_conv_bwd<1, TT><<<(unsigned)g.groups, 256, 0, s>>>(a, g.per, g.lper, (int)g.blocks);
-  else k_conv_bwd<0, TT><<<(unsigned)g.groups, 256, 0, s>>>(a, g.per, g.lper, (int)g.blocks);
+void conv_backward_tt(const ConvArgs& a, const ConvBackwardGrid& g, hipStream_t s) {
+  const unsigned n = (unsigned)(g.parts * a.D);
+  if (a.io) k_conv_bwd<1, TT><<<n, 256, 0, s>>>(a, g);
+  else k_conv_bwd<0, TT><<<n, 256, 0, s>>>(a, g);
 }
 
 }  // namespace
@@ -306,14 +308,14 @@ hipError_t short_conv_step(const ConvArgs& a, hipStream_t s) {
 }
 
 hipError_t short_conv_backward(const ConvArgs& a, hipStream_t s) {
-  const ConvGrid g = conv_grid(a.B, a.D, a.L, kConvSpan);
+  const ConvBackwardGrid g = conv_backward_grid(a.B, a.D, a.L);
   if (a.T <= 4) conv_backward_tt<4>(a, g, s);
   else if (a.T <= 8) conv_backward_tt<8>(a, g, s);
   else conv_backward_tt<16>(a, g, s);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int64_t W = (int64_t)a.D * (a.T + 1);
-  k_conv_sum<<<(unsigned)((W + 31) / 32), 256, 0, s>>>(a, conv_backward_parts(a.B, a.L));
+  k_conv_sum<<<(unsigned)((W + 31) / 32), SUM_THREADS, 0, s>>>(a, g.parts);
   return hipGetLastError();
 }
 

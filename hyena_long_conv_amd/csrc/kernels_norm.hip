@@ -212,7 +212,7 @@ __global__ __launch_bounds__(256) void k_quantize_tiles(NormArgs a) {
 //
 //   gx = r (weight gy - s r mean(s r weight gy)) + gs,  gweight = sum_rows gy s r.
 // A workgroup walks over rows; a thread keeps its columns' share of gweight
-// in registers and leaves one partial, which k_norm_sum adds up.
+// in registers, and the workgroup leaves one partial, which k_norm_sum adds up.
 template <int IOT, int LANES, int V>
 __global__ __launch_bounds__(NORM_THREADS) void k_norm_bwd(NormArgs a) {
   __shared__ float lds[NORM_THREADS / 64];
@@ -260,11 +260,28 @@ __global__ __launch_bounds__(NORM_THREADS) void k_norm_bwd(NormArgs a) {
       if (n > 0) st8n<IOT>(a.gx, base + 8 * (int64_t)w, o, n);
     }
   }
-  const int64_t slot = blockIdx.x * (int64_t)RPW + threadIdx.x / LANES;
+  if constexpr (RPW > 1) {                            // the workgroup's rows, in order
+    __shared__ float sum[RPW - 1][V * LANES * 8];
+    const int g = threadIdx.x / LANES;
+    if (g > 0) {
+#pragma unroll
+      for (int k = 0; k < V; ++k)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[g - 1][(8 * k + e) * LANES + lane] = gw[k][e];
+    }
+    __syncthreads();
+    if (g > 0) return;
+#pragma unroll
+    for (int j = 0; j < RPW - 1; ++j)
+#pragma unroll
+      for (int k = 0; k < V; ++k)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) gw[k][e] += sum[j][(8 * k + e) * LANES + lane];
+  }
 #pragma unroll
   for (int k = 0; k < V; ++k) {
     const int w = lane + LANES * k;
-    if (8 * w < D) st8n<0>(a.partial, slot * D + 8 * (int64_t)w, gw[k], D - 8 * w);
+    if (8 * w < D) st8n<0>(a.partial, blockIdx.x * (int64_t)D + 8 * (int64_t)w, gw[k], D - 8 * w);
   }
 }
 
@@ -313,44 +330,28 @@ __global__ __launch_bounds__(NORM_THREADS) void k_norm_bwd_long(NormArgs a, int6
     }
     fresh = false;
   }
-  if (fresh) {                                       // more partials than rows
-    for (int w = tid; w < words; w += NORM_THREADS) {
-      const float gw[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      st8n<0>(part, 8 * (int64_t)w, gw, D - 8 * w);
-    }
-  }
 }
 
-__global__ __launch_bounds__(256) void k_norm_sum(NormArgs a, int64_t parts) {
-  __shared__ float s[8][33];
-  const int c = threadIdx.x & 31, k = threadIdx.x >> 5;
-  const int64_t i = blockIdx.x * (int64_t)32 + c;
-  float v = 0.f;
-  if (i < a.D)
-    for (int64_t p = k; p < parts; p += 8) v += a.partial[p * a.D + i];
-  s[k][c] = v;
-  __syncthreads();
-  if (k == 0 && i < a.D) {
-#pragma unroll
-    for (int j = 1; j < 8; ++j) v += s[j][c];
-    a.gw[i] = v;
-  }
+__global__ __launch_bounds__(SUM_THREADS) void k_norm_sum(NormArgs a, int64_t parts) {
+  __shared__ float lds[32][33];
+  const int64_t i = blockIdx.x * (int64_t)32 + (threadIdx.x & 31);
+  const float v = column_sum(i < a.D ? a.partial + i : nullptr, parts, a.D, lds);
+  if (threadIdx.x < 32 && i < a.D) a.gw[i] = v;
 }
 
 template <int IOT>
 hipError_t launch_norm_backward(const NormArgs& a, hipStream_t s) {
-  // norm_backward_parts(rows) partials: one for each row slot of the grid
-  const int64_t parts = norm_backward_parts(a.rows);
-  const auto grid = [&](int lanes) { return dim3((unsigned)((parts * lanes + NORM_THREADS - 1) / NORM_THREADS)); };
-  if (a.D <= 512) k_norm_bwd<IOT, 64, 1><<<grid(64), NORM_THREADS, 0, s>>>(a);
-  else if (a.D <= 1024) k_norm_bwd<IOT, 64, 2><<<grid(64), NORM_THREADS, 0, s>>>(a);
-  else if (a.D <= 2048) k_norm_bwd<IOT, 256, 1><<<grid(256), NORM_THREADS, 0, s>>>(a);
-  else if (a.D <= 4096) k_norm_bwd<IOT, 256, 2><<<grid(256), NORM_THREADS, 0, s>>>(a);
-  else if (a.D <= 8192) k_norm_bwd<IOT, 256, 4><<<grid(256), NORM_THREADS, 0, s>>>(a);
-  else k_norm_bwd_long<IOT><<<dim3((unsigned)parts), NORM_THREADS, 0, s>>>(a, parts);
+  const int64_t parts = norm_backward_parts(a.rows, a.D);   // a workgroup leaves one partial
+  const dim3 grid((unsigned)parts);
+  if (a.D <= 512) k_norm_bwd<IOT, 64, 1><<<grid, NORM_THREADS, 0, s>>>(a);
+  else if (a.D <= 1024) k_norm_bwd<IOT, 64, 2><<<grid, NORM_THREADS, 0, s>>>(a);
+  else if (a.D <= 2048) k_norm_bwd<IOT, 256, 1><<<grid, NORM_THREADS, 0, s>>>(a);
+  else if (a.D <= 4096) k_norm_bwd<IOT, 256, 2><<<grid, NORM_THREADS, 0, s>>>(a);
+  else if (a.D <= 8192) k_norm_bwd<IOT, 256, 4><<<grid, NORM_THREADS, 0, s>>>(a);
+  else k_norm_bwd_long<IOT><<<grid, NORM_THREADS, 0, s>>>(a, parts);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  k_norm_sum<<<(unsigned)((a.D + 31) / 32), 256, 0, s>>>(a, parts);
+  k_norm_sum<<<(unsigned)((a.D + 31) / 32), SUM_THREADS, 0, s>>>(a, parts);
   return hipGetLastError();
 }
 

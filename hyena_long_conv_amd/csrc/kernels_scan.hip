@@ -626,31 +626,20 @@ __global__ __launch_bounds__(256) void k_scan_bwd_sum_bc(ScanArgs a) {
   }
 }
 
-// gA, gskip and gdelta_bias from the chunks' parts: a workgroup sums 32
-// columns, 8 threads to a column.
-__global__ __launch_bounds__(256) void k_scan_bwd_sum_t(ScanArgs a) {
-  __shared__ float s[8][33];
-  const int c = threadIdx.x & 31, k = threadIdx.x >> 5;
+// gA, gskip and gdelta_bias from the chunks' parts.
+__global__ __launch_bounds__(SUM_THREADS) void k_scan_bwd_sum_t(ScanArgs a) {
+  __shared__ float lds[32][33];
   const int64_t DN = (int64_t)a.D * a.N, rows = (int64_t)a.B * a.chunks;
-  const int64_t i = blockIdx.x * (int64_t)32 + c;    // columns: gA's D*N, then gskip's D, then gdelta_bias's D
+  // columns: gA's D*N, then gskip's D, then gdelta_bias's D
+  const int64_t i = blockIdx.x * (int64_t)32 + (threadIdx.x & 31);
   const float* src = nullptr;
-  int64_t stride = 0;
+  int64_t stride = a.D;
   float* dst = nullptr;
   if (i < DN) { src = a.hc + i; stride = DN; dst = a.gA + i; }
-  else if (i < DN + a.D) { src = a.ps + (i - DN); stride = a.D; dst = a.gskip ? a.gskip + (i - DN) : nullptr; }
-  else if (i < DN + 2 * a.D) { src = a.pb + (i - DN - a.D); stride = a.D; dst = a.gdbias ? a.gdbias + (i - DN - a.D) : nullptr; }
-  float v = 0.f;
-  if (dst) {
-#pragma unroll 4
-    for (int64_t r = k; r < rows; r += 8) v += src[r * stride];
-  }
-  s[k][c] = v;
-  __syncthreads();
-  if (k == 0 && dst) {
-#pragma unroll
-    for (int j = 1; j < 8; ++j) v += s[j][c];
-    *dst = v;
-  }
+  else if (i < DN + a.D && a.gskip) { src = a.ps + (i - DN); dst = a.gskip + (i - DN); }
+  else if (i >= DN + a.D && i < DN + 2 * a.D && a.gdbias) { src = a.pb + (i - DN - a.D); dst = a.gdbias + (i - DN - a.D); }
+  const float v = column_sum(src, rows, stride, lds);
+  if (threadIdx.x < 32 && dst) *dst = v;
 }
 
 template <int IOT>
@@ -664,7 +653,7 @@ hipError_t launch_scan_backward(const ScanArgs& a, hipStream_t s) {
     const int64_t n = (int64_t)2 * a.B * a.G * a.N * a.L;
     k_scan_bwd_sum_bc<IOT><<<dim3((unsigned)min((n + 255) / 256, (int64_t)8192)), 256, 0, s>>>(a);
   }
-  k_scan_bwd_sum_t<<<dim3((unsigned)(((int64_t)a.D * (a.N + 2) + 31) / 32)), 256, 0, s>>>(a);
+  k_scan_bwd_sum_t<<<dim3((unsigned)(((int64_t)a.D * (a.N + 2) + 31) / 32)), SUM_THREADS, 0, s>>>(a);
   return hipGetLastError();
 }
 

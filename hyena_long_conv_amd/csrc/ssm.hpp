@@ -24,15 +24,10 @@ struct ConvArgs {
   float* gw;               // [D][T]
   float* gbias;            // [D] or nullptr
   void* gstate;            // or nullptr
-  float* partial;          // workspace, [conv_backward_parts][D][T+1]
+  float* partial;          // workspace, [parts][D][T+1]
   int B, D, T, silu, io;
   int64_t L;
 };
-
-// Samples of one row that a workgroup of the backward covers: its sums over
-// time leave one partial for each.
-constexpr int64_t kConvSpan = 16384;
-inline int64_t conv_backward_parts(int64_t B, int64_t L) { return B * ((L + kConvSpan - 1) / kConvSpan); }
 
 // Rows share a workgroup of 256 threads when they are short: `per` threads
 // (a power of two, 8 steps each) to a row, or `blocks` workgroups of `span`
@@ -51,6 +46,30 @@ inline ConvGrid conv_grid(int64_t B, int64_t D, int64_t L, int64_t span) {
   g.blocks = (L + span - 1) / span;
   const int64_t rows = 256 >> g.lper;
   g.groups = (B * D + rows - 1) / rows * g.blocks;
+  return g;
+}
+
+// Backward: a workgroup keeps to one channel and walks over `seqs` sequences
+// (256 / per of them at a time) and kConvSpan steps of each, so that its sums
+// over batch and time leave one partial.  Sequences are spread over
+// workgroups until there are about eight to a compute unit.
+constexpr int64_t kConvSpan = 16384;
+struct ConvBackwardGrid {
+  int per, lper;
+  int64_t blocks, groups, seqs, parts;   // blocks along time, groups of sequences
+};
+inline ConvBackwardGrid conv_backward_grid(int64_t B, int64_t D, int64_t L) {
+  const ConvGrid c = conv_grid(B, D, L, kConvStep);
+  ConvBackwardGrid g;
+  g.per = c.per;
+  g.lper = c.lper;
+  g.blocks = (L + kConvSpan - 1) / kConvSpan;
+  const int64_t at_once = 256 >> c.lper, most = (B + at_once - 1) / at_once;
+  int64_t n = (2048 + D * g.blocks - 1) / (D * g.blocks);
+  if (n > most) n = most;
+  g.seqs = (most + n - 1) / n * at_once;
+  g.groups = (B + g.seqs - 1) / g.seqs;
+  g.parts = g.blocks * g.groups;
   return g;
 }
 
@@ -155,8 +174,12 @@ struct NormArgs {
   int block_rows;
 };
 
-// Row slots of the backward's grid, a multiple of the 4 rows a workgroup may hold.
-inline int64_t norm_backward_parts(int64_t rows) { return rows < 4096 ? (rows + 15) / 16 * 4 : 1024; }
+// Workgroups of the backward, which leave a partial each: they take 4 rows at
+// a time up to D = 1024, one beyond.
+inline int64_t norm_backward_parts(int64_t rows, int64_t D) {
+  const int64_t n = D <= 1024 ? (rows + 3) / 4 : rows;
+  return n < 1024 ? n : 1024;
+}
 
 hipError_t rms_norm(const NormArgs& a, hipStream_t s);
 hipError_t rms_norm_backward(const NormArgs& a, hipStream_t s);

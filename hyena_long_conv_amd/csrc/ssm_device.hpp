@@ -139,6 +139,29 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
+// A workgroup of 1024 threads sums 32 columns of `parts` rows of partials in a
+// fixed order: 32 threads to a column, whose sum thread (slice 0) returns.
+// `col` is the column's first value (nullptr: none), `stride` a row's length.
+constexpr int SUM_THREADS = 1024;
+__device__ __forceinline__ float column_sum(const float* col, int64_t parts, int64_t stride, float (*lds)[33]) {
+  const int c = threadIdx.x & 31, k = threadIdx.x >> 5;
+  float v = 0.f;
+  if (col) {
+    int64_t p = k;
+    for (; p + 96 < parts; p += 128) {               // four loads in flight
+      const float a = col[p * stride], b = col[(p + 32) * stride];
+      const float d = col[(p + 64) * stride], e = col[(p + 96) * stride];
+      v += (a + b) + (d + e);
+    }
+    for (; p < parts; p += 32) v += col[p * stride];
+  }
+  lds[k][c] = v;
+  __syncthreads();
+  if (k == 0)
+    for (int j = 1; j < 32; ++j) v += lds[j][c];
+  return v;
+}
+
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }   // 1 ulp
 __device__ __forceinline__ float rcp_fast(float x) { return __builtin_amdgcn_rcpf(x); }     // 1 ulp
 
