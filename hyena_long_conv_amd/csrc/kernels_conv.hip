@@ -31,45 +31,35 @@ __device__ __forceinline__ float conv_at(const ConvArgs& a, int64_t r, int64_t t
   return a.state && i >= 0 ? ld1<IOT>(a.state, r * (a.T - 1) + i) : 0.f;
 }
 
+// v = inputs t .. t+7 of row r (t a multiple of 8, possibly negative; zeros from len on).
 template <int IOT>
-__device__ __forceinline__ void ld4(const void* p, int64_t i, float (&v)[4]) {
-  if constexpr (IOT == 0) {
-    const f32x4v w = *reinterpret_cast<const f32x4_e4*>(static_cast<const float*>(p) + i);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = w[e];
+__device__ __forceinline__ void conv_word(const ConvArgs& a, int64_t r, int t, int len, float (&v)[8]) {
+  if (t >= 0) {
+    widen8<IOT>(ld8n<IOT>(a.x, r * a.L + t, len - t, (int64_t)a.B * a.D * a.L), v);
   } else {
-    typedef uint32_t u2 __attribute__((ext_vector_type(2), aligned(2)));
-    const u2 w = *reinterpret_cast<const u2*>(static_cast<const uint16_t*>(p) + i);
-    v[0] = __uint_as_float(w.x << 16);
-    v[1] = __uint_as_float(w.x & 0xffff0000u);
-    v[2] = __uint_as_float(w.y << 16);
-    v[3] = __uint_as_float(w.y & 0xffff0000u);
+    const int S = a.T - 1, i = t + S;                 // the state's place of v[0]
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = a.state && i + e >= 0 ? ld1<IOT>(a.state, r * S + i + e) : 0.f;
   }
 }
 
-// v[0..n) = inputs t .. t+n of row r (n a multiple of 4, t possibly negative
-// or its end behind len; zeros there).
-template <int IOT, int N>
-__device__ __forceinline__ void conv_window(const ConvArgs& a, int64_t r, int t, int len, float (&v)[N]) {
-  if (t >= 0 && t + N <= len) {
-    const int64_t i = r * a.L + t;
-    // where N is no multiple of 8, the odd four values come first
-    if constexpr (N % 8) {
-      float o[4];
-      ld4<IOT>(a.x, i, o);
+// x = the H inputs before t, then those of t .. t + N - 1 (H, N multiples of 4).
+template <int IOT, int H, int N>
+__device__ __forceinline__ void conv_window(const ConvArgs& a, int64_t r, int t, int len, float (&x)[H + N]) {
+  float v[8];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = o[e];
-    }
+  for (int k = 0; k < (H + 7) / 8; ++k) {
+    conv_word<IOT>(a, r, t - 8 * (k + 1), len, v);
 #pragma unroll
-    for (int k = N % 8; k < N; k += 8) {
-      float o[8];
-      widen8<IOT>(ld8<IOT>(a.x, i + k), o);
+    for (int e = 0; e < 8; ++e)
+      if (H - 8 * (k + 1) + e >= 0) x[H - 8 * (k + 1) + e] = v[e];
+  }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[k + e] = o[e];
-    }
-  } else {
+  for (int k = 0; k < (N + 7) / 8; ++k) {
+    conv_word<IOT>(a, r, t + 8 * k, len, v);
 #pragma unroll
-    for (int k = 0; k < N; ++k) v[k] = t + k < len ? conv_at<IOT>(a, r, t + k) : 0.f;
+    for (int e = 0; e < 8; ++e)
+      if (8 * k + e < N) x[H + 8 * k + e] = v[e];
   }
 }
 
@@ -96,7 +86,7 @@ __global__ __launch_bounds__(256) void k_conv(ConvArgs a, int per, int lper, int
   float x[TT + 8], w[TT], y[8];
   conv_taps<TT>(a, d, w);
   if (t < len) {
-    conv_window<IOT, TT + 8>(a, r, t - TT, len, x);
+    conv_window<IOT, TT, 8>(a, r, t, len, x);
     const float bias = a.bias ? a.bias[d] : 0.f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -142,29 +132,14 @@ __global__ __launch_bounds__(256) void k_conv_step(ConvArgs a) {
 template <int IOT, int TT>
 __device__ __forceinline__ void conv_gp(const ConvArgs& a, int64_t r, int t, int len, const float (&w)[TT], float bias,
                                         float (&x)[2 * TT + 8], float (&gp)[TT + 8]) {
-  // x: inputs t - TT .. t + TT + 8
-  conv_window<IOT, 2 * TT + 8>(a, r, t - TT, len, x);
+  conv_window<IOT, TT, TT + 8>(a, r, t, len, x);
 #pragma unroll
-  for (int e = 0; e < TT + 8; ++e) gp[e] = 0.f;
-  if (t >= 0 && t + TT + 8 <= len) {
+  for (int k = 0; k < (TT + 15) / 8; ++k) {
+    float v[8];
+    widen8<IOT>(ld8n<IOT>(a.gy, r * a.L + t + 8 * k, len - t - 8 * k, (int64_t)a.B * a.D * a.L), v);
 #pragma unroll
-    for (int e = 0; e < TT + 8; e += 8) {
-      if (e + 8 <= TT + 8) {
-        float v[8];
-        widen8<IOT>(ld8<IOT>(a.gy, r * a.L + t + e), v);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) gp[e + k] = v[k];
-      } else {
-        float v[4];
-        ld4<IOT>(a.gy, r * a.L + t + e, v);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) gp[e + k] = v[k];
-      }
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < TT + 8; ++e)
-      if (t + e >= 0 && t + e < len) gp[e] = ld1<IOT>(a.gy, r * a.L + t + e);
+    for (int e = 0; e < 8; ++e)
+      if (8 * k + e < TT + 8) gp[8 * k + e] = v[e];
   }
   if (a.silu) {
 #pragma unroll
@@ -173,7 +148,7 @@ __device__ __forceinline__ void conv_gp(const ConvArgs& a, int64_t r, int t, int
 #pragma unroll
       for (int j = 0; j < TT; ++j) p = fmaf(w[j], x[TT + e - j], p);
       const float s = sigmoid_f(p);
-      gp[e] = t + e >= 0 && t + e < len ? gp[e] * (s * fmaf(p, 1.f - s, 1.f)) : 0.f;
+      gp[e] *= s * fmaf(p, 1.f - s, 1.f);                // 0 from len on
     }
   }
 }

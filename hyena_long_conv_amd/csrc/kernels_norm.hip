@@ -95,13 +95,13 @@ __global__ __launch_bounds__(NORM_THREADS) void k_norm(NormArgs a) {
     const int n = live ? D - 8 * w : 0;
     const int64_t i = base + 8 * (int64_t)w;
     if (a.residual && !first) {
-      widen8<IOT>(ld8n<IOT>(a.s_out, i, n), o);
+      widen8<IOT>(ld8n<IOT>(a.s_out, i, n, a.rows * D), o);
       return;
     }
-    widen8<IOT>(ld8n<IOT>(a.x, i, n), o);
+    widen8<IOT>(ld8n<IOT>(a.x, i, n, a.rows * D), o);
     if (!a.residual) return;
     float r[8];
-    widen8<IOT>(ld8n<IOT>(a.residual, i, n), r);
+    widen8<IOT>(ld8n<IOT>(a.residual, i, n, a.rows * D), r);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       o[e] += r[e];
@@ -126,7 +126,7 @@ __global__ __launch_bounds__(NORM_THREADS) void k_norm(NormArgs a) {
       const int w = lane + LANES * (k + V * p), n = live ? D - 8 * w : 0;
       float wt[8], y[8];
       if (MORE) take(w, f[k], false);
-      widen8<0>(ld8n<0>(a.weight, 8 * (int64_t)w, D - 8 * w), wt);
+      widen8<0>(ld8n<0>(a.weight, 8 * (int64_t)w, D - 8 * w, D), wt);
       float top = 0.f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -170,7 +170,7 @@ __global__ __launch_bounds__(256) void k_quantize_rows(NormArgs a) {
   const int64_t row = live ? blk / kb : 0;
   const int c = (int)(live ? blk - row * kb : 0) * 128 + 8 * l, n = live ? a.D - c : 0;
   float y[8], top = 0.f, scale;
-  widen8<IOT>(ld8n<IOT>(a.x, row * a.D + c, n), y);
+  widen8<IOT>(ld8n<IOT>(a.x, row * a.D + c, n, a.rows * a.D), y);
 #pragma unroll
   for (int e = 0; e < 8; ++e) top = nan_max(fabsf(y[e]), top);
   const uint2 q = codes8(y, row_max(top), scale);
@@ -189,7 +189,7 @@ __global__ __launch_bounds__(256) void k_quantize_tiles(NormArgs a) {
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     const int64_t row = rb * 128 + 16 * k + rw;
-    widen8<IOT>(ld8n<IOT>(a.x, row * a.D + c, row < a.rows ? a.D - c : 0), y[k]);
+    widen8<IOT>(ld8n<IOT>(a.x, row * a.D + c, row < a.rows ? a.D - c : 0, a.rows * a.D), y[k]);
 #pragma unroll
     for (int e = 0; e < 8; ++e) top = nan_max(fabsf(y[k][e]), top);
   }
@@ -222,7 +222,7 @@ __global__ __launch_bounds__(NORM_THREADS) void k_norm_bwd(NormArgs a) {
 #pragma unroll
   for (int k = 0; k < V; ++k) {
     const int w = lane + LANES * k;
-    widen8<0>(ld8n<0>(a.weight, 8 * (int64_t)w, D - 8 * w), wt[k]);
+    widen8<0>(ld8n<0>(a.weight, 8 * (int64_t)w, D - 8 * w, D), wt[k]);
 #pragma unroll
     for (int e = 0; e < 8; ++e) gw[k][e] = 0.f;
   }
@@ -235,8 +235,8 @@ __global__ __launch_bounds__(NORM_THREADS) void k_norm_bwd(NormArgs a) {
 #pragma unroll
     for (int k = 0; k < V; ++k) {
       const int w = lane + LANES * k, n = live ? D - 8 * w : 0;
-      widen8<IOT>(ld8n<IOT>(a.x, base + 8 * (int64_t)w, n), f[k]);
-      widen8<IOT>(ld8n<IOT>(a.gy, base + 8 * (int64_t)w, n), g[k]);
+      widen8<IOT>(ld8n<IOT>(a.x, base + 8 * (int64_t)w, n, a.rows * D), f[k]);
+      widen8<IOT>(ld8n<IOT>(a.gy, base + 8 * (int64_t)w, n, a.rows * D), g[k]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         ss = fmaf(f[k][e], f[k][e], ss);
@@ -250,7 +250,7 @@ __global__ __launch_bounds__(NORM_THREADS) void k_norm_bwd(NormArgs a) {
     for (int k = 0; k < V; ++k) {
       const int w = lane + LANES * k, n = live ? D - 8 * w : 0;
       float o[8];
-      if (a.gs) widen8<IOT>(ld8n<IOT>(a.gs, base + 8 * (int64_t)w, n), o);
+      if (a.gs) widen8<IOT>(ld8n<IOT>(a.gs, base + 8 * (int64_t)w, n, a.rows * D), o);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float v = r * fmaf(g[k][e], wt[k][e], -m * f[k][e]);
@@ -299,9 +299,9 @@ __global__ __launch_bounds__(NORM_THREADS) void k_norm_bwd_long(NormArgs a, int6
     for (int w = tid; w < words; w += NORM_THREADS) {
       float f[8], g[8], wt[8];
       const int n = D - 8 * w;
-      widen8<IOT>(ld8n<IOT>(a.x, base + 8 * (int64_t)w, n), f);
-      widen8<IOT>(ld8n<IOT>(a.gy, base + 8 * (int64_t)w, n), g);
-      widen8<0>(ld8n<0>(a.weight, 8 * (int64_t)w, n), wt);
+      widen8<IOT>(ld8n<IOT>(a.x, base + 8 * (int64_t)w, n, a.rows * D), f);
+      widen8<IOT>(ld8n<IOT>(a.gy, base + 8 * (int64_t)w, n, a.rows * D), g);
+      widen8<0>(ld8n<0>(a.weight, 8 * (int64_t)w, n, D), wt);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         ss = fmaf(f[e], f[e], ss);
@@ -314,11 +314,11 @@ __global__ __launch_bounds__(NORM_THREADS) void k_norm_bwd_long(NormArgs a, int6
     for (int w = tid; w < words; w += NORM_THREADS) {
       float f[8], g[8], wt[8], o[8], gw[8];
       const int n = D - 8 * w;
-      widen8<IOT>(ld8n<IOT>(a.x, base + 8 * (int64_t)w, n), f);
-      widen8<IOT>(ld8n<IOT>(a.gy, base + 8 * (int64_t)w, n), g);
-      widen8<0>(ld8n<0>(a.weight, 8 * (int64_t)w, n), wt);
-      widen8<0>(fresh ? zero8<0>() : ld8n<0>(part, 8 * (int64_t)w, n), gw);   // this thread's own words
-      if (a.gs) widen8<IOT>(ld8n<IOT>(a.gs, base + 8 * (int64_t)w, n), o);
+      widen8<IOT>(ld8n<IOT>(a.x, base + 8 * (int64_t)w, n, a.rows * D), f);
+      widen8<IOT>(ld8n<IOT>(a.gy, base + 8 * (int64_t)w, n, a.rows * D), g);
+      widen8<0>(ld8n<0>(a.weight, 8 * (int64_t)w, n, D), wt);
+      widen8<0>(fresh ? zero8<0>() : ld8n<0>(part, 8 * (int64_t)w, n, D), gw);   // this thread's own words
+      if (a.gs) widen8<IOT>(ld8n<IOT>(a.gs, base + 8 * (int64_t)w, n, a.rows * D), o);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float v = r * fmaf(g[e], wt[e], -m * f[e]);

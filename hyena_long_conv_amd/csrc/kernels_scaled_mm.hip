@@ -255,7 +255,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_scaled_mm(ScaledArgs a) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = ep[r * LD + c + e];
         if (a.bias) {
-          widen8<0>(ld8n<0>(a.bias, n, (int)min(a.N - n, (int64_t)8)), bv);
+          widen8<0>(ld8n<0>(a.bias, n, (int)min(a.N - n, (int64_t)8), a.N), bv);
 #pragma unroll
           for (int e = 0; e < 8; ++e) v[e] += bv[e];
         }

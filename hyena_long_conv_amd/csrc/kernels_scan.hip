@@ -106,6 +106,7 @@ __global__ __launch_bounds__(SCAN_THREADS) void k_scan(ScanArgs a) {
   const int len = seq_length(a, b);
   const int64_t base = ((int64_t)b * a.D + d) * L;
   const int64_t bc = ((int64_t)b * a.G + g) * N * L;
+  const int64_t total = (int64_t)a.B * a.D * L, bc_total = (int64_t)a.B * a.G * N * L;
   const int t_begin = (int)(seg * a.seg);
   const int t_end = (int)min(L, (int64_t)t_begin + a.seg);
 
@@ -144,14 +145,14 @@ __global__ __launch_bounds__(SCAN_THREADS) void k_scan(ScanArgs a) {
       rbc[k] = zero8<IOT>();
       if (i < words) {
         const bool isC = n >= N;
-        rbc[k] = ld8n<IOT>(isC ? a.Cm : a.Bm, bc + (int64_t)(isC ? n - N : n) * L + t0 + 8 * v, len - t0 - 8 * v);
+        rbc[k] = ld8n<IOT>(isC ? a.Cm : a.Bm, bc + (int64_t)(isC ? n - N : n) * L + t0 + 8 * v, len - t0 - 8 * v, bc_total);
       }
     }
     const int t = t0 + 8 * l, m = live ? len - t : 0;
-    ru = ld8n<IOT>(a.u, base + t, m);
-    rd = ld8n<IOT>(a.delta, base + t, m);
+    ru = ld8n<IOT>(a.u, base + t, m, total);
+    rd = ld8n<IOT>(a.delta, base + t, m, total);
     if constexpr (!END)
-      if (a.z) rz = ld8n<IOT>(a.z, base + t, m);
+      if (a.z) rz = ld8n<IOT>(a.z, base + t, m, total);
   };
   if (t_begin < len) load(t_begin);
 
@@ -350,13 +351,14 @@ __global__ __launch_bounds__(SCAN_THREADS) void k_scan_bwd_ends(ScanArgs a) {
   const int64_t L = a.L;
   const int len = seq_length(a, b), t0 = c * CH, t = t0 + 8 * l, m = len - t;
   const int64_t bc = ((int64_t)b * a.G + g) * N * L;
+  const int64_t total = (int64_t)a.B * a.D * L, bc_total = (int64_t)a.B * a.G * N * L;
   float* sB = lds;
   float* sC = lds + N * CH;
   for (int i = tid; i < 2 * N * 16; i += SCAN_THREADS) {
     const int v = i & 15, n = i >> 4;
     const bool isC = n >= N;
     float x[8];
-    widen8<IOT>(ld8n<IOT>(isC ? a.Cm : a.Bm, bc + (int64_t)(isC ? n - N : n) * L + t0 + 8 * v, len - t0 - 8 * v), x);
+    widen8<IOT>(ld8n<IOT>(isC ? a.Cm : a.Bm, bc + (int64_t)(isC ? n - N : n) * L + t0 + 8 * v, len - t0 - 8 * v, bc_total), x);
     stage8(lds + n * CH, v, x);
   }
   __syncthreads();
@@ -367,10 +369,10 @@ __global__ __launch_bounds__(SCAN_THREADS) void k_scan_bwd_ends(ScanArgs a) {
     const int d = g * Dg + (live ? dg : Dg - 1), mm = live ? m : 0;
     const int64_t at = ((int64_t)b * a.D + d) * L + t;
     float u[8], dt[8], gy[8];
-    const Raw8<IOT> rg = ld8n<IOT>(a.gy, at, mm);
+    const Raw8<IOT> rg = ld8n<IOT>(a.gy, at, mm, total);
     Raw8<IOT> rz;
-    if (a.z) rz = ld8n<IOT>(a.z, at, mm);
-    steps8<IOT>(a, ld8n<IOT>(a.u, at, mm), ld8n<IOT>(a.delta, at, mm), a.dbias ? a.dbias[d] : 0.f, mm, u, dt);
+    if (a.z) rz = ld8n<IOT>(a.z, at, mm, total);
+    steps8<IOT>(a, ld8n<IOT>(a.u, at, mm, total), ld8n<IOT>(a.delta, at, mm, total), a.dbias ? a.dbias[d] : 0.f, mm, u, dt);
     widen8<IOT>(rg, gy);
     if (a.z) {
       float z[8];
@@ -466,6 +468,7 @@ __global__ __launch_bounds__(SCAN_THREADS) void k_scan_bwd(ScanArgs a) {
   const int len = seq_length(a, b), t0 = c * CH, t = t0 + 8 * l, m = len - t;
   const int room = (int)min(L - t, (int64_t)8);      // this lane's steps in the array (<= 0: none)
   const int64_t bc = ((int64_t)b * a.G + g) * N * L;
+  const int64_t total = (int64_t)a.B * a.D * L, bc_total = (int64_t)a.B * a.G * N * L;
   float* sB = lds;                                             // [N][128]
   float* sC = sB + N * CH;                                     // [N][128]
   f32x4v* sG = reinterpret_cast<f32x4v*>(sC + N * CH);         // [N][64 lanes]: sums over channels
@@ -474,7 +477,7 @@ __global__ __launch_bounds__(SCAN_THREADS) void k_scan_bwd(ScanArgs a) {
     const int v = i & 15, n = i >> 4;
     const bool isC = n >= N;
     float x[8];
-    widen8<IOT>(ld8n<IOT>(isC ? a.Cm : a.Bm, bc + (int64_t)(isC ? n - N : n) * L + t0 + 8 * v, len - t0 - 8 * v), x);
+    widen8<IOT>(ld8n<IOT>(isC ? a.Cm : a.Bm, bc + (int64_t)(isC ? n - N : n) * L + t0 + 8 * v, len - t0 - 8 * v, bc_total), x);
     stage8(lds + n * CH, v, x);
   }
   for (int i = tid; i < N * 64; i += SCAN_THREADS) sG[i] = f32x4v{0.f, 0.f, 0.f, 0.f};
@@ -486,9 +489,9 @@ __global__ __launch_bounds__(SCAN_THREADS) void k_scan_bwd(ScanArgs a) {
     const bool live = dg < Dg;
     const int d = g * Dg + (live ? dg : Dg - 1), mm = live ? m : 0;
     const int64_t at = ((int64_t)b * a.D + d) * L + t, r = ((int64_t)b * a.chunks + c) * a.D + d;
-    const Raw8<IOT> ru = ld8n<IOT>(a.u, at, mm), rd = ld8n<IOT>(a.delta, at, mm), rg = ld8n<IOT>(a.gy, at, mm);
+    const Raw8<IOT> ru = ld8n<IOT>(a.u, at, mm, total), rd = ld8n<IOT>(a.delta, at, mm, total), rg = ld8n<IOT>(a.gy, at, mm, total);
     Raw8<IOT> rz = zero8<IOT>();
-    if (a.z) rz = ld8n<IOT>(a.z, at, mm);
+    if (a.z) rz = ld8n<IOT>(a.z, at, mm, total);
     // this wave's channels only: no other wave reads or writes these words
     for (int n = l; n < N; n += 16) {
       const float A = a.A[(int64_t)d * N + n];

@@ -57,12 +57,30 @@ __device__ __forceinline__ Raw8<IOT> ld8(const void* p, int64_t i) {
   return r;
 }
 
-// The first n of eight values from element i, zeros behind them.
+// The first n of eight values from element i of an array of `total`, zeros
+// behind them.  The eight are read whole wherever the array has them and
+// masked in registers: loads under a lane's condition wait for each other.
 template <int IOT>
-__device__ __forceinline__ Raw8<IOT> ld8n(const void* p, int64_t i, int n) {
-  if (n >= 8) return ld8<IOT>(p, i);
+__device__ __forceinline__ Raw8<IOT> ld8n(const void* p, int64_t i, int n, int64_t total) {
   Raw8<IOT> r = zero8<IOT>();
-  if constexpr (IOT == 0) {
+  if (n <= 0) return r;
+  if (i + 8 <= total) {
+    r = ld8<IOT>(p, i);
+    if (n < 8) {
+      if constexpr (IOT == 0) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          r.a[e] = e < n ? r.a[e] : 0.f;
+          r.b[e] = e + 4 < n ? r.b[e] : 0.f;
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) r.a[e] = 2 * e + 1 < n ? r.a[e] : (2 * e < n ? r.a[e] & 0xffffu : 0u);
+      }
+    }
+    return r;
+  }
+  if constexpr (IOT == 0) {                           // the array's last values
     const float* q = static_cast<const float*>(p) + i;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -92,7 +110,8 @@ __device__ __forceinline__ void widen8(const Raw8<IOT>& r, float (&o)[8]) {
   }
 }
 
-// The first n of eight values to element i (bf16: rounded to nearest even).
+// The first n of eight values to element i (bf16: rounded to nearest even),
+// n >= 1.
 template <int IOT>
 __device__ __forceinline__ void st8n(void* p, int64_t i, const float (&v)[8], int n) {
   if constexpr (IOT == 0) {
@@ -101,9 +120,17 @@ __device__ __forceinline__ void st8n(void* p, int64_t i, const float (&v)[8], in
       *reinterpret_cast<f32x4_e4*>(q) = f32x4v{v[0], v[1], v[2], v[3]};
       *reinterpret_cast<f32x4_e4*>(q + 4) = f32x4v{v[4], v[5], v[6], v[7]};
     } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (e < n) q[e] = v[e];
+      int e = 0;
+      float x = v[0], y = v[1], z = v[2];
+      if (n & 4) {
+        *reinterpret_cast<f32x4_e4*>(q) = f32x4v{v[0], v[1], v[2], v[3]};
+        e = 4, x = v[4], y = v[5], z = v[6];
+      }
+      if (n & 2) {
+        q[e] = x, q[e + 1] = y;
+        e += 2, x = z;
+      }
+      if (n & 1) q[e] = x;
     }
   } else {
     uint16_t* q = static_cast<uint16_t*>(p) + i;
@@ -112,9 +139,19 @@ __device__ __forceinline__ void st8n(void* p, int64_t i, const float (&v)[8], in
     if (n >= 8) {
       *reinterpret_cast<u32x4_e2*>(q) = w;
     } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (e < n) q[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+      typedef uint32_t u2 __attribute__((ext_vector_type(2), aligned(2)));
+      typedef uint32_t u1 __attribute__((aligned(2)));
+      int e = 0;
+      uint32_t x = w[0], y = w[1];
+      if (n & 4) {
+        *reinterpret_cast<u2*>(q) = u2{w[0], w[1]};
+        e = 4, x = w[2], y = w[3];
+      }
+      if (n & 2) {
+        *reinterpret_cast<u1*>(q + e) = x;
+        e += 2, x = y;
+      }
+      if (n & 1) q[e] = (uint16_t)x;
     }
   }
 }
