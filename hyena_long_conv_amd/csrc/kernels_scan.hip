@@ -17,6 +17,8 @@
 // B and C in LDS as fp32.
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "ssm.hpp"
 #include "ssm_device.hpp"
 
@@ -25,26 +27,40 @@ namespace {
 
 constexpr int CH = kScanChunk, TILE = kScanTile, SCAN_THREADS = 256;
 
-// Inclusive scan of the maps (P, H) over a row, lane 0 first.
+// Inclusive scan of the maps (P, H) over a row, lane 0 first.  A lane whose
+// range reaches lane 0 has nothing more to take in: the zeros that come from
+// outside the row leave its H as it is, and its P, which they clear, has no
+// other use.
+//
+// H += P * (lane i-k's or i+k's H) as one instruction.  A lane move may read a
+// register only two issue slots after it was written; the compiler sees to
+// that around its own instructions, but not at either end of these.
+template <int K> __device__ __forceinline__ void add_shr(float& H, float P) {
+  asm("s_nop 1\n\tv_fmac_f32_dpp %0, %0, %1 row_shr:%2 row_mask:0xf bank_mask:0xf bound_ctrl:1\n\ts_nop 1" : "+v"(H) : "v"(P), "n"(K));
+}
+template <int K> __device__ __forceinline__ void add_shl(float& H, float P) {
+  asm("s_nop 1\n\tv_fmac_f32_dpp %0, %0, %1 row_shl:%2 row_mask:0xf bank_mask:0xf bound_ctrl:1\n\ts_nop 1" : "+v"(H) : "v"(P), "n"(K));
+}
+
 __device__ __forceinline__ void row_scan(float P, float& H) {
-  H = fmaf(P, row_shr<1>(0.f, H), H);
-  P *= row_shr<1>(1.f, P);
-  H = fmaf(P, row_shr<2>(0.f, H), H);
-  P *= row_shr<2>(1.f, P);
-  H = fmaf(P, row_shr<4>(0.f, H), H);
-  P *= row_shr<4>(1.f, P);
-  H = fmaf(P, row_shr<8>(0.f, H), H);
+  add_shr<1>(H, P);
+  P *= row_shr<1>(P);
+  add_shr<2>(H, P);
+  P *= row_shr<2>(P);
+  add_shr<4>(H, P);
+  P *= row_shr<4>(P);
+  add_shr<8>(H, P);
 }
 
 // The same, lane 15 first.
 __device__ __forceinline__ void row_scan_back(float P, float& H) {
-  H = fmaf(P, row_shl<1>(0.f, H), H);
-  P *= row_shl<1>(1.f, P);
-  H = fmaf(P, row_shl<2>(0.f, H), H);
-  P *= row_shl<2>(1.f, P);
-  H = fmaf(P, row_shl<4>(0.f, H), H);
-  P *= row_shl<4>(1.f, P);
-  H = fmaf(P, row_shl<8>(0.f, H), H);
+  add_shl<1>(H, P);
+  P *= row_shl<1>(P);
+  add_shl<2>(H, P);
+  P *= row_shl<2>(P);
+  add_shl<4>(H, P);
+  P *= row_shl<4>(P);
+  add_shl<8>(H, P);
 }
 
 // LDS place of step t's value among a state's 128: lanes read their 8 steps
@@ -190,35 +206,46 @@ __global__ __launch_bounds__(SCAN_THREADS) void k_scan(ScanArgs a) {
       sum += dt[i];
     }
     dt_total += sum;
-    for (int n = 0; n < N; ++n) {
-      const float2 sc = sS[cw * N + n];
-      const float A2 = sc.x, h0 = sc.y;
-      float x[8], al[8];
-      fetch8(sB + n * CH, l, x);
+    // U states at once: their lane moves fill each other's waits
+    auto states = [&](int n, auto count) {
+      constexpr int U = decltype(count)::value;
+      float x[U][8], al[U][8], h0[U], H[U];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        al[i] = exp2_fast(dt[i] * A2);
-        x[i] *= u[i];
-      }
-      float H = x[0];
-#pragma unroll
-      for (int i = 1; i < 8; ++i) H = fmaf(al[i], H, x[i]);
-      const float P = exp2_fast(A2 * sum);
-      H = fmaf(P, l == 0 ? h0 : 0.f, H);
-      row_scan(P, H);
-      const float r = row_ror<1>(H);                  // lane 0: the state at the chunk's end
-      if (l == 0) sS[cw * N + n].y = r;
-      if constexpr (!END) {
-        float c[8];
-        fetch8(sC + n * CH, l, c);
-        float h = l == 0 ? h0 : r;
+      for (int k = 0; k < U; ++k) {
+        const float2 sc = sS[cw * N + n + k];
+        h0[k] = sc.y;
+        fetch8(sB + (n + k) * CH, l, x[k]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          h = fmaf(al[i], h, x[i]);
-          y[i] = fmaf(h, c[i], y[i]);
+          al[k][i] = exp2_fast(dt[i] * sc.x);
+          x[k][i] *= u[i];
+        }
+        H[k] = x[k][0];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) H[k] = fmaf(al[k][i], H[k], x[k][i]);
+        const float P = exp2_fast(sc.x * sum);
+        H[k] = fmaf(P, l == 0 ? h0[k] : 0.f, H[k]);
+        row_scan(P, H[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const float r = row_ror<1>(H[k]);             // lane 0: the state at the chunk's end
+        if (l == 0) sS[cw * N + n + k].y = r;
+        if constexpr (!END) {
+          float c[8];
+          fetch8(sC + (n + k) * CH, l, c);
+          float h = l == 0 ? h0[k] : r;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            h = fmaf(al[k][i], h, x[k][i]);
+            y[i] = fmaf(h, c[i], y[i]);
+          }
         }
       }
-    }
+    };
+    int n = 0;
+    for (; n + 2 <= N; n += 2) states(n, std::integral_constant<int, 2>());
+    if (n < N) states(n, std::integral_constant<int, 1>());
     if constexpr (!END) {
       if (a.z) {
 #pragma unroll
@@ -456,7 +483,7 @@ __device__ __forceinline__ float fold_rows(float x, float y) {
 }
 
 template <int IOT>
-__global__ __launch_bounds__(SCAN_THREADS) void k_scan_bwd(ScanArgs a) {
+__global__ __launch_bounds__(SCAN_THREADS, 3) void k_scan_bwd(ScanArgs a) {
   extern __shared__ float lds[];
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, row = lane >> 4, l = lane & 15;
   const int N = a.N, Dg = a.D / a.G, tiles = (Dg + TILE - 1) / TILE, per = (tiles + a.splits - 1) / a.splits;
@@ -527,11 +554,14 @@ __global__ __launch_bounds__(SCAN_THREADS) void k_scan_bwd(ScanArgs a) {
         fetch8(sB + n * CH, l, x);
         fetch8(sC + n * CH, l, cc);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) al[i] = exp2_fast(dt[i] * A2);
-        float H = du[0] * x[0], Q = al[7] * (cc[7] * gy[7]);
+        for (int i = 0; i < 8; ++i) {
+          al[i] = exp2_fast(dt[i] * A2);
+          h[i] = du[i] * x[i];
+        }
+        float H = h[0], Q = al[7] * (cc[7] * gy[7]);
 #pragma unroll
         for (int i = 1; i < 8; ++i) {
-          H = fmaf(al[i], H, du[i] * x[i]);
+          H = fmaf(al[i], H, h[i]);
           Q = al[7 - i] * fmaf(cc[7 - i], gy[7 - i], Q);
         }
         const float P = exp2_fast(A2 * sum);
@@ -539,11 +569,13 @@ __global__ __launch_bounds__(SCAN_THREADS) void k_scan_bwd(ScanArgs a) {
         Q = fmaf(P, l == 15 ? sc[2] : 0.f, Q);
         row_scan(P, H);
         row_scan_back(P, Q);
-        const float hb = row_shr<1>(sc[1], H);        // the state before this lane's steps
-        float q = row_shl<1>(sc[2], Q);               // the carry from behind them
+        // moved in all lanes, then chosen: the state before this lane's steps, the carry from behind them
+        const float hm = row_shr<1>(H), qm = row_shl<1>(Q);
+        const float hb = l == 0 ? sc[1] : hm;
+        float q = l == 15 ? sc[2] : qm;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          h[i] = fmaf(al[i], i ? h[i - 1] : hb, du[i] * x[i]);
+          h[i] = fmaf(al[i], i ? h[i - 1] : hb, h[i]);
           y[i] = fmaf(h[i], cc[i], y[i]);
         }
         float gA = 0.f;

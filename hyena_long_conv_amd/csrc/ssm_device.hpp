@@ -157,15 +157,16 @@ __device__ __forceinline__ void st8n(void* p, int64_t i, const float (&v)[8], in
 }
 
 // Lane moves within rows of 16 lanes.  shr<k>: lane i gets lane i-k's value,
-// shl<k>: lane i+k's; lanes without a source get `none`.  ror<k>: lane i gets
-// lane (i-k) mod 16's.
+// shl<k>: lane i+k's; lanes without a source get 0, which lets the move become
+// part of the instruction that uses it.  ror<k>: lane i gets lane (i-k) mod
+// 16's.
 template <int CTRL>
-__device__ __forceinline__ float row_move(float none, float v) {
-  return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(none), __float_as_int(v), CTRL, 0xf, 0xf, false));
+__device__ __forceinline__ float row_move(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true));
 }
-template <int K> __device__ __forceinline__ float row_shr(float none, float v) { return row_move<0x110 + K>(none, v); }
-template <int K> __device__ __forceinline__ float row_shl(float none, float v) { return row_move<0x100 + K>(none, v); }
-template <int K> __device__ __forceinline__ float row_ror(float v) { return row_move<0x120 + K>(v, v); }
+template <int K> __device__ __forceinline__ float row_shr(float v) { return row_move<0x110 + K>(v); }
+template <int K> __device__ __forceinline__ float row_shl(float v) { return row_move<0x100 + K>(v); }
+template <int K> __device__ __forceinline__ float row_ror(float v) { return row_move<0x120 + K>(v); }
 
 // The sum over a row of 16 lanes, in every lane.
 __device__ __forceinline__ float row_sum(float v) {
