@@ -92,7 +92,11 @@ __device__ __forceinline__ void steps8(const ScanArgs& a, const Raw8<IOT>& ru, c
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const float x = dt[i] + bias;
-    dt[i] = i < n ? (a.softplus ? softplus_f(x) : x) : 0.f;
+    dt[i] = a.softplus ? softplus_f(x) : x;
+  }
+  if (n < 8) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dt[i] = i < n ? dt[i] : 0.f;
   }
 }
 
@@ -155,20 +159,23 @@ __global__ __launch_bounds__(SCAN_THREADS) void k_scan(ScanArgs a) {
   const int words = (END ? N : 2 * N) * 16;
   Raw8<IOT> rbc[NW], ru, rd, rz;
   auto load = [&](int t0) {
+    const int t = t0 + 8 * l;
+    const auto word = [&](const void* p, int64_t i, int n, int64_t end) {
+      return t0 + CH <= len ? ld8<IOT>(p, i) : ld8n<IOT>(p, i, n, end);     // the same way for the whole workgroup
+    };
 #pragma unroll
     for (int k = 0; k < NW; ++k) {
       const int i = tid + SCAN_THREADS * k, v = i & 15, n = i >> 4;
-      rbc[k] = zero8<IOT>();
       if (i < words) {
         const bool isC = n >= N;
-        rbc[k] = ld8n<IOT>(isC ? a.Cm : a.Bm, bc + (int64_t)(isC ? n - N : n) * L + t0 + 8 * v, len - t0 - 8 * v, bc_total);
+        rbc[k] = word(isC ? a.Cm : a.Bm, bc + (int64_t)(isC ? n - N : n) * L + t0 + 8 * v, len - t0 - 8 * v, bc_total);
       }
     }
-    const int t = t0 + 8 * l, m = live ? len - t : 0;
-    ru = ld8n<IOT>(a.u, base + t, m, total);
-    rd = ld8n<IOT>(a.delta, base + t, m, total);
+    // a wave's channels behind the group's last one read that one's row
+    ru = word(a.u, base + t, len - t, total);
+    rd = word(a.delta, base + t, len - t, total);
     if constexpr (!END)
-      if (a.z) rz = ld8n<IOT>(a.z, base + t, m, total);
+      if (a.z) rz = word(a.z, base + t, len - t, total);
   };
   if (t_begin < len) load(t_begin);
 
@@ -192,7 +199,7 @@ __global__ __launch_bounds__(SCAN_THREADS) void k_scan(ScanArgs a) {
       }
     }
     float u[8], dt[8], z[8], y[8];
-    steps8<IOT>(a, ru, rd, bias, live ? m : 0, u, dt);
+    steps8<IOT>(a, ru, rd, bias, m, u, dt);
     if constexpr (!END)
       if (a.z) widen8<IOT>(rz, z);
     __syncthreads();
