@@ -75,19 +75,21 @@ def _take(t, name, shape, dtype, device):
     """The address of tensor t, which has to be what the operator takes; None gives 0."""
     if t is None:
         return None
+    try:                                              # one expression for a single token's call, where this counts
+        if t.is_cuda and t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == device:
+            return t.data_ptr()
+    except AttributeError:
+        pass
     _H._need_cuda(t, name, dtype)
     if t.shape != shape:
         raise ValueError(f"{name} shape {tuple(t.shape)} != {tuple(shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
-    return t.data_ptr()
+    raise ValueError(f"{name} is on {t.device}, not on {device}")
 
 
 def _call(name, device, *args):
     """One C-ABI call on the device's current stream, with that device current."""
     torch = _torch()
-    stream = vp(torch.cuda.current_stream(device).cuda_stream)
-    fn = getattr(_H.lib(), name)
+    fn, stream = getattr(_H._lib or _H.lib(), name), torch._C._cuda_getCurrentRawStream(device.index)
     if torch.cuda.current_device() == device.index:
         code = fn(*args, stream)
     else:
@@ -98,8 +100,8 @@ def _call(name, device, *args):
 
 
 def _activation(x, name, dims):
-    io = _H._io_of(x)
     _H._need_cuda(x, name)
+    io = _H._io_of(x)
     if x.dim() != dims:
         raise ValueError(f"{name} has {x.dim()} dimensions, not {dims}")
     return io
