@@ -110,17 +110,25 @@ struct ScanArgs {
   float* gbc;                              // [splits][2][B][G][N][L] parts of gB and gC, when splits > 1
 };
 
-// Segments of the forward scan and their length.  A wave scans 4 channels;
-// with fewer than about two waves for each SIMD of the chip (1024) the time
-// axis is split, which costs a second pass over the decays.
+// Segments of the forward scan and their length.  The scan is bound by its
+// arithmetic once a SIMD holds three waves; with k of them it takes t(k) of
+// their single times (1.98, 2.4 and 3.15 of a saturated one measured for k =
+// 1, 2, 3), k being what the fullest of 256 compute units gets.  Splitting
+// the time axis fills the chip and costs the first pass over the segments'
+// ends, 0.72 of the scan itself.  768 rows of 65536 steps (48 workgroups): 581
+// us in 11 segments, 2.1 workgroups to a compute unit, 475 us in 16, which
+// are 3.  12288 rows of 2048 steps in one: 133 us.
 inline void scan_segments(int64_t B, int64_t D, int64_t L, int* segs, int64_t* seg) {
-  const int64_t waves = B * ((D + kScanTile - 1) / kScanTile) * 4;
-  int64_t s = 1;
-  if (waves < 1024) s = (2048 + waves - 1) / waves;
-  const int64_t chunks = (L + kScanChunk - 1) / kScanChunk;
-  if (s > chunks / 4) s = chunks / 4;      // at least four chunks in a segment
-  if (s < 1) s = 1;
-  const int64_t per = (chunks + s - 1) / s;
+  const int64_t groups = B * ((D + kScanTile - 1) / kScanTile), chunks = (L + kScanChunk - 1) / kScanChunk;
+  int64_t best = 1;
+  double least = 0;
+  for (int64_t s = 1; s <= 64 && 2 * s <= (s == 1 ? 2 : chunks); ++s) {   // at least two chunks in a segment
+    const int64_t k = (groups * s + 255) / 256, per = (chunks + s - 1) / s;
+    const double t = k == 1 ? 1.98 : k == 2 ? 2.4 : k == 3 ? 3.15 : (double)k;
+    const double cost = t * (double)per * (s > 1 ? 1.72 : 1.0);
+    if (s == 1 || cost < least) least = cost, best = s;
+  }
+  const int64_t per = (chunks + best - 1) / best;
   *seg = per * kScanChunk;
   *segs = (int)((chunks + per - 1) / per);
 }

@@ -19,6 +19,7 @@ stream of that GPU, whichever GPU is the current one.
 from __future__ import annotations
 
 import ctypes
+import os
 
 import hyena_long_conv_amd as _H
 
@@ -76,7 +77,7 @@ def _take(t, name, shape, dtype, device):
     if t is None:
         return None
     try:                                              # one expression for a single token's call, where this counts
-        if t.is_cuda and t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == device:
+        if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
             return t.data_ptr()
     except AttributeError:
         pass
@@ -88,9 +89,10 @@ def _take(t, name, shape, dtype, device):
 
 def _call(name, device, *args):
     """One C-ABI call on the device's current stream, with that device current."""
-    torch = _torch()
-    fn, stream = getattr(_H._lib or _H.lib(), name), torch._C._cuda_getCurrentRawStream(device.index)
-    if torch.cuda.current_device() == device.index:
+    import torch
+    fn, at = getattr(_H._lib or _H.lib(), name), device.index
+    stream = torch._C._cuda_getCurrentRawStream(at)
+    if torch._C._cuda_getDevice() == at:
         code = fn(*args, stream)
     else:
         with torch.cuda.device(device):
@@ -99,12 +101,25 @@ def _call(name, device, *args):
         raise _H.HyenaError(code, name)
 
 
+_POISON = os.environ.get("HYENA_POISON") == "1"       # asked for once: a token's call has no time for it
+
+
+def _like(t):
+    """An output of t's shape and dtype (filled with NaN under the package's test instrument)."""
+    import torch
+    return _H._empty_like(t) if _POISON else torch.empty_like(t)
+
+
 def _activation(x, name, dims):
-    _H._need_cuda(x, name)
-    io = _H._io_of(x)
+    """Checks the tensor that sets a call's shape, dtype and device: 0 for float32, 1 for bfloat16."""
+    import torch
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        raise TypeError(f"{name} must be a CUDA (ROCm) tensor")
     if x.dim() != dims:
         raise ValueError(f"{name} has {x.dim()} dimensions, not {dims}")
-    return io
+    if not x.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return _H._io_of(x)
 
 
 def _workspace(workspace, nbytes, name, device):
@@ -147,7 +162,7 @@ def short_conv(x, w, bias=None, silu: bool = False, state=None, lengths=None, re
     io = _activation(x, "x", 3)
     B, D, L = x.shape
     T, p = _conv_params(x, w, bias, silu, state, lengths, B, D, L)
-    y = out if out is not None else _H._empty_like(x)
+    y = out if out is not None else _like(x)
     if return_state and state_out is None:
         state_out = _H._empty((B, D, T - 1), dtype=x.dtype, device=x.device)
     so = _take(state_out, "state_out", (B, D, T - 1), x.dtype, x.device) if T > 1 else None
@@ -162,10 +177,11 @@ def short_conv_step(x, w, state, bias=None, silu: bool = False, out=None):
     io = _activation(x, "x", 2)
     B, D = x.shape
     T, p = _conv_params(x, w, bias, silu, None, None, B, D, 1)
-    y = out if out is not None else _H._empty_like(x)
-    st = _take(state, "state", (B, D, T - 1), x.dtype, x.device) if T > 1 else None
-    _call("hyena_short_conv_step", x.device, x.data_ptr(), ctypes.byref(p), st,
-          _take(y, "out", x.shape, x.dtype, x.device), io)
+    dev, t = x.device, x.dtype
+    y = _like(x) if out is None else out
+    yp = y.data_ptr() if out is None else _take(out, "out", (B, D), t, dev)
+    st = _take(state, "state", (B, D, T - 1), t, dev) if T > 1 else None
+    _call("hyena_short_conv_step", dev, x.data_ptr(), ctypes.byref(p), st, yp, io)
     return y
 
 
@@ -184,9 +200,9 @@ def short_conv_backward(x, w, gy, bias=None, silu: bool = False, state=None, len
     B, D, L = x.shape
     T, p = _conv_params(x, w, bias, silu, state, lengths, B, D, L)
     dev = x.device
-    gx, gw = _H._empty_like(x), _H._empty_like(w)
-    gbias = _H._empty_like(bias) if bias is not None else None
-    gstate = _H._empty_like(state) if state is not None else None
+    gx, gw = _like(x), _like(w)
+    gbias = _like(bias) if bias is not None else None
+    gstate = _like(state) if state is not None else None
     gso = _take(gstate_out, "gstate_out", (B, D, T - 1), x.dtype, dev) if T > 1 else None
     keep, ws, wsb = _workspace(workspace, short_conv_backward_workspace_bytes(B, D, T, L),
                                "hyena_short_conv_backward_workspace_bytes", dev)
@@ -233,7 +249,7 @@ def selective_scan(u, delta, A, Bm, Cm, skip=None, z=None, delta_bias=None, soft
     B, D, L = u.shape
     N, G, p = _scan_params(u, delta, A, Bm, Cm, skip, z, delta_bias, softplus, state, lengths, B, D, (L,))
     dev = u.device
-    y = out if out is not None else _H._empty_like(u)
+    y = out if out is not None else _like(u)
     if return_state and state_out is None:
         state_out = _H._empty((B, D, N), dtype=torch.float32, device=dev)
     keep, ws, wsb = _workspace(workspace, selective_scan_workspace_bytes(B, D, N, L),
@@ -252,9 +268,10 @@ def selective_scan_step(u, delta, A, Bm, Cm, state, skip=None, z=None, delta_bia
     B, D = u.shape
     N, G, p = _scan_params(u, delta, A, Bm, Cm, skip, z, delta_bias, softplus, None, None, B, D, ())
     dev = u.device
-    y = out if out is not None else _H._empty_like(u)
-    _call("hyena_selective_scan_step", dev, ctypes.byref(p), _take(state, "state", (B, D, N), torch.float32, dev),
-          _take(y, "out", u.shape, u.dtype, dev), io)
+    y = _like(u) if out is None else out
+    yp = y.data_ptr() if out is None else _take(out, "out", (B, D), u.dtype, dev)
+    _call("hyena_selective_scan_step", dev, ctypes.byref(p), _take(state, "state", (B, D, N), torch.float32, dev), yp,
+          io)
     return y
 
 
@@ -274,7 +291,7 @@ def selective_scan_backward(u, delta, A, Bm, Cm, gy, skip=None, z=None, delta_bi
     N, G, p = _scan_params(u, delta, A, Bm, Cm, skip, z, delta_bias, softplus, state, lengths, B, D, (L,))
     dev = u.device
     out = dict(gu=u, gdelta=delta, gA=A, gB=Bm, gC=Cm, gskip=skip, gz=z, gdelta_bias=delta_bias, gstate=state)
-    out = {k: _H._empty_like(v) if v is not None else None for k, v in out.items()}
+    out = {k: _like(v) if v is not None else None for k, v in out.items()}
     g = SelectiveScanGrads(*[v.data_ptr() if v is not None else None for v in out.values()])
     keep, ws, wsb = _workspace(workspace, selective_scan_backward_workspace_bytes(B, D, G, N, L),
                                "hyena_selective_scan_backward_workspace_bytes", dev)
@@ -300,8 +317,8 @@ def rms_norm(x, weight, residual=None, eps: float = 1e-6, out=None):
     torch = _torch()
     io, rows, D = _rows(x, "x")
     dev = x.device
-    y = out if out is not None else _H._empty_like(x)
-    s = _H._empty_like(x) if residual is not None else None
+    y = out if out is not None else _like(x)
+    s = _like(x) if residual is not None else None
     _call("hyena_rms_norm", dev, x.data_ptr(), _take(residual, "residual", x.shape, x.dtype, dev),
           _take(weight, "weight", (D,), torch.float32, dev), _take(y, "out", x.shape, x.dtype, dev),
           s.data_ptr() if s is not None else None, rows, D, eps, io)
@@ -326,7 +343,7 @@ def rms_norm_quantized(x, weight, residual=None, eps: float = 1e-6):
     io, rows, D = _rows(x, "x")
     dev = x.device
     q, scales = _codes(x.shape, dev)
-    s = _H._empty_like(x) if residual is not None else None
+    s = _like(x) if residual is not None else None
     _call("hyena_rms_norm_quantized", dev, x.data_ptr(), _take(residual, "residual", x.shape, x.dtype, dev),
           _take(weight, "weight", (D,), torch.float32, dev), q.data_ptr(), scales.data_ptr(),
           s.data_ptr() if s is not None else None, rows, D, eps, io)
@@ -344,7 +361,7 @@ def rms_norm_backward(s, weight, gy, gs=None, eps: float = 1e-6, workspace=None)
     torch = _torch()
     io, rows, D = _rows(s, "s")
     dev = s.device
-    gx, gw = _H._empty_like(s), _H._empty((D,), dtype=torch.float32, device=dev)
+    gx, gw = _like(s), _H._empty((D,), dtype=torch.float32, device=dev)
     keep, ws, wsb = _workspace(workspace, rms_norm_backward_workspace_bytes(rows, D),
                                "hyena_rms_norm_backward_workspace_bytes", dev)
     _call("hyena_rms_norm_backward", dev, s.data_ptr(), _take(weight, "weight", (D,), torch.float32, dev),
