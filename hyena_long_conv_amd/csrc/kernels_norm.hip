@@ -27,13 +27,20 @@ __device__ __forceinline__ float wave_sum(float v) {
   return v + __shfl_xor(v, 32);
 }
 
-// Maximum over a row of 16 lanes; a NaN among them stays.
-__device__ __forceinline__ float nan_max(float x, float y) { return x != x || x > y ? x : y; }
-__device__ __forceinline__ float row_max(float v) {
-  v = nan_max(v, row_ror<8>(v));
-  v = nan_max(v, row_ror<4>(v));
-  v = nan_max(v, row_ror<2>(v));
-  return nan_max(v, row_ror<1>(v));
+// The size of a value as its bits, whose order as whole numbers is that of the
+// sizes, with infinities and then NaN above all others.
+__device__ __forceinline__ uint32_t size_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+// Maximum over a row of 16 lanes, in every lane.
+template <int K>
+__device__ __forceinline__ uint32_t ror_bits(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x120 + K, 0xf, 0xf, true);
+}
+__device__ __forceinline__ uint32_t row_max(uint32_t v) {
+  v = max(v, ror_bits<8>(v));
+  v = max(v, ror_bits<4>(v));
+  v = max(v, ror_bits<2>(v));
+  return max(v, ror_bits<1>(v));
 }
 
 // The sum over the LANES threads (64 to 256, a row each) of a value.
@@ -52,12 +59,28 @@ __device__ __forceinline__ float group_sum(float v, float* lds) {
   return v;
 }
 
-// e4m3 codes of 8 values and their block's scale, from the block's 16 lanes.
-__device__ __forceinline__ uint2 codes8(const float (&y)[8], float top, float& scale) {
-  scale = top > 0.f ? fmaxf(top / kE4m3Max, 1.17549435e-38f) : (top != top ? top : 1.f);
+// e4m3 codes of 8 values and their block's scale, from the block's largest
+// size.  The quotients are correctly rounded: with r the rounded reciprocal
+// of the scale, q = v r corrected once by its remainder is (Markstein 1990),
+// as long as the remainder does not underflow; blocks that small are divided.
+// Three instructions to a value instead of a division's dozen: 8191 rows of
+// 2048 bf16 with a residual take 30 us instead of 35, the cast alone of 8192
+// rows 10.9 instead of 13.3.
+__device__ __forceinline__ uint2 codes8(const float (&y)[8], uint32_t top, float& scale) {
+  const float t = __uint_as_float(top);
+  scale = t > 0.f ? fmaxf(t / kE4m3Max, 1.17549435e-38f) : (t != t ? t : 1.f);
   float v[8];
+  if (scale < 1e-18f) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = y[e] / scale;
+    for (int e = 0; e < 8; ++e) v[e] = y[e] / scale;
+  } else {
+    const float r = 1.f / scale;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float q = y[e] * r;
+      v[e] = fmaf(fmaf(-q, scale, y[e]), r, q);
+    }
+  }
   uint2 q;
   int lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
   lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], lo, true);
@@ -127,11 +150,11 @@ __global__ __launch_bounds__(NORM_THREADS) void k_norm(NormArgs a) {
       float wt[8], y[8];
       if (MORE) take(w, f[k], false);
       widen8<0>(ld8n<0>(a.weight, 8 * (int64_t)w, D - 8 * w, D), wt);
-      float top = 0.f;
+      uint32_t top = 0u;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         y[e] = f[k][e] * r * wt[e];
-        top = nan_max(fabsf(y[e]), top);
+        top = max(top, size_bits(y[e]));
       }
       if constexpr (!Q8) {
         if (n > 0) st8n<IOT>(a.y, base + 8 * (int64_t)w, y, n);
@@ -169,10 +192,11 @@ __global__ __launch_bounds__(256) void k_quantize_rows(NormArgs a) {
   const bool live = blk < a.rows * kb;
   const int64_t row = live ? blk / kb : 0;
   const int c = (int)(live ? blk - row * kb : 0) * 128 + 8 * l, n = live ? a.D - c : 0;
-  float y[8], top = 0.f, scale;
+  float y[8], scale;
+  uint32_t top = 0u;
   widen8<IOT>(ld8n<IOT>(a.x, row * a.D + c, n, a.rows * a.D), y);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) top = nan_max(fabsf(y[e]), top);
+  for (int e = 0; e < 8; ++e) top = max(top, size_bits(y[e]));
   const uint2 q = codes8(y, row_max(top), scale);
   if (n > 0) st_codes(a.q, row * a.D + c, q, n);
   if (live && l == 0) a.scales[blk] = scale;
@@ -181,24 +205,25 @@ __global__ __launch_bounds__(256) void k_quantize_rows(NormArgs a) {
 // Blocks of 128 x 128: a workgroup each, 16 rows at a time.
 template <int IOT>
 __global__ __launch_bounds__(256) void k_quantize_tiles(NormArgs a) {
-  __shared__ float lds[16];
+  __shared__ uint32_t lds[16];
   const int kb = (a.D + 127) / 128, rw = threadIdx.x >> 4, l = threadIdx.x & 15;
   const int64_t rb = blockIdx.x / kb;
   const int c = (int)(blockIdx.x - rb * kb) * 128 + 8 * l;
-  float y[8][8], top = 0.f, scale;
+  float y[8][8], scale;
+  uint32_t top = 0u;
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     const int64_t row = rb * 128 + 16 * k + rw;
     widen8<IOT>(ld8n<IOT>(a.x, row * a.D + c, row < a.rows ? a.D - c : 0, a.rows * a.D), y[k]);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) top = nan_max(fabsf(y[k][e]), top);
+    for (int e = 0; e < 8; ++e) top = max(top, size_bits(y[k][e]));
   }
   top = row_max(top);
   if (l == 0) lds[rw] = top;
   __syncthreads();
   top = lds[0];
 #pragma unroll
-  for (int k = 1; k < 16; ++k) top = nan_max(lds[k], top);
+  for (int k = 1; k < 16; ++k) top = max(top, lds[k]);
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     const int64_t row = rb * 128 + 16 * k + rw;

@@ -128,7 +128,7 @@ def _workspace(workspace, nbytes, name, device):
     if nbytes < 0:
         raise _H.HyenaError(2, name)
     if workspace is None:
-        workspace = _H._empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+        workspace = _new(nbytes, torch.uint8, device) if nbytes else None
     else:
         _H._need_cuda(workspace, "workspace")
         if workspace.device != device:
@@ -164,7 +164,7 @@ def short_conv(x, w, bias=None, silu: bool = False, state=None, lengths=None, re
     T, p = _conv_params(x, w, bias, silu, state, lengths, B, D, L)
     y = out if out is not None else _like(x)
     if return_state and state_out is None:
-        state_out = _H._empty((B, D, T - 1), dtype=x.dtype, device=x.device)
+        state_out = _new((B, D, T - 1), x.dtype, x.device)
     so = _take(state_out, "state_out", (B, D, T - 1), x.dtype, x.device) if T > 1 else None
     _call("hyena_short_conv", x.device, x.data_ptr(), ctypes.byref(p), _take(y, "out", x.shape, x.dtype, x.device), so,
           io)
@@ -251,7 +251,7 @@ def selective_scan(u, delta, A, Bm, Cm, skip=None, z=None, delta_bias=None, soft
     dev = u.device
     y = out if out is not None else _like(u)
     if return_state and state_out is None:
-        state_out = _H._empty((B, D, N), dtype=torch.float32, device=dev)
+        state_out = _new((B, D, N), torch.float32, dev)
     keep, ws, wsb = _workspace(workspace, selective_scan_workspace_bytes(B, D, N, L),
                                "hyena_selective_scan_workspace_bytes", dev)
     _call("hyena_selective_scan", dev, ctypes.byref(p), _take(y, "out", u.shape, u.dtype, dev),
@@ -325,14 +325,20 @@ def rms_norm(x, weight, residual=None, eps: float = 1e-6, out=None):
     return (y, s) if residual is not None else y
 
 
+def _new(shape, dtype, dev):
+    """An output, filled with NaN under the package's test instrument."""
+    import torch
+    t = torch.empty(shape, dtype=dtype, device=dev)
+    if _POISON:
+        _H._poison(t if dtype.itemsize > 1 else t.view(torch.uint8))
+    return t
+
+
 def _codes(shape, dev, block_rows=1):
     """Codes and scales for values [..., K]: a scale for each 128 of a row, or for each 128 x 128."""
-    torch = _torch()
-    kb = -(-shape[-1] // 128)
-    q = torch.empty(shape, dtype=torch.float8_e4m3fn, device=dev)
-    _H._poison(q.view(torch.uint8))
+    import torch
     head = shape[:-1] if block_rows == 1 else (-(-shape[0] // 128),)
-    return q, _H._empty((*head, kb), dtype=torch.float32, device=dev)
+    return (_new(shape, torch.float8_e4m3fn, dev), _new((*head, -(-shape[-1] // 128)), torch.float32, dev))
 
 
 def rms_norm_quantized(x, weight, residual=None, eps: float = 1e-6):
@@ -361,7 +367,7 @@ def rms_norm_backward(s, weight, gy, gs=None, eps: float = 1e-6, workspace=None)
     torch = _torch()
     io, rows, D = _rows(s, "s")
     dev = s.device
-    gx, gw = _like(s), _H._empty((D,), dtype=torch.float32, device=dev)
+    gx, gw = _like(s), _new((D,), torch.float32, dev)
     keep, ws, wsb = _workspace(workspace, rms_norm_backward_workspace_bytes(rows, D),
                                "hyena_rms_norm_backward_workspace_bytes", dev)
     _call("hyena_rms_norm_backward", dev, s.data_ptr(), _take(weight, "weight", (D,), torch.float32, dev),
@@ -405,7 +411,7 @@ def scaled_matmul(q, scales, wq, wscales, bias=None, out_dtype=None, channel_maj
     if out_dtype not in (torch.float32, torch.bfloat16):
         raise TypeError("out_dtype must be float32 or bfloat16")
     shape = (*q.shape[:-2], N, L) if channel_major else (*q.shape[:-1], N)
-    o = out if out is not None else _H._empty(shape, dtype=out_dtype, device=dev)
+    o = out if out is not None else _new(shape, out_dtype, dev)
     _call("hyena_scaled_matmul", dev, q.data_ptr(), _take(scales, "scales", (*q.shape[:-1], kb), f32, dev),
           _take(wq, "wq", (N, K), e4m3, dev), _take(wscales, "wscales", (-(-N // 128), kb), f32, dev),
           _take(bias, "bias", (N,), f32, dev), _take(o, "out", shape, out_dtype, dev), B, L, N, K,
