@@ -179,16 +179,15 @@ static hyena_status scan_args(const hyena_selective_scan_params* p, hyena_dtype 
   return HYENA_OK;
 }
 
-static int64_t scan_tiles(const ScanArgs& a) {
-  return (int64_t)a.B * a.G * ((a.D / a.G + kScanTile - 1) / kScanTile);
+static int64_t scan_groups(const ScanArgs& a) {
+  const int64_t tile = kScanTile / a.split;
+  return (int64_t)a.B * a.G * ((a.D / a.G + tile - 1) / tile);
 }
 
 int64_t hyena_selective_scan_workspace_bytes(int64_t B, int32_t D, int32_t N, int64_t L) {
   if (!batch_ok(B, D, L) || N < 1 || N > HYENA_MAX_STATE) return -1;
-  int segs;
-  int64_t seg;
-  scan_segments(B, D, L, &segs, &seg);
-  return segs > 1 ? (int64_t)segs * B * D * (N + 1) * 4 : 0;
+  const int64_t segs = scan_plan(B, D, N, L).segs;
+  return segs > 1 ? segs * B * D * (N + 1) * 4 : 0;
 }
 
 hyena_status hyena_selective_scan(const hyena_selective_scan_params* p, void* y, float* state_out, hyena_dtype io,
@@ -196,8 +195,11 @@ hyena_status hyena_selective_scan(const hyena_selective_scan_params* p, void* y,
   if (!y) return HYENA_ERR_NULL;
   ScanArgs a;
   if (const hyena_status s = scan_args(p, io, p ? p->L : 1, &a)) return s;
-  scan_segments(a.B, a.D, a.L, &a.segs, &a.seg);
-  if (scan_tiles(a) * a.segs > kMaxGroups) return HYENA_ERR_UNSUPPORTED;
+  const ScanPlan plan = scan_plan(a.B, a.D, a.N, a.L);
+  a.split = plan.split;
+  a.segs = plan.segs;
+  a.seg = plan.seg;
+  if (scan_groups(a) * a.segs > kMaxGroups) return HYENA_ERR_UNSUPPORTED;
   const int64_t need = hyena_selective_scan_workspace_bytes(a.B, a.D, a.N, a.L);
   if (need > 0 && (!workspace || workspace_bytes < need)) return HYENA_ERR_WORKSPACE;
   const int64_t e = size_of(io), rows = p->B * a.D, act = rows * a.L * e, bc = p->B * a.G * a.N * a.L * e;

@@ -102,24 +102,28 @@ __device__ __forceinline__ void steps8(const ScanArgs& a, const Raw8<IOT>& ru, c
 
 // ---------------------------------------------------------------- forward
 //
-// One workgroup: 16 channels of a group over one time segment, chunk after
-// chunk.  END: only the state at the segment's end from a zero start, and the
+// One workgroup: 16 channels of a group (with SPLIT = 4: 4 channels, whose
+// states its waves share) over one time segment, chunk after chunk.  END: only the state at the segment's end from a zero start, and the
 // sum of dt, for the segments behind it (all but the last run this first
 // when the time axis is split); a segment's decay is exp(A sum dt), so the
 // start of segment s is a short recurrence over the ones before it, which
 // each workgroup does for its own channels.
-template <int IOT, int NV, bool END>
+template <int IOT, int NV, int SPLIT, bool END>
 __global__ __launch_bounds__(SCAN_THREADS) void k_scan(ScanArgs a) {
   extern __shared__ float lds[];
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, row = lane >> 4, l = lane & 15;
-  const int N = a.N, Dg = a.D / a.G, tiles = (Dg + TILE - 1) / TILE;
+  constexpr int TC = TILE / SPLIT;                   // channels of the workgroup
+  const int N = a.N, Dg = a.D / a.G, tiles = (Dg + TC - 1) / TC;
   const int nseg = END ? a.segs - 1 : a.segs;
   int id = blockIdx.x;
   const int tile = id % tiles; id /= tiles;
   const int g = id % a.G; id /= a.G;
   const int seg = id % nseg;
   const int b = id / nseg;
-  const int cw = wave * 4 + row, dg = tile * TILE + cw;
+  const int cw = SPLIT == 1 ? wave * 4 + row : row, dg = tile * TC + cw;
+  // this wave's states
+  const int share = (N + SPLIT - 1) / SPLIT, n_begin = SPLIT == 1 ? 0 : wave * share, n_end = min(N, n_begin + share);
+  const bool first = SPLIT == 1 || wave == 0;
   const bool live = dg < Dg;
   const int d = g * Dg + (live ? dg : Dg - 1);
   const int64_t L = a.L;
@@ -132,16 +136,18 @@ __global__ __launch_bounds__(SCAN_THREADS) void k_scan(ScanArgs a) {
 
   float* sB = lds;                                   // [N][128]
   float* sC = END ? lds : lds + N * CH;              // [N][128]
-  float2* sS = reinterpret_cast<float2*>((END ? lds : sC) + N * CH);   // [16][N]: A log2(e), the state at the chunk's start
+  float2* sS = reinterpret_cast<float2*>((END ? lds : sC) + N * CH);   // [TC][N]: A log2(e), the state at the chunk's start
+  f32x4v* sY = reinterpret_cast<f32x4v*>(sS + TC * N);                 // SPLIT > 1: [SPLIT - 1][2][64] parts of y
 
-  for (int i = tid; i < TILE * N; i += SCAN_THREADS) {
-    const int c = i / N, n = i - c * N, dc = tile * TILE + c;
+  for (int i = tid; i < TC * N; i += SCAN_THREADS) {
+    const int c = i / N, n = i - c * N, dc = tile * TC + c;
     float A2 = 0.f, h = 0.f;
     if (dc < Dg) {
       const int ch = g * Dg + dc;
       A2 = a.A[(int64_t)ch * N + n] * kLog2e;
       if constexpr (!END) {
         if (a.state) h = a.state[((int64_t)b * a.D + ch) * N + n];
+#pragma unroll 4
         for (int s = 0; s < seg; ++s) {
           const int64_t r = ((int64_t)b * a.segs + s) * a.D + ch;
           h = fmaf(exp2_fast(A2 * a.sdt[r]), h, a.hend[r * N + n]);
@@ -184,7 +190,7 @@ __global__ __launch_bounds__(SCAN_THREADS) void k_scan(ScanArgs a) {
     if (t0 >= len) {                                  // behind the sequence: zeros
       if constexpr (!END) {
         float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (live && t < L) st8n<IOT>(a.y, base + t, y, (int)min(L - t, (int64_t)8));
+        if (first && live && t < L) st8n<IOT>(a.y, base + t, y, (int)min(L - t, (int64_t)8));
       }
       continue;
     }
@@ -208,7 +214,7 @@ __global__ __launch_bounds__(SCAN_THREADS) void k_scan(ScanArgs a) {
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      y[i] = skip * u[i];
+      y[i] = first ? skip * u[i] : 0.f;
       u[i] *= dt[i];
       sum += dt[i];
     }
@@ -250,10 +256,25 @@ __global__ __launch_bounds__(SCAN_THREADS) void k_scan(ScanArgs a) {
         }
       }
     };
-    int n = 0;
-    for (; n + 2 <= N; n += 2) states(n, std::integral_constant<int, 2>());
-    if (n < N) states(n, std::integral_constant<int, 1>());
-    if constexpr (!END) {
+    int n = n_begin;
+    for (; n + 2 <= n_end; n += 2) states(n, std::integral_constant<int, 2>());
+    if (n < n_end) states(n, std::integral_constant<int, 1>());
+    if constexpr (!END && SPLIT > 1) {                // the states' shares of y meet in the first wave
+      if (wave > 0) {
+        sY[(wave * 2 - 2) * 64 + lane] = f32x4v{y[0], y[1], y[2], y[3]};
+        sY[(wave * 2 - 1) * 64 + lane] = f32x4v{y[4], y[5], y[6], y[7]};
+      }
+      __syncthreads();
+      if (wave == 0) {
+#pragma unroll
+        for (int k = 0; k < SPLIT - 1; ++k) {
+          const f32x4v p = sY[2 * k * 64 + lane], q = sY[(2 * k + 1) * 64 + lane];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) { y[e] += p[e]; y[e + 4] += q[e]; }
+        }
+      }
+    }
+    if (!END && first) {
       if (a.z) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) y[i] *= z[i] * sigmoid_f(z[i]);
@@ -268,13 +289,13 @@ __global__ __launch_bounds__(SCAN_THREADS) void k_scan(ScanArgs a) {
 
   if constexpr (END) {
     dt_total = row_sum(dt_total);
-    if (live && l == 0) a.sdt[((int64_t)b * a.segs + seg) * a.D + d] = dt_total;
+    if (first && live && l == 0) a.sdt[((int64_t)b * a.segs + seg) * a.D + d] = dt_total;
   } else if (!a.state_out || seg != a.segs - 1) {
     return;
   }
   __syncthreads();
-  for (int i = tid; i < TILE * N; i += SCAN_THREADS) {
-    const int c = i / N, n = i - c * N, dc = tile * TILE + c;
+  for (int i = tid; i < TC * N; i += SCAN_THREADS) {
+    const int c = i / N, n = i - c * N, dc = tile * TC + c;
     if (dc >= Dg) continue;
     const int ch = g * Dg + dc;
     if constexpr (END) a.hend[(((int64_t)b * a.segs + seg) * a.D + ch) * N + n] = sS[i].y;
@@ -282,17 +303,27 @@ __global__ __launch_bounds__(SCAN_THREADS) void k_scan(ScanArgs a) {
   }
 }
 
-template <int IOT, int NV>
+template <int IOT, int NV, int SPLIT>
 hipError_t launch_scan(const ScanArgs& a, hipStream_t s) {
-  const int64_t tiles = (a.D / a.G + TILE - 1) / TILE, wgs = tiles * a.G * a.B;
-  const size_t state = (size_t)TILE * a.N * 8, bc = (size_t)a.N * CH * 4;
+  constexpr int TC = TILE / SPLIT;
+  const int64_t tiles = (a.D / a.G + TC - 1) / TC, wgs = tiles * a.G * a.B;
+  const size_t state = (size_t)TC * a.N * 8, bc = (size_t)a.N * CH * 4, parts = (SPLIT - 1) * 2048;
   if (a.segs > 1) {
-    k_scan<IOT, NV, true><<<dim3((unsigned)(wgs * (a.segs - 1))), SCAN_THREADS, bc + state, s>>>(a);
+    k_scan<IOT, NV, SPLIT, true><<<dim3((unsigned)(wgs * (a.segs - 1))), SCAN_THREADS, bc + state, s>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  k_scan<IOT, NV, false><<<dim3((unsigned)(wgs * a.segs)), SCAN_THREADS, 2 * bc + state, s>>>(a);
+  k_scan<IOT, NV, SPLIT, false><<<dim3((unsigned)(wgs * a.segs)), SCAN_THREADS, 2 * bc + state + parts, s>>>(a);
   return hipGetLastError();
+}
+
+template <int IOT, int SPLIT>
+hipError_t launch_scan_nv(const ScanArgs& a, hipStream_t s) {
+  const int nv = (a.N + 7) / 8;
+  return nv <= 1   ? launch_scan<IOT, 1, SPLIT>(a, s)
+         : nv <= 2 ? launch_scan<IOT, 2, SPLIT>(a, s)
+         : nv <= 4 ? launch_scan<IOT, 4, SPLIT>(a, s)
+                   : launch_scan<IOT, 8, SPLIT>(a, s);
 }
 
 // ------------------------------------------------------------ single tokens
@@ -490,7 +521,7 @@ __device__ __forceinline__ float fold_rows(float x, float y) {
 }
 
 template <int IOT>
-__global__ __launch_bounds__(SCAN_THREADS, 3) void k_scan_bwd(ScanArgs a) {
+__global__ __launch_bounds__(SCAN_THREADS, 2) void k_scan_bwd(ScanArgs a) {
   extern __shared__ float lds[];
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, row = lane >> 4, l = lane & 15;
   const int N = a.N, Dg = a.D / a.G, tiles = (Dg + TILE - 1) / TILE, per = (tiles + a.splits - 1) / a.splits;
@@ -702,10 +733,8 @@ hipError_t launch_scan_backward(const ScanArgs& a, hipStream_t s) {
 }  // namespace
 
 hipError_t selective_scan(const ScanArgs& a, hipStream_t s) {
-  const int nv = (a.N + 7) / 8;
-#define HYENA_SCAN(V) (a.io ? launch_scan<1, V>(a, s) : launch_scan<0, V>(a, s))
-  return nv <= 1 ? HYENA_SCAN(1) : nv <= 2 ? HYENA_SCAN(2) : nv <= 4 ? HYENA_SCAN(4) : HYENA_SCAN(8);
-#undef HYENA_SCAN
+  if (a.split > 1) return a.io ? launch_scan_nv<1, 4>(a, s) : launch_scan_nv<0, 4>(a, s);
+  return a.io ? launch_scan_nv<1, 1>(a, s) : launch_scan_nv<0, 1>(a, s);
 }
 
 hipError_t selective_scan_step(const ScanArgs& a, hipStream_t s) {

@@ -79,7 +79,7 @@ hipError_t short_conv_backward(const ConvArgs& a, hipStream_t s);
 
 // ---------------------------------------------------------- selective scan
 constexpr int kScanChunk = 128;     // steps that 16 lanes scan at once, 8 each
-constexpr int kScanTile = 16;       // channels of a workgroup: 4 waves of 4
+constexpr int kScanTile = 16;       // channels of a workgroup: 4 waves of 4 (a wave's 4 where they share the states)
 
 struct ScanArgs {
   const void *u, *delta, *Bm, *Cm, *z;     // z: or nullptr
@@ -89,6 +89,7 @@ struct ScanArgs {
   float* state_out;                        // or nullptr
   int B, D, G, N, softplus, io;
   int64_t L;
+  int split;                               // waves that share a channel's states: 1 or 4
   // time axis split into `segs` segments of `seg` steps (a multiple of the
   // chunk): end states and sums of dt of all but the last, when segs > 1
   int segs;
@@ -110,27 +111,41 @@ struct ScanArgs {
   float* gbc;                              // [splits][2][B][G][N][L] parts of gB and gC, when splits > 1
 };
 
-// Segments of the forward scan and their length.  The scan is bound by its
-// arithmetic once a SIMD holds three waves; with k of them it takes t(k) of
-// their single times (1.98, 2.4 and 3.15 of a saturated one measured for k =
-// 1, 2, 3), k being what the fullest of 256 compute units gets.  Splitting
-// the time axis fills the chip and costs the first pass over the segments'
-// ends, 0.72 of the scan itself.  768 rows of 65536 steps (48 workgroups): 581
-// us in 11 segments, 2.1 workgroups to a compute unit, 475 us in 16, which
-// are 3.  12288 rows of 2048 steps in one: 133 us.
-inline void scan_segments(int64_t B, int64_t D, int64_t L, int* segs, int64_t* seg) {
+// How the forward scan fills the chip.  It is bound by its arithmetic once a
+// SIMD holds three waves; with k of them it takes t(k) of their single times
+// (1.98, 2.4 and 3.15 of a saturated one measured for k = 1, 2, 3), k being
+// what the fullest of 256 compute units gets.  Two ways to more waves:
+//   split  4 waves share 4 channels, a quarter of the states each, instead of
+//          16 channels with all states: what does not depend on the state
+//          (3 states' worth of work, 6.5 with the meeting of the parts) is
+//          done by all four.  1536 rows of 512 steps with 16 states: 23.0 us
+//          alone, 14.8 shared; 4096 rows of 2048 steps: 83 alone, 92 shared;
+//   segs   the time axis in segments of `seg` steps: a first pass over their
+//          ends costs 0.72 of the scan and a launch (about 30 units of one
+//          state of one chunk), and each workgroup joins the ends before it.
+//          768 rows of 65536 fp32 steps: 581 us in 11 segments, 2.1
+//          workgroups to a compute unit, 475 in 16, which are 3.
+struct ScanPlan {
+  int split, segs;
+  int64_t seg;
+};
+inline ScanPlan scan_plan(int64_t B, int64_t D, int64_t N, int64_t L) {
   const int64_t groups = B * ((D + kScanTile - 1) / kScanTile), chunks = (L + kScanChunk - 1) / kScanChunk;
-  int64_t best = 1;
-  double least = 0;
-  for (int64_t s = 1; s <= 64 && 2 * s <= (s == 1 ? 2 : chunks); ++s) {   // at least two chunks in a segment
-    const int64_t k = (groups * s + 255) / 256, per = (chunks + s - 1) / s;
-    const double t = k == 1 ? 1.98 : k == 2 ? 2.4 : k == 3 ? 3.15 : (double)k;
-    const double cost = t * (double)per * (s > 1 ? 1.72 : 1.0);
-    if (s == 1 || cost < least) least = cost, best = s;
+  ScanPlan best{1, 1, chunks * kScanChunk};
+  double least = -1;
+  for (int split = 1; split <= 4; split *= 4) {
+    for (int64_t s = 1; s <= 64 && s <= chunks; ++s) {
+      const int64_t k = (groups * split * s + 255) / 256, per = (chunks + s - 1) / s;
+      const double t = k == 1 ? 1.98 : k == 2 ? 2.4 : k == 3 ? 3.15 : (double)k;
+      const double work = (split > 1 ? 6.5 : 3.1) + (double)((N + split - 1) / split);
+      const double cost = t * work * (double)per * (s > 1 ? 1.72 : 1.0) + (s > 1 ? 30.0 + 0.7 * (double)s : 0.0);
+      if (least < 0 || cost < least) {
+        least = cost;
+        best = ScanPlan{split, (int)((chunks + per - 1) / per), per * kScanChunk};
+      }
+    }
   }
-  const int64_t per = (chunks + best - 1) / best;
-  *seg = per * kScanChunk;
-  *segs = (int)((chunks + per - 1) / per);
+  return best;
 }
 
 struct ScanBackwardLayout {
