@@ -47,6 +47,24 @@ __device__ __forceinline__ void conv_word(const ConvArgs& a, int64_t r, int t, i
 template <int IOT, int H, int N>
 __device__ __forceinline__ void conv_window(const ConvArgs& a, int64_t r, int t, int len, float (&x)[H + N]) {
   float v[8];
+  if (t >= (H + 7) / 8 * 8 && t + (N + 7) / 8 * 8 <= len) {           // nothing to mask: most lanes
+    const int64_t i = r * a.L + t;
+#pragma unroll
+    for (int k = 0; k < (H + 7) / 8; ++k) {
+      widen8<IOT>(ld8<IOT>(a.x, i - 8 * (k + 1)), v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (H - 8 * (k + 1) + e >= 0) x[H - 8 * (k + 1) + e] = v[e];
+    }
+#pragma unroll
+    for (int k = 0; k < (N + 7) / 8; ++k) {
+      widen8<IOT>(ld8<IOT>(a.x, i + 8 * k), v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (8 * k + e < N) x[H + 8 * k + e] = v[e];
+    }
+    return;
+  }
 #pragma unroll
   for (int k = 0; k < (H + 7) / 8; ++k) {
     conv_word<IOT>(a, r, t - 8 * (k + 1), len, v);
@@ -72,12 +90,12 @@ __device__ __forceinline__ void conv_taps(const ConvArgs& a, int d, float (&w)[T
 template <int IOT, int TT>
 __global__ __launch_bounds__(256) void k_conv(ConvArgs a, int per, int lper, int blocks) {
   const int tid = threadIdx.x;
-  const int64_t rb = blockIdx.x / blocks;
+  const uint32_t rb = blockIdx.x / (uint32_t)blocks;
   const int xb = (int)(blockIdx.x - rb * blocks);
-  const int64_t r = rb * (256 >> lper) + (tid >> lper);
+  const int64_t r = (int64_t)rb * (256 >> lper) + (tid >> lper);
   if (r >= (int64_t)a.B * a.D) return;
-  const int64_t b = r / a.D;
-  const int d = (int)(r - b * a.D), len = conv_length(a, b);
+  const uint32_t b = (uint32_t)r / (uint32_t)a.D;     // rows are at most 2^30
+  const int d = (int)((uint32_t)r - b * (uint32_t)a.D), len = conv_length(a, b);
   const int i = xb * per + (tid & (per - 1)), t = 8 * i;
   if (a.state_out)
     for (int k = i; k < a.T - 1; k += blocks * per)
@@ -93,7 +111,11 @@ __global__ __launch_bounds__(256) void k_conv(ConvArgs a, int per, int lper, int
       float p = bias;
 #pragma unroll
       for (int j = 0; j < TT; ++j) p = fmaf(w[j], x[TT + e - j], p);
-      y[e] = t + e < len ? (a.silu ? p * sigmoid_f(p) : p) : 0.f;
+      y[e] = a.silu ? p * sigmoid_f(p) : p;
+    }
+    if (t + 8 > len) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = t + e < len ? y[e] : 0.f;
     }
   } else {
 #pragma unroll
@@ -107,7 +129,7 @@ template <int IOT, int TT>
 __global__ __launch_bounds__(256) void k_conv_step(ConvArgs a) {
   const int64_t r = blockIdx.x * (int64_t)256 + threadIdx.x;
   if (r >= (int64_t)a.B * a.D) return;
-  const int d = (int)(r % a.D), S = a.T - 1;
+  const int d = (int)((uint32_t)r % (uint32_t)a.D), S = a.T - 1;
   float w[TT], x[TT];
   conv_taps<TT>(a, d, w);
   x[0] = ld1<IOT>(a.x, r);
@@ -133,10 +155,12 @@ template <int IOT, int TT>
 __device__ __forceinline__ void conv_gp(const ConvArgs& a, int64_t r, int t, int len, const float (&w)[TT], float bias,
                                         float (&x)[2 * TT + 8], float (&gp)[TT + 8]) {
   conv_window<IOT, TT, TT + 8>(a, r, t, len, x);
+  const bool whole = t + (TT + 15) / 8 * 8 <= len;
 #pragma unroll
   for (int k = 0; k < (TT + 15) / 8; ++k) {
     float v[8];
-    widen8<IOT>(ld8n<IOT>(a.gy, r * a.L + t + 8 * k, len - t - 8 * k, (int64_t)a.B * a.D * a.L), v);
+    const int64_t i = r * a.L + t + 8 * k;
+    widen8<IOT>(whole ? ld8<IOT>(a.gy, i) : ld8n<IOT>(a.gy, i, len - t - 8 * k, (int64_t)a.B * a.D * a.L), v);
 #pragma unroll
     for (int e = 0; e < 8; ++e)
       if (8 * k + e < TT + 8) gp[8 * k + e] = v[e];
@@ -157,22 +181,22 @@ template <int IOT, int TT>
 __global__ __launch_bounds__(256) void k_conv_bwd(ConvArgs a, ConvBackwardGrid g) {
   __shared__ float part[4][TT + 1];
   const int tid = threadIdx.x, per = g.per, at_once = 256 >> g.lper, S = a.T - 1;
-  const int d = (int)(blockIdx.x % a.D);
-  const int64_t id = blockIdx.x / a.D, grp = id / g.blocks, xb = id - grp * g.blocks;
+  const uint32_t id = blockIdx.x / (uint32_t)a.D, grp = id / (uint32_t)g.blocks, xb = id - grp * (uint32_t)g.blocks;
+  const int d = (int)(blockIdx.x - id * (uint32_t)a.D);
   float w[TT], sum[TT + 1];
   conv_taps<TT>(a, d, w);
   const float bias = a.bias ? a.bias[d] : 0.f;
 #pragma unroll
   for (int j = 0; j <= TT; ++j) sum[j] = 0.f;
-  const int64_t t_end = min(a.L, (xb + 1) * kConvSpan), b_end = min((int64_t)a.B, (grp + 1) * g.seqs);
-  for (int64_t b = grp * g.seqs + (tid >> g.lper); b < b_end; b += at_once) {
-    const int64_t r = b * a.D + d;
+  const int t_end = (int)min(a.L, (xb + 1) * kConvSpan), b_end = (int)min((int64_t)a.B, (grp + 1) * g.seqs);
+  for (int b = (int)(grp * g.seqs) + (tid >> g.lper); b < b_end; b += at_once) {
+    const int64_t r = (int64_t)b * a.D + d;
     const int len = conv_length(a, b);
-    for (int64_t t = xb * kConvSpan + 8 * (tid & (per - 1)); t < t_end; t += 8 * per) {
+    for (int t = (int)(xb * kConvSpan) + 8 * (tid & (per - 1)); t < t_end; t += 8 * per) {
       float gx[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
       if (t < len) {
         float x[2 * TT + 8], gp[TT + 8];
-        conv_gp<IOT, TT>(a, r, (int)t, len, w, bias, x, gp);
+        conv_gp<IOT, TT>(a, r, t, len, w, bias, x, gp);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
 #pragma unroll
@@ -184,7 +208,7 @@ __global__ __launch_bounds__(256) void k_conv_bwd(ConvArgs a, ConvBackwardGrid g
         if (a.gstate_out && t + 8 > len - S) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const int64_t i = t + e - (len - S);
+            const int i = t + e - (len - S);
             if (i >= 0 && i < S) gx[e] += ld1<IOT>(a.gstate_out, r * S + i);
           }
         }
@@ -229,7 +253,7 @@ __global__ __launch_bounds__(256) void k_conv_bwd(ConvArgs a, ConvBackwardGrid g
   if (tid <= TT) {
     const float v = (part[0][tid] + part[1][tid]) + (part[2][tid] + part[3][tid]);
     const int j = tid < TT ? tid : a.T;
-    if (tid == TT || tid < a.T) a.partial[(id * a.D + d) * (a.T + 1) + j] = v;
+    if (tid == TT || tid < a.T) a.partial[((int64_t)id * a.D + d) * (a.T + 1) + j] = v;
   }
 }
 

@@ -337,15 +337,15 @@ __global__ __launch_bounds__(256) void k_scan_step(ScanArgs a, int W, int lw, fl
   const bool live = r < (int64_t)a.B * a.D;
   float part = 0.f, u = 0.f, z = 0.f, skip = 0.f;
   if (live) {
-    const int64_t b = r / a.D;
-    const int d = (int)(r - b * a.D), g = d / (a.D / a.G);
+    const uint32_t b = (uint32_t)r / (uint32_t)a.D;   // rows are at most 2^30
+    const int d = (int)((uint32_t)r - b * (uint32_t)a.D), g = a.G > 1 ? d / (a.D / a.G) : 0;
     u = ld1<IOT>(a.u, r);
     float dt = ld1<IOT>(a.delta, r) + (a.dbias ? a.dbias[d] : 0.f);
     if (a.z) z = ld1<IOT>(a.z, r);
     if (a.skip) skip = a.skip[d];
     const float* A = a.A + (int64_t)d * N + n0;
     float* h = state + r * N + n0;
-    const int64_t bc = (b * a.G + g) * N + n0;
+    const int64_t bc = ((int64_t)b * a.G + g) * N + n0;
     float Av[4], hv[4], Bv[4], Cv[4];
     if ((N & 3) == 0) {
       if (n0 < N) {
@@ -521,7 +521,7 @@ __device__ __forceinline__ float fold_rows(float x, float y) {
 }
 
 template <int IOT>
-__global__ __launch_bounds__(SCAN_THREADS, 2) void k_scan_bwd(ScanArgs a) {
+__global__ __launch_bounds__(SCAN_THREADS, 3) void k_scan_bwd(ScanArgs a) {
   extern __shared__ float lds[];
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, row = lane >> 4, l = lane & 15;
   const int N = a.N, Dg = a.D / a.G, tiles = (Dg + TILE - 1) / TILE, per = (tiles + a.splits - 1) / a.splits;
