@@ -190,7 +190,6 @@ __global__ __launch_bounds__(64 * WM * WN) void k_scaled_mm(ScaledArgs a) {
     __builtin_amdgcn_s_waitcnt(0x0070);               // vmcnt(0) lgkmcnt(0)
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
-    if (b + 1 < kb) issue(b + 1);
     const unsigned char* X = stage + (b & 1) * STAGE + wm * IM * 16 * KS;
     const unsigned char* Y = stage + (b & 1) * STAGE + BM * KS + wn * IN * 16 * KS;
     const float* S = reinterpret_cast<const float*>(stage + (b & 1) * STAGE + (BM + BN) * KS) + wm * IM * 16 + l;
@@ -202,40 +201,55 @@ __global__ __launch_bounds__(64 * WM * WN) void k_scaled_mm(ScaledArgs a) {
 #pragma unroll
     for (int j = 0; j < IN; ++j) w[j] = tile_operand(Y + j * 16 * KS, l, h);
     // The products of one row of tiles run while the one before is scaled and
-    // added: a product is ready some 16 cycles after it was issued.
+    // added: a product is ready some 16 cycles after it was issued.  The first
+    // ones start on the first operands, the others' reads follow between them,
+    // then the next step's loads (behind K they write zeros that no one reads).
     f32x4v p[2][IN];
+    i32x8 next = x;
+    if constexpr (IM > 1) next = tile_operand(X + 16 * KS, l, h);
 #pragma unroll
-    for (int i = 0; i < IM; ++i) {
-      i32x8 next = x;
+    for (int j = 0; j < IN; ++j) p[0][j] = mfma128<IOT>(w[j], x);
+    if constexpr (IOT == 1) {
+      __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+#pragma unroll
+      for (int j = 0; j < IN; ++j) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+      }
+      __builtin_amdgcn_sched_group_barrier(0x100, IM, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    issue(b + 1);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 1; i < IM; ++i) {
+      x = next;
       if (i + 1 < IM) next = tile_operand(X + (i + 1) * 16 * KS, l, h);
 #pragma unroll
       for (int j = 0; j < IN; ++j) {
         p[i & 1][j] = mfma128<IOT>(w[j], x);
-        if (i > 0) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[i - 1][j][e] = fmaf(p[(i - 1) & 1][j][e], sc[i - 1], acc[i - 1][j][e]);
-        }
+        for (int e = 0; e < 4; ++e) acc[i - 1][j][e] = fmaf(p[(i - 1) & 1][j][e], sc[i - 1], acc[i - 1][j][e]);
       }
-      x = next;
     }
 #pragma unroll
     for (int j = 0; j < IN; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[IM - 1][j][e] = fmaf(p[(IM - 1) & 1][j][e], sc[IM - 1], acc[IM - 1][j][e]);
     if constexpr (IOT == 1) {                         // that order, for the instruction scheduler
-      __builtin_amdgcn_sched_group_barrier(0x100, 2 * IN + 4 + IM, 0);
 #pragma unroll
-      for (int i = 0; i < IM; ++i) {
+      for (int i = 1; i < IM; ++i) {
+        if (i + 1 < IM) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
 #pragma unroll
         for (int j = 0; j < IN; ++j) {
           __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-          if (i > 0) __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+          __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
         }
-        if (i + 2 < IM) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
       }
       __builtin_amdgcn_sched_group_barrier(0x002, 4 * IN, 0);
     }
   }
+  __builtin_amdgcn_s_waitcnt(0x0070);                 // vmcnt(0): nothing more lands in LDS
 
   // Out through LDS, each wave its own part, 16 rows (or 16 IM tokens of 16
   // channels) at a time, so that global stores are whole words of a row.
