@@ -18,7 +18,7 @@ namespace {
 
 constexpr int64_t kMaxRows = (int64_t)1 << 30;   // B * D
 constexpr int64_t kMaxDim = (int64_t)1 << 20;
-constexpr int64_t kMaxGroups = (int64_t)1 << 24; // workgroups of 256 threads in a launch
+constexpr int64_t kMaxGroups = ((int64_t)1 << 24) - 1;   // workgroups of 256 threads in a launch (2^32 threads)
 
 // Arrays of a call: null checks are the caller's, absent ones are skipped.
 struct Span {

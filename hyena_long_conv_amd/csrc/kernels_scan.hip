@@ -687,15 +687,36 @@ __global__ __launch_bounds__(SCAN_THREADS, 3) void k_scan_bwd(ScanArgs a) {
   }
 }
 
-// gB and gC from the splits' parts.
+// gB and gC from the splits' parts: 64 values to a workgroup, 4 threads to a
+// value, whose loads are in flight eight at a time.
 template <int IOT>
 __global__ __launch_bounds__(256) void k_scan_bwd_sum_bc(ScanArgs a) {
+  __shared__ float lds[3][64];
   const int64_t n = (int64_t)a.B * a.G * a.N * a.L;
-  for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < 2 * n; i += (int64_t)gridDim.x * 256) {
+  const int c = threadIdx.x & 63, k = threadIdx.x >> 6;
+  for (int64_t first = blockIdx.x * (int64_t)64; first < 2 * n; first += gridDim.x * (int64_t)64) {
+    const int64_t i = first + c;
     float v = 0.f;
-    for (int s = 0; s < a.splits; ++s) v += a.gbc[s * 2 * n + i];
-    if (i < n) st1<IOT>(a.gB, i, v);
-    else st1<IOT>(a.gC, i - n, v);
+    if (i < 2 * n) {
+      const float* p = a.gbc + i;
+      int s = k;
+      for (; s + 28 < a.splits; s += 32) {
+        float w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = p[(s + 4 * j) * 2 * n];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v += w[j];
+      }
+      for (; s < a.splits; s += 4) v += p[s * 2 * n];
+    }
+    if (k > 0) lds[k - 1][c] = v;
+    __syncthreads();
+    if (k == 0 && i < 2 * n) {
+      v = (v + lds[0][c]) + (lds[1][c] + lds[2][c]);
+      if (i < n) st1<IOT>(a.gB, i, v);
+      else st1<IOT>(a.gC, i - n, v);
+    }
+    __syncthreads();
   }
 }
 
@@ -724,7 +745,7 @@ hipError_t launch_scan_backward(const ScanArgs& a, hipStream_t s) {
   k_scan_bwd<IOT><<<dim3(wgs), SCAN_THREADS, bc + (size_t)a.N * 64 * 16 + (size_t)TILE * a.N * 16, s>>>(a);
   if (a.splits > 1) {
     const int64_t n = (int64_t)2 * a.B * a.G * a.N * a.L;
-    k_scan_bwd_sum_bc<IOT><<<dim3((unsigned)min((n + 255) / 256, (int64_t)8192)), 256, 0, s>>>(a);
+    k_scan_bwd_sum_bc<IOT><<<dim3((unsigned)min((n + 63) / 64, (int64_t)1 << 20)), 256, 0, s>>>(a);
   }
   k_scan_bwd_sum_t<<<dim3((unsigned)(((int64_t)a.D * (a.N + 2) + 31) / 32)), SUM_THREADS, 0, s>>>(a);
   return hipGetLastError();

@@ -387,7 +387,8 @@ hyena_status hyena_nd_forward(const void* v, const void* const* x, const void* s
  *
  * Shared by all of them: the conventions at the top of this file; sizes
  * 1 <= B <= 2^20, 1 <= D <= 2^20, B*D <= 2^30, 1 <= L <= HYENA_MAX_L (SHAPE
- * outside, UNSUPPORTED beyond a launch's 2^24 workgroups); activations and
+ * outside, UNSUPPORTED from 2^24 workgroups
+ * of a launch on); activations and
  * carried states 16-byte aligned (ALIGN), fp32 parameter vectors and lengths
  * 4-byte aligned; an output may overlap no input and no other output (ALIAS).
  * Arithmetic is fp32, bf16 values are widened exactly and rounded once, to
