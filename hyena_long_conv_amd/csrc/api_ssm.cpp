@@ -120,7 +120,7 @@ hyena_status hyena_short_conv_step(const void* x, const hyena_short_conv_params*
 
 int64_t hyena_short_conv_backward_workspace_bytes(int64_t B, int32_t D, int32_t T, int64_t L) {
   if (!batch_ok(B, D, L) || T < 1 || T > HYENA_MAX_SHORT) return -1;
-  return conv_backward_grid(B, D, L).parts * D * (T + 1) * 4;
+  return conv_backward_grid(B, D, L, T).parts * D * (T + 1) * 4;
 }
 
 hyena_status hyena_short_conv_backward(const void* x, const hyena_short_conv_params* p, const void* gy,
@@ -131,7 +131,7 @@ hyena_status hyena_short_conv_backward(const void* x, const hyena_short_conv_par
   if (const hyena_status s = conv_args(p, io, p ? p->L : 1, &a)) return s;
   if (a.T == 1 && (p->state || gstate_out || gstate)) return HYENA_ERR_SHAPE;
   const int64_t e = size_of(io), act = p->B * a.D * a.L * e, st = p->B * a.D * (a.T - 1) * e;
-  if (conv_backward_grid(p->B, a.D, a.L).parts * a.D > kMaxGroups) return HYENA_ERR_UNSUPPORTED;
+  if (conv_backward_grid(p->B, a.D, a.L, a.T).parts * a.D > kMaxGroups) return HYENA_ERR_UNSUPPORTED;
   const int64_t need = hyena_short_conv_backward_workspace_bytes(p->B, a.D, a.T, a.L);
   if (workspace_bytes < need) return HYENA_ERR_WORKSPACE;
   const Span out[] = {{gx, act, 16}, {gw, (int64_t)a.D * a.T * 4, 4}, {gbias, (int64_t)a.D * 4, 4}, {gstate, st, 16},

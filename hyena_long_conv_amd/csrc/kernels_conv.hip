@@ -151,23 +151,23 @@ __global__ __launch_bounds__(256) void k_conv_step(ConvArgs a) {
 // computed again, for a lane's 8 steps and the TT-1 behind them.  A workgroup
 // sums over its sequences and steps in registers and leaves one partial for
 // each tap, which k_conv_sum adds up in a fixed order.
-template <int IOT, int TT>
+template <int IOT, int TT, int E>
 __device__ __forceinline__ void conv_gp(const ConvArgs& a, int64_t r, int t, int len, const float (&w)[TT], float bias,
-                                        float (&x)[2 * TT + 8], float (&gp)[TT + 8]) {
-  conv_window<IOT, TT, TT + 8>(a, r, t, len, x);
-  const bool whole = t + (TT + 15) / 8 * 8 <= len;
+                                        float (&x)[2 * TT + E], float (&gp)[TT + E]) {
+  conv_window<IOT, TT, TT + E>(a, r, t, len, x);
+  const bool whole = t + (TT + E + 7) / 8 * 8 <= len;
 #pragma unroll
-  for (int k = 0; k < (TT + 15) / 8; ++k) {
+  for (int k = 0; k < (TT + E + 7) / 8; ++k) {
     float v[8];
     const int64_t i = r * a.L + t + 8 * k;
     widen8<IOT>(whole ? ld8<IOT>(a.gy, i) : ld8n<IOT>(a.gy, i, len - t - 8 * k, (int64_t)a.B * a.D * a.L), v);
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      if (8 * k + e < TT + 8) gp[8 * k + e] = v[e];
+      if (8 * k + e < TT + E) gp[8 * k + e] = v[e];
   }
   if (a.silu) {
 #pragma unroll
-    for (int e = 0; e < TT + 7; ++e) {
+    for (int e = 0; e < TT + E - 1; ++e) {
       float p = bias;
 #pragma unroll
       for (int j = 0; j < TT; ++j) p = fmaf(w[j], x[TT + e - j], p);
@@ -179,6 +179,7 @@ __device__ __forceinline__ void conv_gp(const ConvArgs& a, int64_t r, int t, int
 
 template <int IOT, int TT>
 __global__ __launch_bounds__(256) void k_conv_bwd(ConvArgs a, ConvBackwardGrid g) {
+  constexpr int E = conv_each(TT);
   __shared__ float part[4][TT + 1];
   const int tid = threadIdx.x, per = g.per, at_once = 256 >> g.lper, S = a.T - 1;
   const uint32_t id = blockIdx.x / (uint32_t)a.D, grp = id / (uint32_t)g.blocks, xb = id - grp * (uint32_t)g.blocks;
@@ -192,32 +193,40 @@ __global__ __launch_bounds__(256) void k_conv_bwd(ConvArgs a, ConvBackwardGrid g
   for (int b = (int)(grp * g.seqs) + (tid >> g.lper); b < b_end; b += at_once) {
     const int64_t r = (int64_t)b * a.D + d;
     const int len = conv_length(a, b);
-    for (int t = (int)(xb * kConvSpan) + 8 * (tid & (per - 1)); t < t_end; t += 8 * per) {
-      float gx[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (t < len) {
-        float x[2 * TT + 8], gp[TT + 8];
-        conv_gp<IOT, TT>(a, r, t, len, w, bias, x, gp);
+    for (int t = (int)(xb * kConvSpan) + E * (tid & (per - 1)); t < t_end; t += E * per) {
+      float gx[E];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+      for (int e = 0; e < E; ++e) gx[e] = 0.f;
+      if (t < len) {
+        float x[2 * TT + E], gp[TT + E];
+        conv_gp<IOT, TT, E>(a, r, t, len, w, bias, x, gp);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
 #pragma unroll
           for (int j = 0; j < TT; ++j) gx[e] = fmaf(w[j], gp[e + j], gx[e]);
           sum[TT] += gp[e];
 #pragma unroll
           for (int j = 0; j < TT; ++j) sum[j] = fmaf(gp[e], x[TT + e - j], sum[j]);
         }
-        if (a.gstate_out && t + 8 > len - S) {
+        if (a.gstate_out && t + E > len - S) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
+          for (int e = 0; e < E; ++e) {
             const int i = t + e - (len - S);
             if (i >= 0 && i < S) gx[e] += ld1<IOT>(a.gstate_out, r * S + i);
           }
         }
-        if (t + 8 > len) {
+        if (t + E > len) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) gx[e] = t + e < len ? gx[e] : 0.f;
+          for (int e = 0; e < E; ++e) gx[e] = t + e < len ? gx[e] : 0.f;
         }
       }
-      st8n<IOT>(a.gx, r * a.L + t, gx, (int)min(a.L - t, (int64_t)8));
+#pragma unroll
+      for (int k = 0; k < E; k += 8) {
+        float o[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = gx[k + e];
+        if (t + k < a.L) st8n<IOT>(a.gx, r * a.L + t + k, o, (int)min(a.L - t - k, (int64_t)8));
+      }
     }
     // the carried inputs: one thread to a row walks over its T-1 values
     if (a.gstate && xb == 0 && (tid & (per - 1)) == 0) {
@@ -307,7 +316,7 @@ hipError_t short_conv_step(const ConvArgs& a, hipStream_t s) {
 }
 
 hipError_t short_conv_backward(const ConvArgs& a, hipStream_t s) {
-  const ConvBackwardGrid g = conv_backward_grid(a.B, a.D, a.L);
+  const ConvBackwardGrid g = conv_backward_grid(a.B, a.D, a.L, a.T);
   if (a.T <= 4) conv_backward_tt<4>(a, g, s);
   else if (a.T <= 8) conv_backward_tt<8>(a, g, s);
   else conv_backward_tt<16>(a, g, s);

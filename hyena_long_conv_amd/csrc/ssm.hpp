@@ -30,16 +30,16 @@ struct ConvArgs {
 };
 
 // Rows share a workgroup of 256 threads when they are short: `per` threads
-// (a power of two, 8 steps each) to a row, or `blocks` workgroups of `span`
-// steps along a long one.
+// (a power of two, `each` steps to a thread) to a row, or `blocks` workgroups
+// of `span` steps along a long one.
 struct ConvGrid {
   int per, lper;
   int64_t blocks, groups;
 };
 constexpr int64_t kConvStep = 2048;   // the forward's span: one word of 8 steps to a thread
-inline ConvGrid conv_grid(int64_t B, int64_t D, int64_t L, int64_t span) {
+inline ConvGrid conv_grid(int64_t B, int64_t D, int64_t L, int64_t span, int64_t each = 8) {
   ConvGrid g;
-  const int64_t words = ((L < span ? L : span) + 7) / 8;
+  const int64_t words = ((L < span ? L : span) + each - 1) / each;
   g.lper = 0;
   while (g.lper < 8 && (1 << g.lper) < words) ++g.lper;
   g.per = 1 << g.lper;
@@ -54,12 +54,16 @@ inline ConvGrid conv_grid(int64_t B, int64_t D, int64_t L, int64_t span) {
 // over batch and time leave one partial.  Sequences are spread over
 // workgroups until there are about eight to a compute unit.
 constexpr int64_t kConvSpan = 16384;
+// Steps to a thread of the backward: with up to 4 taps 16, of which 3 more
+// have their p computed again instead of 3 of 8 (45 -> 39 us for 8 x 1536 x
+// 2048 bf16); with more taps 8, for want of registers.
+constexpr int conv_each(int T) { return T <= 4 ? 16 : 8; }
 struct ConvBackwardGrid {
   int per, lper;
   int64_t blocks, groups, seqs, parts;   // blocks along time, groups of sequences
 };
-inline ConvBackwardGrid conv_backward_grid(int64_t B, int64_t D, int64_t L) {
-  const ConvGrid c = conv_grid(B, D, L, kConvStep);
+inline ConvBackwardGrid conv_backward_grid(int64_t B, int64_t D, int64_t L, int T) {
+  const ConvGrid c = conv_grid(B, D, L, kConvSpan, conv_each(T));
   ConvBackwardGrid g;
   g.per = c.per;
   g.lper = c.lper;
