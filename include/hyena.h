@@ -393,7 +393,8 @@ hyena_status hyena_nd_forward(const void* v, const void* const* x, const void* s
  * 4-byte aligned; an output may overlap no input and no other output (ALIAS).
  * Arithmetic is fp32, bf16 values are widened exactly and rounded once, to
  * nearest even, where they are stored.  Sums have a fixed order: equal inputs
- * give equal bits.
+ * give equal bits.  A workspace serves one call at a time: calls, or replays
+ * of captured ones, that may run at once need one each.
  *
  * lengths (device int32 [B], or NULL): sequence b holds min(max(lengths[b],
  * 0), L) steps.  Whatever stands behind them (NaN included) is not read into

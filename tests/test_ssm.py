@@ -179,6 +179,7 @@ SCAN = [
     (2, 4, 1, 16, 1100, True, True, True, True, True, [1100, 600]),    # the time axis split in two
     (1, 2, 1, 5, 2200, True, True, True, True, False, [2100]),
     (1, 40, 1, 16, 260, True, True, True, True, True, None),           # several channel tiles
+    (2, 4000, 2, 16, 20, True, True, True, True, True, [20, 13]),      # rows enough for a wave to hold all states
 ]
 
 
@@ -324,7 +325,7 @@ def test_selective_scan_one_bad_value_stays_behind_its_step():
 @pytest.mark.parametrize("io", ["fp32", "bf16"])
 @pytest.mark.parametrize("residual", [False, True])
 @pytest.mark.parametrize("rows,D", [(1, 1), (3, 5), (17, 8), (2, 127), (5, 128), (3, 129), (4, 512), (7, 513),
-                                    (1030, 40), (3, 1024), (5, 1025), (2, 2048), (3, 2049), (2, 4097), (3, 8192),
+                                    (1030, 40), (5000, 24), (3, 1024), (5, 1025), (2, 2048), (3, 2049), (2, 4097), (3, 8192),
                                     (2, 8200), (5, 20001)])
 def test_rms_norm(rows, D, residual, io):
     t, r = TYPES[io], gen(rows + D)
@@ -416,7 +417,8 @@ def test_quantize_tiny_values():
 # -------------------------------------------------------------- 8-bit product
 
 PRODUCT = [(1, 1, 16), (1, 16, 128), (3, 130, 144), (16, 64, 256), (17, 257, 400), (33, 128, 1024), (64, 100, 128),
-           (65, 65, 2048), (130, 384, 272), (200, 513, 640), (300, 129, 1040), (520, 260, 256)]
+           (65, 65, 2048), (130, 384, 272), (200, 513, 640), (300, 129, 1040), (520, 260, 256),
+           (1800, 1700, 272), (3850, 3333, 144)]              # 128 x 128 and 256 x 256 tiles
 
 
 @pytest.mark.parametrize("io", ["fp32", "bf16"])
@@ -645,6 +647,40 @@ def test_steps_replay_from_a_graph():
         torch.cuda.synchronize()
         assert torch.equal(gy, want[k]), k
     assert torch.equal(gcs, cs) and torch.equal(gss, ss)
+
+
+def test_offsets_beyond_32_bits():
+    """The last rows of arrays of more than 2^31 values are what they are alone."""
+    t, D, L = torch.bfloat16, 1030, 1 << 21
+    x = torch.empty(1, D, L, dtype=t, device=DEV)
+    x.normal_(generator=torch.Generator(device=DEV).manual_seed(3))
+    assert x.numel() > 1 << 31
+    r = gen(15)
+    w = dev(r(D, 4))
+    last = x[:, -2:].contiguous()
+    y = H.short_conv(x, w, silu=True)
+    assert torch.equal(y[:, -2:], H.short_conv(last, w[-2:].contiguous(), silu=True))
+    del y
+    gx, gw, _, _ = H.short_conv_backward(x, w, x, silu=True)
+    gx2, gw2, _, _ = H.short_conv_backward(last, w[-2:].contiguous(), last, silu=True)
+    assert torch.equal(gx[:, -2:], gx2)
+    # the same products, in other partials: 2^21 terms of both signs, chains of 128 in a thread, then sums of those
+    assert torch.allclose(gw[-2:], gw2, rtol=0, atol=200 * EPS32 * float(gw2.abs().max()) * 8)
+    del gx
+    N = 2
+    bm, A = dev(r(1, 1, N, L).to(t)), dev(-torch.rand(D, N) - 0.1)
+    y, h = H.selective_scan(x, x, A, bm, bm, return_state=True)
+    y2, h2 = H.selective_scan(last, last, A[-2:].contiguous(), bm, bm, return_state=True)
+    # segments of other lengths: the state's roundings, as in test_selective_scan, twice; time steps of about 1 here
+    close(h[:, -2:], h2.cpu().double(), 2 * 416, float(h2.abs().max()) + 1, "state")
+    off = (y[:, -2:].float() - y2.float()).abs().max()
+    assert float(off) <= 2 * 2.0 ** -8 * float(y2.float().abs().max())
+    del y
+    rows = x.view(D * 16, L // 16)
+    assert torch.equal(H.rms_norm(rows, dev(torch.ones(L // 16)))[-1], H.rms_norm(rows[-1:].contiguous(), dev(torch.ones(L // 16)))[0])
+    q, s = H.quantize(rows)
+    q2, s2 = H.quantize(rows[-1:].contiguous())
+    assert torch.equal(q[-1].view(torch.uint8), q2[0].view(torch.uint8)) and torch.equal(s[-1], s2[0])
 
 
 def test_a_workspace_of_the_callers():
