@@ -401,7 +401,8 @@ __global__ __launch_bounds__(256) void k_scan_step(ScanArgs a, int W, int lw, fl
 // second joins them along time, both ways, into the state at each chunk's
 // start and the carry at its end; the third then does all chunks at once.
 // Its workgroup stays at one chunk and walks over channels, so that B and C
-// are staged once and the sums over channels stay on the chip.
+// are staged once and the sums over channels stay on the chip.  Rows of one
+// chunk need the third pass only.
 
 // Chunk sums: H, Q [N] and sum dt of 4 channels to a wave.
 template <int IOT>
@@ -560,7 +561,14 @@ __global__ __launch_bounds__(SCAN_THREADS, 3) void k_scan_bwd(ScanArgs a) {
     // this wave's channels only: no other wave reads or writes these words
     for (int n = l; n < N; n += 16) {
       const float A = a.A[(int64_t)d * N + n];
-      sS[cw * N + n] = f32x4v{A, live ? a.hc[r * N + n] : 0.f, live ? a.qc[r * N + n] : 0.f, 0.f};
+      float h = 0.f, q = 0.f;
+      if (live) {
+        const int64_t i = a.chunks > 1 ? r * N + n : ((int64_t)b * a.D + d) * N + n;
+        const float *hp = a.chunks > 1 ? a.hc : a.state, *qp = a.chunks > 1 ? a.qc : a.gstate_out;
+        if (hp) h = hp[i];
+        if (qp) q = qp[i];
+      }
+      sS[cw * N + n] = f32x4v{A, h, q, 0.f};
     }
     const float bias = a.dbias ? a.dbias[d] : 0.f, skip = a.skip ? a.skip[d] : 0.f;
     float u[8], dt[8], du[8], gy[8], y[8], s1[8], s2[8];
@@ -632,7 +640,10 @@ __global__ __launch_bounds__(SCAN_THREADS, 3) void k_scan_bwd(ScanArgs a) {
         for (int k = 0; k < 4; ++k) acc[k] += fold_rows(cc[2 * k], cc[2 * k + 1]);
         sG[n * 64 + lane] = acc;
         gA = row_sum(gA);
-        if (l == 0) sS[cw * N + n][3] = gA;
+        if (l == 0) {
+          sS[cw * N + n][3] = gA;
+          if (a.chunks == 1 && a.gstate && live) a.gstate[((int64_t)b * a.D + d) * N + n] = q;
+        }
       }
       __syncthreads();
     }
@@ -687,14 +698,32 @@ __global__ __launch_bounds__(SCAN_THREADS, 3) void k_scan_bwd(ScanArgs a) {
   }
 }
 
-// gB and gC from the splits' parts: 64 values to a workgroup, 4 threads to a
-// value, whose loads are in flight eight at a time.
+// The sums that are left, in one launch: the first `time_groups` workgroups
+// add up the chunks' parts of gA, gskip and gdelta_bias, the others the
+// splits' parts of gB and gC (256 values at a time, 4 threads to a value,
+// whose loads are in flight eight at a time).
 template <int IOT>
-__global__ __launch_bounds__(256) void k_scan_bwd_sum_bc(ScanArgs a) {
-  __shared__ float lds[3][64];
+__global__ __launch_bounds__(SUM_THREADS) void k_scan_bwd_sums(ScanArgs a, int time_groups) {
+  __shared__ float lds[32][33];
+  if ((int)blockIdx.x < time_groups) {
+    const int64_t DN = (int64_t)a.D * a.N, rows = (int64_t)a.B * a.chunks;
+    // columns: gA's D*N, then gskip's D, then gdelta_bias's D
+    const int64_t i = blockIdx.x * (int64_t)32 + (threadIdx.x & 31);
+    const float* src = nullptr;
+    int64_t stride = a.D;
+    float* dst = nullptr;
+    if (i < DN) { src = a.hc + i; stride = DN; dst = a.gA + i; }
+    else if (i < DN + a.D && a.gskip) { src = a.ps + (i - DN); dst = a.gskip + (i - DN); }
+    else if (i >= DN + a.D && i < DN + 2 * a.D && a.gdbias) { src = a.pb + (i - DN - a.D); dst = a.gdbias + (i - DN - a.D); }
+    const float v = column_sum(src, rows, stride, lds);
+    if (threadIdx.x < 32 && dst) *dst = v;
+    return;
+  }
+  float* part = &lds[0][0];                           // [3][256]
   const int64_t n = (int64_t)a.B * a.G * a.N * a.L;
-  const int c = threadIdx.x & 63, k = threadIdx.x >> 6;
-  for (int64_t first = blockIdx.x * (int64_t)64; first < 2 * n; first += gridDim.x * (int64_t)64) {
+  const int c = threadIdx.x & 255, k = threadIdx.x >> 8;
+  for (int64_t first = ((int64_t)blockIdx.x - time_groups) * 256; first < 2 * n;
+       first += ((int64_t)gridDim.x - time_groups) * 256) {
     const int64_t i = first + c;
     float v = 0.f;
     if (i < 2 * n) {
@@ -709,10 +738,10 @@ __global__ __launch_bounds__(256) void k_scan_bwd_sum_bc(ScanArgs a) {
       }
       for (; s < a.splits; s += 4) v += p[s * 2 * n];
     }
-    if (k > 0) lds[k - 1][c] = v;
+    if (k > 0) part[(k - 1) * 256 + c] = v;
     __syncthreads();
     if (k == 0 && i < 2 * n) {
-      v = (v + lds[0][c]) + (lds[1][c] + lds[2][c]);
+      v = (v + part[c]) + (part[256 + c] + part[512 + c]);
       if (i < n) st1<IOT>(a.gB, i, v);
       else st1<IOT>(a.gC, i - n, v);
     }
@@ -720,34 +749,19 @@ __global__ __launch_bounds__(256) void k_scan_bwd_sum_bc(ScanArgs a) {
   }
 }
 
-// gA, gskip and gdelta_bias from the chunks' parts.
-__global__ __launch_bounds__(SUM_THREADS) void k_scan_bwd_sum_t(ScanArgs a) {
-  __shared__ float lds[32][33];
-  const int64_t DN = (int64_t)a.D * a.N, rows = (int64_t)a.B * a.chunks;
-  // columns: gA's D*N, then gskip's D, then gdelta_bias's D
-  const int64_t i = blockIdx.x * (int64_t)32 + (threadIdx.x & 31);
-  const float* src = nullptr;
-  int64_t stride = a.D;
-  float* dst = nullptr;
-  if (i < DN) { src = a.hc + i; stride = DN; dst = a.gA + i; }
-  else if (i < DN + a.D && a.gskip) { src = a.ps + (i - DN); dst = a.gskip + (i - DN); }
-  else if (i >= DN + a.D && i < DN + 2 * a.D && a.gdbias) { src = a.pb + (i - DN - a.D); dst = a.gdbias + (i - DN - a.D); }
-  const float v = column_sum(src, rows, stride, lds);
-  if (threadIdx.x < 32 && dst) *dst = v;
-}
-
 template <int IOT>
 hipError_t launch_scan_backward(const ScanArgs& a, hipStream_t s) {
   const unsigned wgs = (unsigned)((int64_t)a.B * a.G * a.chunks * a.splits);
   const size_t bc = (size_t)2 * a.N * CH * 4;
-  k_scan_bwd_ends<IOT><<<dim3(wgs), SCAN_THREADS, bc, s>>>(a);
-  k_scan_bwd_join<<<dim3((unsigned)(((int64_t)a.B * a.D * a.N + 255) / 256)), 256, 0, s>>>(a);
-  k_scan_bwd<IOT><<<dim3(wgs), SCAN_THREADS, bc + (size_t)a.N * 64 * 16 + (size_t)TILE * a.N * 16, s>>>(a);
-  if (a.splits > 1) {
-    const int64_t n = (int64_t)2 * a.B * a.G * a.N * a.L;
-    k_scan_bwd_sum_bc<IOT><<<dim3((unsigned)min((n + 63) / 64, (int64_t)1 << 20)), 256, 0, s>>>(a);
+  if (a.chunks > 1) {
+    k_scan_bwd_ends<IOT><<<dim3(wgs), SCAN_THREADS, bc, s>>>(a);
+    k_scan_bwd_join<<<dim3((unsigned)(((int64_t)a.B * a.D * a.N + 255) / 256)), 256, 0, s>>>(a);
   }
-  k_scan_bwd_sum_t<<<dim3((unsigned)(((int64_t)a.D * (a.N + 2) + 31) / 32)), SUM_THREADS, 0, s>>>(a);
+  k_scan_bwd<IOT><<<dim3(wgs), SCAN_THREADS, bc + (size_t)a.N * 64 * 16 + (size_t)TILE * a.N * 16, s>>>(a);
+  const int time_groups = (int)(((int64_t)a.D * (a.N + 2) + 31) / 32);
+  const int64_t n = (int64_t)2 * a.B * a.G * a.N * a.L;
+  const int64_t bc_groups = a.splits > 1 ? min((n + 255) / 256, (int64_t)1 << 18) : 0;
+  k_scan_bwd_sums<IOT><<<dim3((unsigned)(time_groups + bc_groups)), SUM_THREADS, 0, s>>>(a, time_groups);
   return hipGetLastError();
 }
 
