@@ -521,11 +521,13 @@ __device__ __forceinline__ float fold_rows(float x, float y) {
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
-template <int IOT>
-__global__ __launch_bounds__(SCAN_THREADS, 3) void k_scan_bwd(ScanArgs a) {
+// W waves to a workgroup: 4, or 8 where a workgroup's LDS fills a compute unit.
+template <int IOT, int W>
+__global__ __launch_bounds__(64 * W, W == 8 ? 2 : 3) void k_scan_bwd(ScanArgs a) {
+  constexpr int THREADS = 64 * W, TC = 4 * W;
   extern __shared__ float lds[];
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, row = lane >> 4, l = lane & 15;
-  const int N = a.N, Dg = a.D / a.G, tiles = (Dg + TILE - 1) / TILE, per = (tiles + a.splits - 1) / a.splits;
+  const int N = a.N, Dg = a.D / a.G, tiles = (Dg + TC - 1) / TC, per = (tiles + a.splits - 1) / a.splits;
   int id = blockIdx.x;
   const int split = id % a.splits; id /= a.splits;
   const int c = id % a.chunks; id /= a.chunks;
@@ -538,20 +540,20 @@ __global__ __launch_bounds__(SCAN_THREADS, 3) void k_scan_bwd(ScanArgs a) {
   float* sB = lds;                                             // [N][128]
   float* sC = sB + N * CH;                                     // [N][128]
   f32x4v* sG = reinterpret_cast<f32x4v*>(sC + N * CH);         // [N][64 lanes]: sums over channels
-  f32x4v* sS = sG + N * 64;                                    // [16][N]: A log2(e), start state, end carry, gA's part
-  for (int i = tid; i < 2 * N * 16; i += SCAN_THREADS) {
+  f32x4v* sS = sG + N * 64;                                    // [TC][N]: A, start state, end carry, gA's part
+  for (int i = tid; i < 2 * N * 16; i += THREADS) {
     const int v = i & 15, n = i >> 4;
     const bool isC = n >= N;
     float x[8];
     widen8<IOT>(ld8n<IOT>(isC ? a.Cm : a.Bm, bc + (int64_t)(isC ? n - N : n) * L + t0 + 8 * v, len - t0 - 8 * v, bc_total), x);
     stage8(lds + n * CH, v, x);
   }
-  for (int i = tid; i < N * 64; i += SCAN_THREADS) sG[i] = f32x4v{0.f, 0.f, 0.f, 0.f};
+  for (int i = tid; i < N * 64; i += THREADS) sG[i] = f32x4v{0.f, 0.f, 0.f, 0.f};
 
-  const int quarter = (N + 3) / 4;
+  const int share = (N + W - 1) / W;
   const int tile_end = min(tiles, (split + 1) * per);
   for (int tile = split * per; tile < tile_end; ++tile) {
-    const int cw = wave * 4 + row, dg = tile * TILE + cw;
+    const int cw = wave * 4 + row, dg = tile * TC + cw;
     const bool live = dg < Dg;
     const int d = g * Dg + (live ? dg : Dg - 1), mm = live ? m : 0;
     const int64_t at = ((int64_t)b * a.D + d) * L + t, r = ((int64_t)b * a.chunks + c) * a.D + d;
@@ -589,10 +591,10 @@ __global__ __launch_bounds__(SCAN_THREADS, 3) void k_scan_bwd(ScanArgs a) {
       s1[i] = s2[i] = 0.f;
     }
     __syncthreads();
-    // the four waves take the states in turn, so that each sum over channels
+    // the waves take the states in turn, so that each sum over channels
     // has one writer at a time and one order
-    for (int turn = 0; turn < 4; ++turn) {
-      const int first = ((turn + wave) & 3) * quarter, last = min(N, first + quarter);
+    for (int turn = 0; turn < W; ++turn) {
+      const int first = ((turn + wave) & (W - 1)) * share, last = min(N, first + share);
       for (int n = first; n < last; ++n) {
         const f32x4v sc = sS[cw * N + n];
         const float A = sc[0], A2 = A * kLog2e;
@@ -688,7 +690,7 @@ __global__ __launch_bounds__(SCAN_THREADS, 3) void k_scan_bwd(ScanArgs a) {
   // step 8 l + 2 k + (r & 1) of gB (r < 2) or gC
   __syncthreads();
   const float* sg = reinterpret_cast<const float*>(sG);
-  for (int i = tid; i < 2 * N * CH; i += SCAN_THREADS) {
+  for (int i = tid; i < 2 * N * CH; i += THREADS) {
     const int tt = i & (CH - 1), n = (i >> 7) % N, isC = (i >> 7) / N;
     if (t0 + tt >= L) continue;
     const float v = sg[(n * 64 + (isC * 2 + (tt & 1)) * 16 + (tt >> 3)) * 4 + ((tt & 7) >> 1)];
@@ -757,7 +759,9 @@ hipError_t launch_scan_backward(const ScanArgs& a, hipStream_t s) {
     k_scan_bwd_ends<IOT><<<dim3(wgs), SCAN_THREADS, bc, s>>>(a);
     k_scan_bwd_join<<<dim3((unsigned)(((int64_t)a.B * a.D * a.N + 255) / 256)), 256, 0, s>>>(a);
   }
-  k_scan_bwd<IOT><<<dim3(wgs), SCAN_THREADS, bc + (size_t)a.N * 64 * 16 + (size_t)TILE * a.N * 16, s>>>(a);
+  const size_t sums = (size_t)a.N * 64 * 16, state = (size_t)scan_backward_tile(a.N) * a.N * 16;
+  if (scan_backward_tile(a.N) == 32) k_scan_bwd<IOT, 8><<<dim3(wgs), 512, bc + sums + state, s>>>(a);
+  else k_scan_bwd<IOT, 4><<<dim3(wgs), 256, bc + sums + state, s>>>(a);
   const int time_groups = (int)(((int64_t)a.D * (a.N + 2) + 31) / 32);
   const int64_t n = (int64_t)2 * a.B * a.G * a.N * a.L;
   const int64_t bc_groups = a.splits > 1 ? min((n + 255) / 256, (int64_t)1 << 18) : 0;

@@ -152,6 +152,12 @@ inline ScanPlan scan_plan(int64_t B, int64_t D, int64_t N, int64_t L) {
   return best;
 }
 
+// Channels of a workgroup of the backward's last pass.  Its LDS is 2.25 KB to
+// a state (2.5 with 32 channels): beyond 32 states one workgroup fills a
+// compute unit, and 8 waves, two to a SIMD, run it instead of 4 (6144 rows of
+// 2048 steps, 64 states: 1.37 ms with 4, 1.08 ms with 8).
+constexpr int scan_backward_tile(int64_t N) { return N > 32 ? 32 : 16; }
+
 struct ScanBackwardLayout {
   int chunks, splits;
   int64_t hc, qc, dts, ps, pb, gbc, total;   // byte offsets
@@ -160,7 +166,7 @@ struct ScanBackwardLayout {
 inline ScanBackwardLayout scan_backward_layout(int64_t B, int64_t D, int64_t G, int64_t N, int64_t L) {
   ScanBackwardLayout w;
   w.chunks = (int)((L + kScanChunk - 1) / kScanChunk);
-  const int64_t tiles = (D / G + kScanTile - 1) / kScanTile;
+  const int64_t tile = scan_backward_tile(N), tiles = (D / G + tile - 1) / tile;
   int64_t s = (1024 + B * G * w.chunks - 1) / (B * G * w.chunks);
   if (s > tiles) s = tiles;
   const int64_t per = (tiles + s - 1) / s;
