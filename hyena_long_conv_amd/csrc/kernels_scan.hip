@@ -550,6 +550,7 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : 3) void k_scan_bwd(ScanArgs a)
   }
   for (int i = tid; i < N * 64; i += THREADS) sG[i] = f32x4v{0.f, 0.f, 0.f, 0.f};
 
+  __syncthreads();                                    // B, C and the zeros are there; the turns order the rest
   const int share = (N + W - 1) / W;
   const int tile_end = min(tiles, (split + 1) * per);
   for (int tile = split * per; tile < tile_end; ++tile) {
@@ -590,7 +591,6 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : 3) void k_scan_bwd(ScanArgs a)
       sum += dt[i];
       s1[i] = s2[i] = 0.f;
     }
-    __syncthreads();
     // the waves take the states in turn, so that each sum over channels
     // has one writer at a time and one order
     for (int turn = 0; turn < W; ++turn) {
