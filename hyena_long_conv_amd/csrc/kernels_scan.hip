@@ -414,8 +414,8 @@ __global__ __launch_bounds__(256) void k_scan_step(ScanArgs a, int W, int lw, fl
 // are staged once and the sums over channels stay on the chip.  Rows of one
 // chunk need the third pass only.
 //
-// 4 x 1536 x 2048, 16 states, bf16: 87 us for the first pass, 13 for the
-// second, 214 for the third and 9 for the sums (305 in all as a call; 37 at a
+// 4 x 1536 x 2048, 16 states, bf16: 87 us for the first pass, 7 for the
+// second, 214 for the third and 9 for the sums (299 in all as a call; 37 at a
 // copy's rate): vector units 89% and 92% busy, some 75 and 200 instructions
 // to 8 (t, n) of a lane.  Tried for the third pass and slower: sums over
 // channels kept per lane in LDS instead of folded over the wave (15% fewer
@@ -501,31 +501,39 @@ __global__ __launch_bounds__(SCAN_THREADS) void k_scan_bwd_ends(ScanArgs a) {
 }
 
 // Joins the chunks along time: hc becomes the state at each chunk's start,
-// qc the carry that comes in behind its end.  One thread to a state.
+// qc the carry that comes in behind its end.  A thread to a state and a
+// direction (blockIdx.y); 16 chunks are read before the first of them is
+// overwritten, since the time is that of their loads, one after the other.
 __global__ __launch_bounds__(256) void k_scan_bwd_join(ScanArgs a) {
+  constexpr int AHEAD = 16;
   const int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x, DN = (int64_t)a.D * a.N;
   if (i >= a.B * DN) return;
   const int64_t b = i / DN, dn = i - b * DN;
-  const int d = (int)(dn / a.N);
+  const int d = (int)(dn / a.N), chunks = a.chunks;
+  const bool back = blockIdx.y;
   const float A2 = a.A[dn] * kLog2e;
-  float* hc = a.hc + b * a.chunks * DN + dn;
-  float* qc = a.qc + b * a.chunks * DN + dn;
-  const float* dts = a.dts + b * a.chunks * (int64_t)a.D + d;
-  float h = a.state ? a.state[i] : 0.f;
-#pragma unroll 4
-  for (int c = 0; c < a.chunks; ++c) {
-    const float e = hc[c * DN];
-    hc[c * DN] = h;
-    h = fmaf(exp2_fast(A2 * dts[(int64_t)c * a.D]), h, e);
+  float* part = (back ? a.qc : a.hc) + b * chunks * DN + dn;
+  const float* dts = a.dts + b * chunks * (int64_t)a.D + d;
+  const float* start = back ? a.gstate_out : a.state;
+  float v = start ? start[i] : 0.f;
+  for (int c0 = 0; c0 < chunks; c0 += AHEAD) {
+    float e[AHEAD], t[AHEAD];
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      const int c = min(c0 + k, chunks - 1), at = back ? chunks - 1 - c : c;
+      e[k] = part[at * DN];
+      t[k] = dts[(int64_t)at * a.D];
+    }
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      const int c = c0 + k, at = back ? chunks - 1 - c : c;
+      if (c < chunks) {
+        part[at * DN] = v;
+        v = fmaf(exp2_fast(A2 * t[k]), v, e[k]);
+      }
+    }
   }
-  float q = a.gstate_out ? a.gstate_out[i] : 0.f;
-#pragma unroll 4
-  for (int c = a.chunks - 1; c >= 0; --c) {
-    const float e = qc[c * DN];
-    qc[c * DN] = q;
-    q = fmaf(exp2_fast(A2 * dts[(int64_t)c * a.D]), q, e);
-  }
-  if (a.gstate) a.gstate[i] = q;
+  if (back && a.gstate) a.gstate[i] = v;
 }
 
 // x + its partner across the wave's halves, for two values at once: the lower
@@ -776,7 +784,7 @@ hipError_t launch_scan_backward(const ScanArgs& a, hipStream_t s) {
   const size_t bc = (size_t)2 * a.N * CH * 4;
   if (a.chunks > 1) {
     k_scan_bwd_ends<IOT><<<dim3(wgs), SCAN_THREADS, bc, s>>>(a);
-    k_scan_bwd_join<<<dim3((unsigned)(((int64_t)a.B * a.D * a.N + 255) / 256)), 256, 0, s>>>(a);
+    k_scan_bwd_join<<<dim3((unsigned)(((int64_t)a.B * a.D * a.N + 255) / 256), 2), 256, 0, s>>>(a);
   }
   const size_t sums = (size_t)a.N * 64 * 16, state = (size_t)scan_backward_tile(a.N) * a.N * 16;
   if (scan_backward_tile(a.N) == 32) k_scan_bwd<IOT, 8><<<dim3(wgs), 512, bc + sums + state, s>>>(a);

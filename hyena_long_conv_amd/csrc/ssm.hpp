@@ -167,8 +167,15 @@ inline ScanBackwardLayout scan_backward_layout(int64_t B, int64_t D, int64_t G, 
   ScanBackwardLayout w;
   w.chunks = (int)((L + kScanChunk - 1) / kScanChunk);
   const int64_t tile = scan_backward_tile(N), tiles = (D / G + tile - 1) / tile;
-  int64_t s = (1024 + B * G * w.chunks - 1) / (B * G * w.chunks);
-  if (s > tiles) s = tiles;
+  // about 1024 workgroups, four to a compute unit; of up to twice as many, the
+  // number that shares the channels out most evenly (48 channels of 65536
+  // steps: three workgroups of one tile rather than one of two and one of one)
+  int64_t least = (1024 + B * G * w.chunks - 1) / (B * G * w.chunks), s = 1;
+  if (least > tiles) least = tiles;
+  for (int64_t k = least, slots = 0; k <= 2 * least && k <= tiles; ++k) {
+    const int64_t n = (tiles + k - 1) / k * k;
+    if (slots == 0 || n < slots) slots = n, s = k;
+  }
   const int64_t per = (tiles + s - 1) / s;
   w.splits = (int)((tiles + per - 1) / per);
   const auto up = [](int64_t n) { return (n + 255) / 256 * 256; };
