@@ -184,10 +184,13 @@ static int64_t scan_groups(const ScanArgs& a) {
   return (int64_t)a.B * a.G * ((a.D / a.G + tile - 1) / tile);
 }
 
+static int64_t scan_workspace(const ScanPlan& plan, int64_t B, int64_t D, int64_t N) {
+  return plan.segs > 1 ? plan.segs * B * D * (N + 1) * 4 : 0;
+}
+
 int64_t hyena_selective_scan_workspace_bytes(int64_t B, int32_t D, int32_t N, int64_t L) {
   if (!batch_ok(B, D, L) || N < 1 || N > HYENA_MAX_STATE) return -1;
-  const int64_t segs = scan_plan(B, D, N, L).segs;
-  return segs > 1 ? segs * B * D * (N + 1) * 4 : 0;
+  return scan_workspace(scan_plan(B, D, N, L), B, D, N);
 }
 
 hyena_status hyena_selective_scan(const hyena_selective_scan_params* p, void* y, float* state_out, hyena_dtype io,
@@ -200,7 +203,7 @@ hyena_status hyena_selective_scan(const hyena_selective_scan_params* p, void* y,
   a.segs = plan.segs;
   a.seg = plan.seg;
   if (scan_groups(a) * a.segs > kMaxGroups) return HYENA_ERR_UNSUPPORTED;
-  const int64_t need = hyena_selective_scan_workspace_bytes(a.B, a.D, a.N, a.L);
+  const int64_t need = scan_workspace(plan, a.B, a.D, a.N);
   if (need > 0 && (!workspace || workspace_bytes < need)) return HYENA_ERR_WORKSPACE;
   const int64_t e = size_of(io), rows = p->B * a.D, act = rows * a.L * e, bc = p->B * a.G * a.N * a.L * e;
   const int64_t st = rows * a.N * 4;

@@ -155,10 +155,19 @@ __global__ __launch_bounds__(SCAN_THREADS) void k_scan(ScanArgs a) {
       A2 = a.A[(int64_t)ch * N + n] * kLog2e;
       if constexpr (!END) {
         if (a.state) h = a.state[((int64_t)b * a.D + ch) * N + n];
-#pragma unroll 4
-        for (int s = 0; s < seg; ++s) {
-          const int64_t r = ((int64_t)b * a.segs + s) * a.D + ch;
-          h = fmaf(exp2_fast(A2 * a.sdt[r]), h, a.hend[r * N + n]);
+        const float* ends = a.hend + ((int64_t)b * a.segs * a.D + ch) * N + n;
+        const float* sums = a.sdt + (int64_t)b * a.segs * a.D + ch;
+        for (int s0 = 0; s0 < seg; s0 += 16) {        // 16 segments' loads in flight
+          float e[16], t[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const int64_t at = (int64_t)min(s0 + k, seg - 1) * a.D;
+            e[k] = ends[at * N];
+            t[k] = sums[at];
+          }
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+            if (s0 + k < seg) h = fmaf(exp2_fast(A2 * t[k]), h, e[k]);
         }
       }
     }

@@ -138,15 +138,18 @@ inline ScanPlan scan_plan(int64_t B, int64_t D, int64_t N, int64_t L) {
   ScanPlan best{1, 1, chunks * kScanChunk};
   double least = -1;
   for (int split = 1; split <= 4; split *= 4) {
-    for (int64_t s = 1; s <= 64 && s <= chunks; ++s) {
-      const int64_t k = (groups * split * s + 255) / 256, per = (chunks + s - 1) / s;
+    for (int64_t s = 1; s <= 256;) {
+      const int64_t per = (chunks + s - 1) / s;       // s is the least number that gives segments of `per` chunks
+      const int64_t k = (groups * split * s + 255) / 256;
       const double t = k == 1 ? 1.98 : k == 2 ? 2.4 : k == 3 ? 3.15 : (double)k;
       const double work = (split > 1 ? 6.5 : 3.1) + (double)((N + split - 1) / split);
-      const double cost = t * work * (double)per * (s > 1 ? 1.72 : 1.0) + (s > 1 ? 30.0 + 0.7 * (double)s : 0.0);
+      const double cost = t * work * (double)per * (s > 1 ? 1.72 : 1.0) + (s > 1 ? 30.0 + 0.4 * (double)s : 0.0);
       if (least < 0 || cost < least) {
         least = cost;
-        best = ScanPlan{split, (int)((chunks + per - 1) / per), per * kScanChunk};
+        best = ScanPlan{split, (int)s, per * kScanChunk};
       }
+      if (per == 1) break;
+      s = (chunks + per - 2) / (per - 1);
     }
   }
   return best;

@@ -178,6 +178,7 @@ SCAN = [
     (1, 18, 1, 64, 140, True, True, True, True, True, [139]),
     (2, 4, 1, 16, 1100, True, True, True, True, True, [1100, 600]),    # the time axis split in two
     (1, 2, 1, 5, 2200, True, True, True, True, False, [2100]),
+    (1, 2, 1, 3, 5000, True, True, True, True, True, [4700]),          # 40 segments, 40 chunks
     (1, 40, 1, 16, 260, True, True, True, True, True, None),           # several channel tiles
     (2, 4000, 2, 16, 20, True, True, True, True, True, [20, 13]),      # rows enough for a wave to hold all states
 ]
