@@ -161,12 +161,12 @@ template <int IOT, int TT, int E>
 __device__ __forceinline__ void conv_gp(const ConvArgs& a, int64_t r, int t, int len, const float (&w)[TT], float bias,
                                         float (&x)[2 * TT + E], float (&gp)[TT + E]) {
   conv_window<IOT, TT, TT + E>(a, r, t, len, x);
-  const bool whole = t + (TT + E + 7) / 8 * 8 <= len;
+  const bool whole = t >= 0 && t + (TT + E + 7) / 8 * 8 <= len;
 #pragma unroll
   for (int k = 0; k < (TT + E + 7) / 8; ++k) {
     float v[8];
     const int64_t i = r * a.L + t + 8 * k;
-    widen8<IOT>(whole ? ld8<IOT>(a.gy, i) : ld8n<IOT>(a.gy, i, len - t - 8 * k, (int64_t)a.B * a.D * a.L), v);
+    widen8<IOT>(whole ? ld8<IOT>(a.gy, i) : ld8n<IOT>(a.gy, i, t + 8 * k < 0 ? 0 : len - t - 8 * k, (int64_t)a.B * a.D * a.L), v);
 #pragma unroll
     for (int e = 0; e < 8; ++e)
       if (8 * k + e < TT + E) gp[8 * k + e] = v[e];
@@ -178,7 +178,7 @@ __device__ __forceinline__ void conv_gp(const ConvArgs& a, int64_t r, int t, int
 #pragma unroll
       for (int j = 0; j < TT; ++j) p = fmaf(w[j], x[TT + e - j], p);
       const float s = sigmoid_f(p);
-      gp[e] *= s * fmaf(p, 1.f - s, 1.f);                // 0 from len on
+      gp[e] *= s * fmaf(p, 1.f - s, 1.f);                // 0 before 0 and from len on
     }
   }
 }
@@ -199,7 +199,16 @@ __global__ __launch_bounds__(256) void k_conv_bwd(ConvArgs a, ConvBackwardGrid g
   for (int b = (int)(grp * g.seqs) + (tid >> g.lper); b < b_end; b += at_once) {
     const int64_t r = (int64_t)b * a.D + d;
     const int len = conv_length(a, b);
-    for (int t = (int)(xb * kConvSpan) + E * (tid & (per - 1)); t < t_end; t += E * per) {
+    // the row's words, then the carried inputs' (those before t = 0), one or two more to a row
+    const int lane = tid & (per - 1);
+    int t = (int)(xb * kConvSpan) + E * lane;
+    for (bool carried = false;; t += carried ? -E * per : E * per) {
+      if (!carried && t >= t_end) {
+        if (!a.gstate || xb != 0) break;
+        carried = true;
+        t = -E * (lane + 1);
+      }
+      if (carried && t < -E * ((TT + E - 2) / E)) break;
       float gx[E];
 #pragma unroll
       for (int e = 0; e < E; ++e) gx[e] = 0.f;
@@ -226,33 +235,18 @@ __global__ __launch_bounds__(256) void k_conv_bwd(ConvArgs a, ConvBackwardGrid g
           for (int e = 0; e < E; ++e) gx[e] = t + e < len ? gx[e] : 0.f;
         }
       }
+      if (carried) {
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          if (t + e + S >= 0) st1<IOT>(a.gstate, r * S + t + e + S, gx[e]);
+        continue;
+      }
 #pragma unroll
       for (int k = 0; k < E; k += 8) {
         float o[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[e] = gx[k + e];
         if (t + k < a.L) st8n<IOT>(a.gx, r * a.L + t + k, o, (int)min(a.L - t - k, (int64_t)8));
-      }
-    }
-    // the carried inputs: one thread to a row walks over its T-1 values
-    if (a.gstate && xb == 0 && (tid & (per - 1)) == 0) {
-      for (int i = 0; i < S; ++i) {
-        const int t = i - S;                              // gx[t] = sum_j w[j] gp[t+j], t + j in [0, len)
-        float v = 0.f;
-        for (int j = -t; j <= S && t + j < len; ++j) {
-          const int s = t + j;
-          float gp = ld1<IOT>(a.gy, r * a.L + s);
-          if (a.silu) {
-            float p = bias;
-            for (int k = 0; k <= S; ++k) p = fmaf(a.w[(int64_t)d * a.T + k], conv_at<IOT>(a, r, s - k), p);
-            const float sg = sigmoid_f(p);
-            gp *= sg * fmaf(p, 1.f - sg, 1.f);
-          }
-          v = fmaf(a.w[(int64_t)d * a.T + j], gp, v);
-        }
-        // the state left behind still holds this carried input when len < T-1
-        if (a.gstate_out && i >= len) v += ld1<IOT>(a.gstate_out, r * S + i - len);
-        st1<IOT>(a.gstate, r * S + i, v);
       }
     }
   }

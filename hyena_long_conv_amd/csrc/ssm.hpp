@@ -159,7 +159,8 @@ inline ScanPlan scan_plan(int64_t B, int64_t D, int64_t N, int64_t L) {
 // a state (2.5 with 32 channels): beyond 32 states one workgroup fills a
 // compute unit, and 8 waves, two to a SIMD, run it instead of 4 (6144 rows of
 // 2048 steps, 64 states: 1.37 ms with 4, 1.08 ms with 8).
-constexpr int scan_backward_tile(int64_t N) { return N > 32 ? 32 : 16; }
+// A group of up to 16 channels fills no more than 4.
+constexpr int scan_backward_tile(int64_t N, int64_t per_group) { return N > 32 && per_group > 16 ? 32 : 16; }
 
 struct ScanBackwardLayout {
   int chunks, splits;
@@ -169,7 +170,7 @@ struct ScanBackwardLayout {
 inline ScanBackwardLayout scan_backward_layout(int64_t B, int64_t D, int64_t G, int64_t N, int64_t L) {
   ScanBackwardLayout w;
   w.chunks = (int)((L + kScanChunk - 1) / kScanChunk);
-  const int64_t tile = scan_backward_tile(N), tiles = (D / G + tile - 1) / tile;
+  const int64_t tile = scan_backward_tile(N, D / G), tiles = (D / G + tile - 1) / tile;
   // about 1024 workgroups, four to a compute unit; of up to twice as many, the
   // number that shares the channels out most evenly (48 channels of 65536
   // steps: three workgroups of one tile rather than one of two and one of one)
