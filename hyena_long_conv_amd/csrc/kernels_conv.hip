@@ -154,7 +154,7 @@ __global__ __launch_bounds__(256) void k_conv_step(ConvArgs a) {
 // computed again, for a lane's 8 steps and the TT-1 behind them.  A workgroup
 // sums over its sequences and steps in registers and leaves one partial for
 // each tap, which k_conv_sum adds up in a fixed order.  8 x 1536 x 2048 bf16:
-// 39 us and 4.5 for the sums, vector units 85% busy (a p, a sigmoid and a
+// 39 us and 4 for the sums, vector units 85% busy (a p, a sigmoid and a
 // derivative for 19 steps of 16, the sums over taps twice); 31 us at a copy's
 // rate.
 template <int IOT, int TT, int E>

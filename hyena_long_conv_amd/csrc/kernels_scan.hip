@@ -19,7 +19,7 @@
 // Arithmetic bounds it: to 8 (t, n) of a lane 8 products dt A, 9 exponentials
 // (four issue slots each), 8 products with B, 7 + 8 steps of the recurrence, 8
 // with C and about 12 for the row's scan, 88 slots.  8 x 1536 x 2048, 16
-// states, bf16: 134 us, vector units 93% busy; its bytes at a copy's rate are
+// states, bf16: 133 us, vector units 93% busy; its bytes at a copy's rate are
 // 42 us.  (A lane to a channel, with B and C as scalars, would need 64 slots
 // and no scan, but 65536 channels to fill the chip, or a second pass over the
 // exponentials.)
