@@ -179,8 +179,10 @@ __global__ __launch_bounds__(64 * WM * WN) void k_scaled_mm(ScaledArgs a) {
     unsigned char* st = stage + (b & 1) * STAGE;
     lx.issue(st, wave, b * KS, K);
     lw.issue(st + BM * KS, wave, b * KS, K);
+    // the scalar offset is outside the buffer's bounds check, so it stays in the row behind K
     if (wave < BM / 64)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rss, (lds_ptr_t)(st + (BM + BN) * KS + wave * 256), 4, (int)so, 4 * b, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rss, (lds_ptr_t)(st + (BM + BN) * KS + wave * 256), 4, (int)so,
+                                               4 * min(b, kb - 1), 0, 0);
   };
 
   f32x4v acc[IM][IN];
