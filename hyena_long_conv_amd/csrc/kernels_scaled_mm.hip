@@ -395,7 +395,9 @@ hipError_t launch_product(const ScaledArgs& a, hipStream_t s) {
   // 2048 rows 33, 26 and 33 (128 of them; 512 of 128), 1024 rows 30, 18.6 and
   // 17.3 (256 of 128).
   if (a.M <= 64) return launch_rows<IOT, CM>(a, s);
-  if (IOT == 1 && tiles(256, 256) >= 192) return launch_tiles<IOT, CM, IOT ? 8 : 4, 4, 2, IOT ? 4 : 2>(a, s);
+  if constexpr (IOT == 1) {                           // widened operands leave no registers for these
+    if (tiles(256, 256) >= 192) return launch_tiles<IOT, CM, 8, 4, 2, 4>(a, s);
+  }
   if (tiles(128, 128) >= 384) return launch_tiles<IOT, CM, 4, 4, 2, 2>(a, s);
   return launch_tiles<IOT, CM, 2, 2, 2, 2>(a, s);
 }
