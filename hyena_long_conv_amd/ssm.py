@@ -162,12 +162,12 @@ def short_conv(x, w, bias=None, silu: bool = False, state=None, lengths=None, re
     io = _activation(x, "x", 3)
     B, D, L = x.shape
     T, p = _conv_params(x, w, bias, silu, state, lengths, B, D, L)
-    y = out if out is not None else _like(x)
+    y = _like(x) if out is None else out
+    yp = y.data_ptr() if out is None else _take(out, "out", x.shape, x.dtype, x.device)
     if return_state and state_out is None:
         state_out = _new((B, D, T - 1), x.dtype, x.device)
     so = _take(state_out, "state_out", (B, D, T - 1), x.dtype, x.device) if T > 1 else None
-    _call("hyena_short_conv", x.device, x.data_ptr(), ctypes.byref(p), _take(y, "out", x.shape, x.dtype, x.device), so,
-          io)
+    _call("hyena_short_conv", x.device, x.data_ptr(), ctypes.byref(p), yp, so, io)
     return (y, state_out) if return_state else y
 
 
@@ -249,12 +249,13 @@ def selective_scan(u, delta, A, Bm, Cm, skip=None, z=None, delta_bias=None, soft
     B, D, L = u.shape
     N, G, p = _scan_params(u, delta, A, Bm, Cm, skip, z, delta_bias, softplus, state, lengths, B, D, (L,))
     dev = u.device
-    y = out if out is not None else _like(u)
+    y = _like(u) if out is None else out
+    yp = y.data_ptr() if out is None else _take(out, "out", u.shape, u.dtype, dev)
     if return_state and state_out is None:
         state_out = _new((B, D, N), torch.float32, dev)
     keep, ws, wsb = _workspace(workspace, selective_scan_workspace_bytes(B, D, N, L),
                                "hyena_selective_scan_workspace_bytes", dev)
-    _call("hyena_selective_scan", dev, ctypes.byref(p), _take(y, "out", u.shape, u.dtype, dev),
+    _call("hyena_selective_scan", dev, ctypes.byref(p), yp,
           _take(state_out, "state_out", (B, D, N), torch.float32, dev), io, ws, wsb)
     return (y, state_out) if return_state else y
 
@@ -317,11 +318,12 @@ def rms_norm(x, weight, residual=None, eps: float = 1e-6, out=None):
     torch = _torch()
     io, rows, D = _rows(x, "x")
     dev = x.device
-    y = out if out is not None else _like(x)
+    y = _like(x) if out is None else out
+    yp = y.data_ptr() if out is None else _take(out, "out", x.shape, x.dtype, dev)
     s = _like(x) if residual is not None else None
     _call("hyena_rms_norm", dev, x.data_ptr(), _take(residual, "residual", x.shape, x.dtype, dev),
-          _take(weight, "weight", (D,), torch.float32, dev), _take(y, "out", x.shape, x.dtype, dev),
-          s.data_ptr() if s is not None else None, rows, D, eps, io)
+          _take(weight, "weight", (D,), torch.float32, dev), yp, s.data_ptr() if s is not None else None, rows, D, eps,
+          io)
     return (y, s) if residual is not None else y
 
 
@@ -411,9 +413,10 @@ def scaled_matmul(q, scales, wq, wscales, bias=None, out_dtype=None, channel_maj
     if out_dtype not in (torch.float32, torch.bfloat16):
         raise TypeError("out_dtype must be float32 or bfloat16")
     shape = (*q.shape[:-2], N, L) if channel_major else (*q.shape[:-1], N)
-    o = out if out is not None else _new(shape, out_dtype, dev)
+    o = _new(shape, out_dtype, dev) if out is None else out
+    op = o.data_ptr() if out is None else _take(out, "out", shape, out_dtype, dev)
     _call("hyena_scaled_matmul", dev, q.data_ptr(), _take(scales, "scales", (*q.shape[:-1], kb), f32, dev),
           _take(wq, "wq", (N, K), e4m3, dev), _take(wscales, "wscales", (-(-N // 128), kb), f32, dev),
-          _take(bias, "bias", (N,), f32, dev), _take(o, "out", shape, out_dtype, dev), B, L, N, K,
-          int(bool(channel_major)), _H.HYENA_FP32 if out_dtype == f32 else _H.HYENA_BF16)
+          _take(bias, "bias", (N,), f32, dev), op, B, L, N, K, int(bool(channel_major)),
+          _H.HYENA_FP32 if out_dtype == f32 else _H.HYENA_BF16)
     return o
