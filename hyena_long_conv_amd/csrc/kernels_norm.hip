@@ -275,7 +275,8 @@ __global__ __launch_bounds__(NORM_THREADS) void k_norm_bwd(NormArgs a) {
     }
     ss = group_sum<LANES>(ss, lds);
     dot = group_sum<LANES>(dot, lds);
-    const float r = 1.f / sqrtf(ss / (float)D + a.eps), m = dot * r * r / (float)D;
+    // a place behind the last row has no sum to divide by, and with eps = 0 nothing to add
+    const float r = live ? 1.f / sqrtf(ss / (float)D + a.eps) : 0.f, m = dot * r * r / (float)D;
 #pragma unroll
     for (int k = 0; k < V; ++k) {
       const int w = lane + LANES * k, n = live ? D - 8 * w : 0;
