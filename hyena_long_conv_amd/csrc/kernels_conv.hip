@@ -5,9 +5,11 @@
 //
 // per channel; x[-1], x[-2], .. come from a carried state (zeros without
 // one), and the last T-1 inputs are what the next call carries.  Taps are
-// rounded up to TT = 4, 8 or 16 with zero weights.  A thread holds 8
+// rounded up to TT = 4, 8 or 16 in the registers.  A thread holds 8
 // consecutive outputs of a row and reads the TT values before them again,
-// from the cache that its neighbours' loads have filled.  8 x 1536 x 2048 bf16,
+// from the cache that its neighbours' loads have filled.  The taps behind T are
+// passed over, not multiplied by zero: an infinity or NaN there is not theirs.
+// The condition is the same for all lanes.  8 x 1536 x 2048 bf16,
 // 4 taps, with silu: 21 us, 4.9 TB/s of x and y, a copy's rate; the vector
 // units are busy 97% of that time (the sigmoid is a third of it), so the two
 // bounds meet here.
@@ -109,11 +111,16 @@ __global__ __launch_bounds__(256) void k_conv(ConvArgs a, int per, int lper, int
     conv_window<IOT, TT, 8>(a, r, t, len, x);
     const float bias = a.bias ? a.bias[d] : 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      float p = bias;
+    for (int e = 0; e < 8; ++e) y[e] = bias;
 #pragma unroll
-      for (int j = 0; j < TT; ++j) p = fmaf(w[j], x[TT + e - j], p);
-      y[e] = a.silu ? p * sigmoid_f(p) : p;
+    for (int j = 0; j < TT; ++j)
+      if (j < a.T) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = fmaf(w[j], x[TT + e - j], y[e]);
+      }
+    if (a.silu) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] *= sigmoid_f(y[e]);
     }
     if (t + 8 > len) {
 #pragma unroll
@@ -157,7 +164,7 @@ __global__ __launch_bounds__(256) void k_conv_step(ConvArgs a) {
 // 39 us and 4 for the sums, vector units 85% busy (a p, a sigmoid and a
 // derivative for 19 steps of 16, the sums over taps twice); 31 us at a copy's
 // rate.
-template <int IOT, int TT, int E>
+template <int IOT, int TT, int E, bool EXACT>
 __device__ __forceinline__ void conv_gp(const ConvArgs& a, int64_t r, int t, int len, const float (&w)[TT], float bias,
                                         float (&x)[2 * TT + E], float (&gp)[TT + E]) {
   conv_window<IOT, TT, TT + E>(a, r, t, len, x);
@@ -172,18 +179,27 @@ __device__ __forceinline__ void conv_gp(const ConvArgs& a, int64_t r, int t, int
       if (8 * k + e < TT + E) gp[8 * k + e] = v[e];
   }
   if (a.silu) {
+    float p[TT + E - 1];
+#pragma unroll
+    for (int e = 0; e < TT + E - 1; ++e) p[e] = bias;
+#pragma unroll
+    for (int j = 0; j < TT; ++j)
+      if (EXACT || j < a.T) {
+#pragma unroll
+        for (int e = 0; e < TT + E - 1; ++e) p[e] = fmaf(w[j], x[TT + e - j], p[e]);
+      }
 #pragma unroll
     for (int e = 0; e < TT + E - 1; ++e) {
-      float p = bias;
-#pragma unroll
-      for (int j = 0; j < TT; ++j) p = fmaf(w[j], x[TT + e - j], p);
-      const float s = sigmoid_f(p);
-      gp[e] *= s * fmaf(p, 1.f - s, 1.f);                // 0 before 0 and from len on
+      const float s = sigmoid_f(p[e]);
+      gp[e] *= s * fmaf(p[e], 1.f - s, 1.f);             // 0 before 0 and from len on
     }
   }
 }
 
-template <int IOT, int TT>
+// EXACT: T = TT, and no condition at each tap (8 x 1536 x 2048 bf16, 16 taps:
+// 117 us, 131 with the conditions; 13 taps, which need them, 125; with up to 8
+// taps no difference).
+template <int IOT, int TT, bool EXACT>
 __global__ __launch_bounds__(256) void k_conv_bwd(ConvArgs a, ConvBackwardGrid g) {
   constexpr int E = conv_each(TT);
   __shared__ float part[4][TT + 1];
@@ -214,14 +230,18 @@ __global__ __launch_bounds__(256) void k_conv_bwd(ConvArgs a, ConvBackwardGrid g
       for (int e = 0; e < E; ++e) gx[e] = 0.f;
       if (t < len) {
         float x[2 * TT + E], gp[TT + E];
-        conv_gp<IOT, TT, E>(a, r, t, len, w, bias, x, gp);
+        conv_gp<IOT, TT, E, EXACT>(a, r, t, len, w, bias, x, gp);
+#pragma unroll
+        for (int j = 0; j < TT; ++j)
+          if (EXACT || j < a.T) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) gx[e] = fmaf(w[j], gp[e + j], gx[e]);
+          }
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-#pragma unroll
-          for (int j = 0; j < TT; ++j) gx[e] = fmaf(w[j], gp[e + j], gx[e]);
           sum[TT] += gp[e];
 #pragma unroll
-          for (int j = 0; j < TT; ++j) sum[j] = fmaf(gp[e], x[TT + e - j], sum[j]);
+          for (int j = 0; j < TT; ++j) sum[j] = fmaf(gp[e], x[TT + e - j], sum[j]);    // those behind T are not used
         }
         if (a.gstate_out && t + E > len - S) {
 #pragma unroll
@@ -294,8 +314,13 @@ void conv_step_tt(const ConvArgs& a, hipStream_t s) {
 template <int TT>
 void conv_backward_tt(const ConvArgs& a, const ConvBackwardGrid& g, hipStream_t s) {
   const unsigned n = (unsigned)(g.parts * a.D);
-  if (a.io) k_conv_bwd<1, TT><<<n, 256, 0, s>>>(a, g);
-  else k_conv_bwd<0, TT><<<n, 256, 0, s>>>(a, g);
+  if (a.T == TT) {
+    if (a.io) k_conv_bwd<1, TT, true><<<n, 256, 0, s>>>(a, g);
+    else k_conv_bwd<0, TT, true><<<n, 256, 0, s>>>(a, g);
+  } else {
+    if (a.io) k_conv_bwd<1, TT, false><<<n, 256, 0, s>>>(a, g);
+    else k_conv_bwd<0, TT, false><<<n, 256, 0, s>>>(a, g);
+  }
 }
 
 }  // namespace

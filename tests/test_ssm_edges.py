@@ -9,6 +9,14 @@ from tests import ssm_reference as R
 from tests.test_ssm import TYPES, close, dev, gen, leaves
 
 pytestmark = pytest.mark.gpu
+NAN, INF = float("nan"), float("inf")
+
+
+def same(a, b, what):
+    """Equal bits, or both None."""
+    assert (a is None) == (b is None), what
+    if a is not None:
+        assert torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8)), what
 
 
 # -------------------------------------------------------------- residual norm
@@ -31,3 +39,41 @@ def test_norm_backward_without_eps(rows, D, io):
     big = rr * (R.up(w).abs() * R.up(gy).abs()).amax(-1, keepdim=True) * 4
     close(gx, v["s"].grad, 4 * c + 16, big, "gx")
     close(gw, v["w"].grad, c + 8 + rows / 256 + 16, (R.up(gy).abs() * (R.up(s) * rr).abs()).sum(0), "gw")
+
+
+# --------------------------------------------------------- short convolution
+
+@pytest.mark.parametrize("bad", [NAN, INF])
+@pytest.mark.parametrize("silu", [False, True])
+@pytest.mark.parametrize("T", [1, 2, 3, 4, 5, 7, 8, 9, 13, 16])
+def test_short_conv_bad_value_reaches_its_own_taps(T, silu, bad):
+    """x[t] is read by y[t .. t+T-1] alone, and gy[t] by gx[t-T+1 .. t]."""
+    r = gen(T)
+    B, D, L, at = 2, 5, 70, 37
+    x, w, bias, gy = r(B, D, L), r(D, T), r(D), r(B, D, L)
+    clean = H.short_conv(dev(x), dev(w), dev(bias), silu=silu)
+    gclean = H.short_conv_backward(dev(x), dev(w), dev(gy), dev(bias), silu=silu)
+    xb, gb = x.clone(), gy.clone()
+    xb[1, 2, at], gb[1, 2, at] = bad, bad
+    got = H.short_conv(dev(xb), dev(w), dev(bias), silu=silu)
+    reach = torch.zeros(B, D, L, dtype=torch.bool)
+    reach[1, 2, at:at + T] = True
+    same(got.cpu()[~reach], clean.cpu()[~reach], "y elsewhere")
+    if bad != bad:
+        assert bool(got.cpu()[reach].isnan().all())
+    else:
+        assert not bool((got.cpu()[reach].abs() < 1e30).any() and not silu)
+    # the loss's gradient: through gy, taps ahead of it
+    g = H.short_conv_backward(dev(x), dev(w), dev(gb), dev(bias), silu=silu)
+    reach = torch.zeros(B, D, L, dtype=torch.bool)
+    reach[1, 2, max(0, at - T + 1):at + 1] = True
+    same(g[0].cpu()[~reach], gclean[0].cpu()[~reach], "gx elsewhere, a bad gy")
+    assert not bool(g[0].cpu()[reach].isfinite().any())
+    keep = [d for d in range(D) if d != 2]
+    same(g[1][keep], gclean[1][keep], "gw of other channels")
+    # through x: nothing of gx without an activation, and the taps on both sides of it with one
+    g = H.short_conv_backward(dev(xb), dev(w), dev(gy), dev(bias), silu=silu)
+    reach = torch.zeros(B, D, L, dtype=torch.bool)
+    if silu:
+        reach[1, 2, max(0, at - T + 1):at + T] = True
+    same(g[0].cpu()[~reach], gclean[0].cpu()[~reach], "gx elsewhere, a bad x")
