@@ -196,9 +196,8 @@ __device__ __forceinline__ void conv_gp(const ConvArgs& a, int64_t r, int t, int
   }
 }
 
-// EXACT: T = TT, and no condition at each tap (8 x 1536 x 2048 bf16, 16 taps:
-// 117 us, 131 with the conditions; 13 taps, which need them, 125; with up to 8
-// taps no difference).
+// EXACT: T = TT, and no condition at each tap (8 x 1536 x 2048 bf16: 16 taps
+// 104 us, 13 taps, which need the conditions, 126; no difference with up to 8).
 template <int IOT, int TT, bool EXACT>
 __global__ __launch_bounds__(256) void k_conv_bwd(ConvArgs a, ConvBackwardGrid g) {
   constexpr int E = conv_each(TT);
@@ -228,7 +227,8 @@ __global__ __launch_bounds__(256) void k_conv_bwd(ConvArgs a, ConvBackwardGrid g
       float gx[E];
 #pragma unroll
       for (int e = 0; e < E; ++e) gx[e] = 0.f;
-      if (t < len) {
+      // an empty sequence's state is handed on and read by no output: it may hold anything
+      if (t < len && len > 0) {
         float x[2 * TT + E], gp[TT + E];
         conv_gp<IOT, TT, E, EXACT>(a, r, t, len, w, bias, x, gp);
 #pragma unroll
@@ -243,6 +243,8 @@ __global__ __launch_bounds__(256) void k_conv_bwd(ConvArgs a, ConvBackwardGrid g
 #pragma unroll
           for (int j = 0; j < TT; ++j) sum[j] = fmaf(gp[e], x[TT + e - j], sum[j]);    // those behind T are not used
         }
+      }
+      if (t < len) {
         if (a.gstate_out && t + E > len - S) {
 #pragma unroll
           for (int e = 0; e < E; ++e) {

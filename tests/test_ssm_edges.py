@@ -77,3 +77,26 @@ def test_short_conv_bad_value_reaches_its_own_taps(T, silu, bad):
     if silu:
         reach[1, 2, max(0, at - T + 1):at + T] = True
     same(g[0].cpu()[~reach], gclean[0].cpu()[~reach], "gx elsewhere, a bad x")
+
+
+@pytest.mark.parametrize("io", ["fp32", "bf16"])
+@pytest.mark.parametrize("silu", [False, True])
+@pytest.mark.parametrize("T", [2, 4, 7, 16])
+def test_short_conv_empty_sequence_with_any_state(T, silu, io):
+    """A sequence of no steps hands its state on and adds nothing to a gradient, whatever the state holds."""
+    t, r = TYPES[io], gen(T)
+    B, D, L = 3, 6, 40
+    x, w, bias, gy = r(B, D, L).to(t), r(D, T), r(D), r(B, D, L).to(t)
+    state, gso = r(B, D, T - 1).to(t), r(B, D, T - 1).to(t)
+    lengths = dev(torch.tensor([0, 40, 3], dtype=torch.int32))
+    bad = state.clone()
+    bad[0, ::2], bad[0, 1::2] = NAN, INF
+    out = []
+    for s in (state, bad):
+        y, last = H.short_conv(dev(x), dev(w), dev(bias), silu=silu, state=dev(s), lengths=lengths, return_state=True)
+        same(last[0], dev(s)[0], "the state of an empty sequence")
+        out.append((y, *H.short_conv_backward(dev(x), dev(w), dev(gy), dev(bias), silu=silu, state=dev(s), lengths=lengths,
+                                              gstate_out=dev(gso))))
+    for name, a, b in zip(("y", "gx", "gw", "gbias", "gstate"), *out):
+        same(a, b, name)
+    same(out[0][4][0], dev(gso)[0], "gstate of an empty sequence")
