@@ -588,7 +588,27 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : 3) void k_scan_bwd(ScanArgs a)
 
   __syncthreads();                                    // B, C and the zeros are there; the turns order the rest
   const int share = (N + W - 1) / W;
-  const int tile_end = min(tiles, (split + 1) * per);
+  int tile_end = min(tiles, (split + 1) * per);
+  if (t0 >= len) {
+    // Behind the sequence: zeros, without a look at the state, which an empty
+    // sequence only hands on and which may hold anything.
+    const int first = split * per * TC, count = min(Dg, tile_end * TC) - first;
+    const int64_t ch = (int64_t)b * a.D + g * Dg + first, rc = ((int64_t)b * a.chunks + c) * a.D + g * Dg + first;
+    const float none[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int i = tid; i < count * N; i += THREADS) {
+      a.hc[rc * N + i] = 0.f;
+      if (a.chunks == 1 && a.gstate) a.gstate[ch * N + i] = a.gstate_out ? a.gstate_out[ch * N + i] : 0.f;
+    }
+    for (int i = tid; i < count; i += THREADS) a.ps[rc + i] = a.pb[rc + i] = 0.f;
+    if (room > 0)                                     // THREADS is a multiple of 16: a thread keeps its steps
+      for (int i = tid >> 4; i < count; i += THREADS / 16) {
+        const int64_t at = (ch + i) * L + t;
+        if (a.z) st8n<IOT>(a.gz, at, none, room);
+        st8n<IOT>(a.gu, at, none, room);
+        st8n<IOT>(a.gdelta, at, none, room);
+      }
+    tile_end = 0;                                     // no tile; gB and gC below
+  }
   for (int tile = split * per; tile < tile_end; ++tile) {
     const int cw = wave * 4 + row, dg = tile * TC + cw;
     const bool live = dg < Dg;
@@ -729,7 +749,7 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : 3) void k_scan_bwd(ScanArgs a)
   for (int i = tid; i < 2 * N * CH; i += THREADS) {
     const int tt = i & (CH - 1), n = (i >> 7) % N, isC = (i >> 7) / N;
     if (t0 + tt >= L) continue;
-    const float v = sg[(n * 64 + (isC * 2 + (tt & 1)) * 16 + (tt >> 3)) * 4 + ((tt & 7) >> 1)];
+    const float v = t0 + tt < len ? sg[(n * 64 + (isC * 2 + (tt & 1)) * 16 + (tt >> 3)) * 4 + ((tt & 7) >> 1)] : 0.f;
     const int64_t o = bc + (int64_t)n * L + t0 + tt;
     if (a.splits > 1) a.gbc[((int64_t)(split * 2 + isC) * a.B * a.G) * N * L + o] = v;
     else st1<IOT>(isC ? a.gC : a.gB, o, v);

@@ -6,7 +6,7 @@ import torch
 
 import hyena_long_conv_amd as H
 from tests import ssm_reference as R
-from tests.test_ssm import TYPES, close, dev, gen, leaves
+from tests.test_ssm import TYPES, close, dev, gen, leaves, scan_inputs, scan_on_gpu
 
 pytestmark = pytest.mark.gpu
 NAN, INF = float("nan"), float("inf")
@@ -100,3 +100,30 @@ def test_short_conv_empty_sequence_with_any_state(T, silu, io):
     for name, a, b in zip(("y", "gx", "gw", "gbias", "gstate"), *out):
         same(a, b, name)
     same(out[0][4][0], dev(gso)[0], "gstate of an empty sequence")
+
+
+# ------------------------------------------------------------ selective scan
+
+GRADS = ("gu", "gdelta", "gA", "gB", "gC", "gskip", "gz", "gdelta_bias", "gstate")
+
+
+@pytest.mark.parametrize("io", ["fp32", "bf16"])
+@pytest.mark.parametrize("D,G,N,L", [(6, 2, 5, 60), (18, 1, 40, 60), (6, 2, 16, 300), (40, 1, 40, 300), (4, 1, 16, 2100)])
+def test_selective_scan_empty_sequence_with_any_state(D, G, N, L, io):
+    """A sequence of no steps hands its state on and adds nothing to a gradient, whatever the state holds."""
+    t, r = TYPES[io], gen(N + L)
+    B = 3
+    a, lengths, _ = scan_inputs((B, D, G, N, L, True, True, True, True, True, [L, 0, L // 2]), t, L)
+    gy, gso = dev(r(B, D, L).to(t)), dev(r(B, D, N))
+    out = []
+    for bad in (False, True):
+        if bad:
+            a["state"][1, ::2], a["state"][1, 1::2] = NAN, INF
+        on = scan_on_gpu(a, lengths, True)
+        y, h = H.selective_scan(**on, return_state=True)
+        same(h[1], on["state"][1], "the state of an empty sequence")
+        out.append((y, H.selective_scan_backward(**on, gy=gy, gstate_out=gso)))
+    same(out[0][0], out[1][0], "y")
+    for k in GRADS:
+        same(out[0][1][k], out[1][1][k], k)
+    same(out[0][1]["gstate"][1], gso[1], "gstate of an empty sequence")
