@@ -731,6 +731,13 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : 3) void k_scan_bwd(ScanArgs a)
       sb += gd;
       s1[i] = fmaf(s1[i], dt[i], skip * gy[i]);
     }
+    if (mm < 8) {                                     // zeros behind the sequence, whatever its state and carry are
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (a.z) gz[i] = i < mm ? gz[i] : 0.f;
+        s1[i] = i < mm ? s1[i] : 0.f;
+      }
+    }
     sk = row_sum(sk);
     sb = row_sum(sb);
     if (live) {

@@ -127,3 +127,29 @@ def test_selective_scan_empty_sequence_with_any_state(D, G, N, L, io):
     for k in GRADS:
         same(out[0][1][k], out[1][1][k], k)
     same(out[0][1]["gstate"][1], gso[1], "gstate of an empty sequence")
+
+
+@pytest.mark.parametrize("io", ["fp32", "bf16"])
+@pytest.mark.parametrize("D,G,N,L", [(6, 2, 5, 60), (18, 1, 40, 60), (6, 2, 16, 300), (40, 1, 40, 300)])
+def test_selective_scan_gradients_behind_a_length_are_zeros(D, G, N, L, io):
+    """Also behind a sequence whose own values, or whose later gradient, are not finite."""
+    t, r = TYPES[io], gen(N * L)
+    B = 2
+    lens = [L - 30, 20]
+    a, lengths, _ = scan_inputs((B, D, G, N, L, True, True, True, True, True, lens), t, L)
+    gy, gso = dev(r(B, D, L).to(t)), r(B, D, N)
+    for where in ("u", "state", "gstate_out"):
+        b, g = {k: v.clone() for k, v in a.items()}, gso.clone()
+        if where == "gstate_out":
+            g[:, 1] = NAN
+        elif where == "u":
+            b["u"][0, 1, L - 32], b["u"][1, 1, 3] = NAN, INF
+        else:
+            b["state"][:, 1] = INF
+        on = scan_on_gpu(b, lengths, True)
+        y = H.selective_scan(**on)
+        out = H.selective_scan_backward(**on, gy=gy, gstate_out=dev(g))
+        for i, n in enumerate(lens):
+            assert not bool((y[i, :, n:] != 0).any()), (where, "y")
+            for k in ("gu", "gdelta", "gz", "gB", "gC"):
+                assert not bool((out[k][i, ..., n:] != 0).any()), (where, k)
