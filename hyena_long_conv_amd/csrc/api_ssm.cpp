@@ -255,7 +255,10 @@ hyena_status hyena_selective_scan_backward(const hyena_selective_scan_params* p,
   if (workspace_bytes < w.total) return HYENA_ERR_WORKSPACE;
   const int64_t e = size_of(io), rows = p->B * a.D, act = rows * a.L * e, bc = p->B * a.G * a.N * a.L * e;
   const int64_t st = rows * a.N * 4, dn = (int64_t)a.D * a.N * 4, dv = (int64_t)a.D * 4;
-  if (p->B * a.G * w.chunks * w.splits > kMaxGroups || rows * a.N / 256 >= kMaxGroups) return HYENA_ERR_UNSUPPORTED;
+  // a workgroup of 32 channels has 512 threads, kMaxGroups counts 256
+  const int64_t size = scan_backward_tile(a.N, a.D / a.G) / 16;
+  if (p->B * a.G * w.chunks * w.splits * size > kMaxGroups || rows * a.N / 256 >= kMaxGroups)
+    return HYENA_ERR_UNSUPPORTED;
   const Span out[] = {{g->gu, act, 16}, {g->gdelta, act, 16}, {g->gz, act, 16}, {g->gB, bc, 16}, {g->gC, bc, 16},
                       {g->gA, dn, 4}, {g->gskip, dv, 4}, {g->gdelta_bias, dv, 4}, {g->gstate, st, 16},
                       {workspace, w.total, 16}};
