@@ -818,14 +818,18 @@ template <int IOT>
 hipError_t launch_scan_backward(const ScanArgs& a, hipStream_t s) {
   const unsigned wgs = (unsigned)((int64_t)a.B * a.G * a.chunks * a.splits);
   const size_t bc = (size_t)2 * a.N * CH * 4;
+  hipError_t e;
   if (a.chunks > 1) {
     k_scan_bwd_ends<IOT><<<dim3(wgs), SCAN_THREADS, bc, s>>>(a);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
     k_scan_bwd_join<<<dim3((unsigned)(((int64_t)a.B * a.D * a.N + 255) / 256), 2), 256, 0, s>>>(a);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   const size_t sums = (size_t)a.N * 64 * 16, tile = scan_backward_tile(a.N, a.D / a.G);
   const size_t state = tile * a.N * 16;
   if (tile == 32) k_scan_bwd<IOT, 8><<<dim3(wgs), 512, bc + sums + state, s>>>(a);
   else k_scan_bwd<IOT, 4><<<dim3(wgs), 256, bc + sums + state, s>>>(a);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
   const int time_groups = (int)(((int64_t)a.D * (a.N + 2) + 31) / 32);
   const int64_t n = (int64_t)2 * a.B * a.G * a.N * a.L;
   const int64_t bc_groups = a.splits > 1 ? min((n + 255) / 256, (int64_t)1 << 18) : 0;
