@@ -394,9 +394,11 @@ hyena_status hyena_scaled_matmul(const void* q, const float* scales, const void*
                                  const float* bias, void* out, int64_t B, int64_t L, int32_t N, int32_t K,
                                  int32_t channel_major, hyena_dtype io, void* stream) {
   if (!q || !scales || !wq || !wscales || !out) return HYENA_ERR_NULL;
-  if (B < 1 || B > kMaxDim || L < 1 || L > HYENA_MAX_L || B * L > ((int64_t)1 << 31) || N < 1 || N > kMaxDim || K < 1 ||
-      K > kMaxDim)
+  constexpr int64_t kRows = (int64_t)1 << 31;
+  if (B < 1 || B > kRows || L < 1 || L > kRows || B * L > kRows || N < 1 || N > kMaxDim || K < 1 || K > kMaxDim)
     return HYENA_ERR_SHAPE;
+  // sequences are told apart in the channel-major layout only
+  if (channel_major && (B > kMaxDim || L > HYENA_MAX_L)) return HYENA_ERR_SHAPE;
   if (K % 16 || (channel_major != 0 && channel_major != 1) || !io_ok(io)) return HYENA_ERR_UNSUPPORTED;
   const int64_t M = B * L, kb = (K + 127) / 128;
   if (((M + 63) / 64) * ((N + 63) / 64) > kMaxGroups) return HYENA_ERR_UNSUPPORTED;

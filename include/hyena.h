@@ -553,7 +553,8 @@ hyena_status hyena_rms_norm_backward(const void* s, const float* weight, const v
  * for a bf16 output by the 8-bit instructions, whose sums are good to about
  * 2^-16 of the terms' sizes.  M = B * L rows of
  * tokens; out is [B][L][N], or with channel_major [B][N][L], the layout of
- * the operators above, in the I/O dtype.  K a multiple of 16 (UNSUPPORTED
+ * the operators above, in the I/O dtype.  M <= 2^31, whatever B and L are
+ * unless channel_major; K a multiple of 16 (UNSUPPORTED
  * otherwise), K, N <= 2^20, out 16-byte aligned.  It serves a product's
  * forward, and the gradient of its left operand with the transposed weight's
  * codes.

@@ -6,7 +6,7 @@ import torch
 
 import hyena_long_conv_amd as H
 from tests import ssm_reference as R
-from tests.test_ssm import TYPES, close, dev, gen, leaves, scan_inputs, scan_on_gpu
+from tests.test_ssm import DEV, TYPES, close, dev, gen, leaves, scan_inputs, scan_on_gpu
 
 pytestmark = pytest.mark.gpu
 NAN, INF = float("nan"), float("inf")
@@ -153,3 +153,21 @@ def test_selective_scan_gradients_behind_a_length_are_zeros(D, G, N, L, io):
             assert not bool((y[i, :, n:] != 0).any()), (where, "y")
             for k in ("gu", "gdelta", "gz", "gB", "gC"):
                 assert not bool((out[k][i, ..., n:] != 0).any()), (where, k)
+
+
+# -------------------------------------------------------------- 8-bit product
+
+def test_scaled_matmul_more_rows_than_a_sequence_holds():
+    """A left of [M, K] counts its rows together: M beyond the longest sequence's 2^22 steps."""
+    M, N, K = (1 << 22) + 77, 32, 16
+    g = torch.Generator(device=DEV).manual_seed(5)
+    q, s = H.quantize(torch.randn(M, K, generator=g, device=DEV))
+    wq, ws = H.quantize(torch.randn(N, K, generator=g, device=DEV), 128)
+    got = H.scaled_matmul(q, s, wq, ws)
+    assert got.shape == (M, N)
+    for lo, hi in ((0, 300), (M - 300, M)):
+        # tiles of other sizes hold the same sums of one block
+        same(got[lo:hi], H.scaled_matmul(q[lo:hi].contiguous(), s[lo:hi].contiguous(), wq, ws), (lo, hi))
+    with pytest.raises(H.HyenaError) as e:
+        H.scaled_matmul(q, s, wq, ws, channel_major=True)     # there the rows are one sequence
+    assert e.value.code == 2
