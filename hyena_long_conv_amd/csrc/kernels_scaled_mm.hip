@@ -47,15 +47,22 @@ __device__ __forceinline__ bf16x8v widen_codes(int lo, int hi) {
   return bf16x8v{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-// The sum over one block of 128.  The 8-bit matrix instructions drop low bits
-// when they add up the products of a step: 1.4e-5 of the result's norm on
-// normal data, far below a bf16 output's half step (2e-3) but not below an
-// fp32 output's, which takes the codes as bf16 through the bf16 instructions
-// (1e-8) at half their rate.
-template <int IOT>
+// The sum over one block of 128: with SUM32 in fp32, the codes widened to
+// bf16 and multiplied by the bf16 instructions, otherwise by the 8-bit ones at
+// twice the rate.  Those add up 8 neighbouring products at 2^-13 of the
+// largest one, the bits below cut towards zero (2^16 beside a product of 7 in
+// its group loses the 7; the groups' sums keep some 23 bits).  What is lost of
+// 8 products is below 7 * 2^-13 of the largest, 2^-10, while the codes of
+// that product are each rounded by up to 2^-4 of it.  On normal data the sums
+// are off by 1.4e-5 of the result's norm (1e-8 with SUM32), a bf16 output's
+// rounding by 1.7e-3.  So: 8-bit sums for tiles with a bf16 output, which are
+// bound by the matrix units (8192 x 8192 x 2048: 143 us, 294 with SUM32), and
+// SUM32 for an fp32 output and for few rows, which are bound by the weights'
+// bytes (16 rows of 4096 x 2048: 5.2 us, 5.3 with SUM32; 64 rows 9.3 and 9.8).
+template <bool SUM32>
 __device__ __forceinline__ f32x4v mfma128(i32x8 a, i32x8 b) {
   f32x4v z = {0.f, 0.f, 0.f, 0.f};
-  if constexpr (IOT == 1) {
+  if constexpr (!SUM32) {
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, z, 0, 0, 0, 0, 0, 0);
   } else {
 #pragma unroll
@@ -216,7 +223,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_scaled_mm(ScaledArgs a) {
     i32x8 next = x;
     if constexpr (IM > 1) next = tile_operand(X + 16 * KS, l, h);
 #pragma unroll
-    for (int j = 0; j < IN; ++j) p[0][j] = mfma128<IOT>(w[j], x);
+    for (int j = 0; j < IN; ++j) p[0][j] = mfma128<IOT == 0>(w[j], x);
     if constexpr (IOT == 1) {
       __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
 #pragma unroll
@@ -235,7 +242,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_scaled_mm(ScaledArgs a) {
       if (i + 1 < IM) next = tile_operand(X + (i + 1) * 16 * KS, l, h);
 #pragma unroll
       for (int j = 0; j < IN; ++j) {
-        p[i & 1][j] = mfma128<IOT>(w[j], x);
+        p[i & 1][j] = mfma128<IOT == 0>(w[j], x);
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[i - 1][j][e] = fmaf(p[(i - 1) & 1][j][e], sc[i - 1], acc[i - 1][j][e]);
       }
@@ -345,7 +352,7 @@ __global__ __launch_bounds__(512) void k_scaled_mm_rows(ScaledArgs a) {
     for (int u = 0; u < 2; ++u)
 #pragma unroll
       for (int i = 0; i < IM; ++i) {
-        const f32x4v p = mfma128<IOT>(y[u], x[u][i]);
+        const f32x4v p = mfma128<true>(y[u], x[u][i]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[i][e] = fmaf(p[e], sc[u][i], acc[i][e]);
       }

@@ -549,9 +549,11 @@ hyena_status hyena_rms_norm_backward(const void* s, const float* weight, const v
  *   out[m][n] = sum_k (q[m][k] scales[m][k/128]) (wq[n][k] wscales[n/128][k/128]) + bias[n]
  * q [M][K], wq [N][K] e4m3, scales [M][ceil(K/128)], wscales [ceil(N/128)]
  * [ceil(K/128)] fp32, bias [N] fp32 or NULL.  Each block of 128 is summed on
- * the matrix cores and scaled into an fp32 sum: for an fp32 output in fp32,
- * for a bf16 output by the 8-bit instructions, whose sums are good to about
- * 2^-16 of the terms' sizes.  M = B * L rows of
+ * the matrix cores and scaled into an fp32 sum: in fp32 for an fp32 output and
+ * for M <= 64; for a bf16 output of more rows by the 8-bit instructions, which
+ * add up each 8 neighbouring products with less than 2^-13 of the largest one
+ * lost of each of the others, cut towards zero (an fp32 output avoids it where
+ * sums cancel).  M = B * L rows of
  * tokens; out is [B][L][N], or with channel_major [B][N][L], the layout of
  * the operators above, in the I/O dtype.  M <= 2^31, whatever B and L are
  * unless channel_major; K a multiple of 16 (UNSUPPORTED
