@@ -629,6 +629,8 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : 3) void k_scan_bwd(ScanArgs a)
       }
       sS[cw * N + n] = f32x4v{A, h, q, 0.f};
     }
+    // read by the row's other lanes: a wave's LDS accesses are done in order
+    __builtin_amdgcn_wave_barrier();
     const float bias = a.dbias ? a.dbias[d] : 0.f, skip = a.skip ? a.skip[d] : 0.f;
     float u[8], dt[8], du[8], gy[8], y[8], s1[8], s2[8];
     steps8<IOT>(a, ru, rd, bias, mm, u, dt);
