@@ -122,6 +122,15 @@ def _activation(x, name, dims):
     return _H._io_of(x)
 
 
+def _dims(t, name, dims):
+    """Checks the tensor that sets a call's other sizes."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a CUDA (ROCm) tensor")
+    if t.dim() != dims:
+        raise ValueError(f"{name} has {t.dim()} dimensions, not {dims}")
+
+
 def _workspace(workspace, nbytes, name, device):
     """(workspace, its address, its bytes): the caller's, or one allocated here."""
     torch = _torch()
@@ -142,7 +151,8 @@ def _workspace(workspace, nbytes, name, device):
 
 def _conv_params(x, w, bias, silu, state, lengths, B, D, L):
     torch = _torch()
-    if w.dim() != 2 or w.shape[0] != D:
+    _dims(w, "w", 2)
+    if w.shape[0] != D:
         raise ValueError(f"w shape {tuple(w.shape)} is not [{D}, T]")
     T = w.shape[1]
     dev = x.device
@@ -217,11 +227,11 @@ def short_conv_backward(x, w, gy, bias=None, silu: bool = False, state=None, len
 def _scan_params(u, delta, A, Bm, Cm, skip, z, delta_bias, softplus, state, lengths, B, D, tail):
     torch = _torch()
     dev, t, f32 = u.device, u.dtype, torch.float32
-    if A.dim() != 2 or A.shape[0] != D:
+    _dims(A, "A", 2)
+    if A.shape[0] != D:
         raise ValueError(f"A shape {tuple(A.shape)} is not [{D}, N]")
     N = A.shape[1]
-    if Bm.dim() != 3 + len(tail):
-        raise ValueError(f"Bm has {Bm.dim()} dimensions, not {3 + len(tail)}")
+    _dims(Bm, "Bm", 3 + len(tail))
     G = Bm.shape[1]
     bc = (B, G, N, *tail)
     return N, G, SelectiveScanParams(
@@ -304,8 +314,8 @@ def selective_scan_backward(u, delta, A, Bm, Cm, gy, skip=None, z=None, delta_bi
 # -------------------------------------------------------------- residual norm
 
 def _rows(x, name):
-    io = _H._io_of(x)
     _H._need_cuda(x, name)
+    io = _H._io_of(x)
     if x.dim() < 1:
         raise ValueError(f"{name} has no dimension")
     D = x.shape[-1]
@@ -399,9 +409,11 @@ def scaled_matmul(q, scales, wq, wscales, bias=None, out_dtype=None, channel_maj
     [..., N], with channel_major [N, M] of a left [M, K], or [B, N, L] of a
     left [B, L, K], the layout of the convolutions and the scan."""
     torch = _torch()
-    dev, e4m3, f32 = q.device, torch.float8_e4m3fn, torch.float32
+    e4m3, f32 = torch.float8_e4m3fn, torch.float32
     _H._need_cuda(q, "q", e4m3)
-    if q.dim() < 2 or wq.dim() != 2 or q.shape[-1] != wq.shape[1]:
+    dev = q.device
+    _dims(wq, "wq", 2)
+    if q.dim() < 2 or q.shape[-1] != wq.shape[1]:
         raise ValueError(f"shapes {tuple(q.shape)} and {tuple(wq.shape)} do not make a product")
     if channel_major and q.dim() > 3:
         raise ValueError("channel_major takes [M, K] or [B, L, K]")
