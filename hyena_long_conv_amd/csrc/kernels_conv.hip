@@ -10,8 +10,8 @@
 // from the cache that its neighbours' loads have filled.  The taps behind T are
 // passed over, not multiplied by zero: an infinity or NaN there is not theirs.
 // The condition is the same for all lanes.  8 x 1536 x 2048 bf16,
-// 4 taps, with silu: 21 us, 4.9 TB/s of x and y, a copy's rate; the vector
-// units are busy 97% of that time (the sigmoid is a third of it), so the two
+// 4 taps, with silu: 20.4 us, 4.9 TB/s of x and y, a copy's rate; the vector
+// units are busy 95% of that time (the sigmoid is a third of it), so the two
 // bounds meet here.
 #include <hip/hip_runtime.h>
 
@@ -134,7 +134,8 @@ __global__ __launch_bounds__(256) void k_conv(ConvArgs a, int per, int lper, int
 }
 
 // One token for each of B sequences: a thread to a channel; 16 x 1536 take 2.9
-// us, a launch.
+// us, a launch.  (The state's values are loaded one after the other, each
+// under its tap's condition.)
 template <int IOT, int TT>
 __global__ __launch_bounds__(256) void k_conv_step(ConvArgs a) {
   const int64_t r = blockIdx.x * (int64_t)256 + threadIdx.x;
@@ -161,7 +162,7 @@ __global__ __launch_bounds__(256) void k_conv_step(ConvArgs a) {
 // computed again, for a lane's 8 steps and the TT-1 behind them.  A workgroup
 // sums over its sequences and steps in registers and leaves one partial for
 // each tap, which k_conv_sum adds up in a fixed order.  8 x 1536 x 2048 bf16:
-// 39 us and 4 for the sums, vector units 85% busy (a p, a sigmoid and a
+// 38 us and 4 for the sums, vector units 88% busy (a p, a sigmoid and a
 // derivative for 19 steps of 16, the sums over taps twice); 31 us at a copy's
 // rate.
 template <int IOT, int TT, int E, bool EXACT>

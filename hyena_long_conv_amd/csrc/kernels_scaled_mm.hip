@@ -4,11 +4,12 @@
 //   out[m][n] = sum_kb scales[m][kb] wscales[n / 128][kb]
 //                 sum_{k in kb} q[m][k] wq[n][k]  + bias[n].
 //
-// 8192 x 8192 x 2048 to bf16: 143 us, 1.9 PFLOP/s; 2.25 at K = 8192, where the
-// matrix units are busy 58% of the cycles and the vector units, which scale
-// and add every block's products, 48%, at a clock that has come down to 1.9
-// GHz.  (A library product without block scales reaches 2.6 at 8192^3.)  To
-// fp32, through the bf16 instructions: 294 us, 0.94 PFLOP/s.
+// 8192 x 8192 x 2048 to bf16: 143 us, 1.9 PFLOP/s (149 channel-major with a
+// bias, 171 at the profiler's clock, where the matrix units are busy 44% of
+// the cycles and the vector units, which scale and add every block's products,
+// 46%); 2.15 at K = 8192.  (A library product without block scales reaches 2.6
+// at 8192^3.)  To fp32, through the bf16 instructions: 292 us, 0.94 PFLOP/s;
+// 227 us at the 1.21 of a library product in bf16.
 #include <hip/hip_runtime.h>
 
 #include "ssm.hpp"
@@ -320,8 +321,8 @@ __global__ __launch_bounds__(64 * WM * WN) void k_scaled_mm(ScaledArgs a) {
 // Up to 64 rows: the weights' bytes are the call.  A workgroup takes 16
 // columns and splits k over its 8 waves; a lane loads its operands straight
 // into registers (a row of 128 bytes is one line), and the waves' sums meet
-// in LDS.  1, 16, 32 and 64 rows of 4096 x 2048: 3.9, 5.0, 6.4 and 9.3 us (one
-// round of loads to a wave, so latency counts: 1.7 TB/s with 16 rows), where
+// in LDS.  1, 16, 32 and 64 rows of 4096 x 2048: 4.4, 5.3, 6.7 and 9.8 us (one
+// round of loads to a wave, so latency counts: 1.6 TB/s with 16 rows), where
 // tiles of 64 x 64 take 9 us, and far more with fewer columns, for want of
 // workgroups.
 template <int IOT, bool CM, int IM>
@@ -400,7 +401,9 @@ hipError_t launch_product(const ScaledArgs& a, hipStream_t s) {
   // The largest tiles that still fill the chip.  N = 4096, K = 2048, bf16, in
   // tiles of 256, 128 and 64: 4096 rows 38, 49 and 64 us (256 tiles of 256),
   // 2048 rows 33, 26 and 33 (128 of them; 512 of 128), 1024 rows 30, 18.6 and
-  // 17.3 (256 of 128).
+  // 17.3 (256 of 128).  The two smaller ones' products lie in accumulator
+  // registers and are each read back from there (64 and 16 reads to a step),
+  // which these times include.
   if (a.M <= 64) return launch_rows<IOT, CM>(a, s);
   if constexpr (IOT == 1) {                           // widened operands leave no registers for these
     if (tiles(256, 256) >= 192) return launch_tiles<IOT, CM, 8, 4, 2, 4>(a, s);

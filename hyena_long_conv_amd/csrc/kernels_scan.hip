@@ -19,8 +19,9 @@
 // Arithmetic bounds it: to 8 (t, n) of a lane 8 products dt A, 9 exponentials
 // (four issue slots each), 8 products with B, 7 + 8 steps of the recurrence, 8
 // with C and about 12 for the row's scan, 88 slots.  8 x 1536 x 2048, 16
-// states, bf16: 133 us, vector units 93% busy; its bytes at a copy's rate are
-// 42 us.  (A lane to a channel, with B and C as scalars, would need 64 slots
+// states, bf16: 309 000 cycles of a compute unit, 94% of them with vector
+// instructions: 134 us a call at some 2.3 GHz (147 to 153 where the clock is
+// 2.0, as under the profiler); its bytes at a copy's rate are 42 us.  (A lane to a channel, with B and C as scalars, would need 64 slots
 // and no scan, but 65536 channels to fill the chip, or a second pass over the
 // exponentials.)
 #include <hip/hip_runtime.h>
@@ -347,8 +348,10 @@ hipError_t launch_scan_nv(const ScanArgs& a, hipStream_t s) {
 //
 // 4 states to a lane, W lanes (a power of two, W * 4 >= N) to a channel of a
 // sequence; the state's read and write are the call's traffic: 128 x 1536
-// channels of 16 states in 9.5 us, 2.8 TB/s (one round of loads to a wave, so
-// latency counts; 5.6 us at a copy's rate).
+// channels of 16 states in 8.8 us, 3.0 TB/s (5.6 us at a copy's rate).  What
+// is above that is latency: u, delta and z, then A and the state, then B's
+// and C's eight values, each a load under its lane's condition that is waited
+// for before the next.
 template <int IOT>
 __global__ __launch_bounds__(256) void k_scan_step(ScanArgs a, int W, int lw, float* __restrict__ state) {
   const int64_t idx = blockIdx.x * (int64_t)256 + threadIdx.x, r = idx >> lw;
@@ -423,14 +426,14 @@ __global__ __launch_bounds__(256) void k_scan_step(ScanArgs a, int W, int lw, fl
 // are staged once and the sums over channels stay on the chip.  Rows of one
 // chunk need the third pass only.
 //
-// 4 x 1536 x 2048, 16 states, bf16: 87 us for the first pass, 7 for the
-// second, 214 for the third and 9 for the sums (299 in all as a call; 37 at a
+// 4 x 1536 x 2048, 16 states, bf16: 78 us for the first pass, 7 for the
+// second, 194 for the third and 9 for the sums (298 in all as a call; 37 at a
 // copy's rate): vector units 89% and 92% busy, some 75 and 200 instructions
-// to 8 (t, n) of a lane.  Tried for the third pass and slower: sums over
-// channels kept per lane in LDS instead of folded over the wave (15% fewer
-// instructions, but 84 KB of LDS: 239 us), 8 waves to a workgroup up to 32
-// states (248 us: twice the turns), two waves to a SIMD without the few
-// spilled registers of three (220 us).
+// to 8 (t, n) of a lane.  Tried for the third pass and slower, on a card where
+// it took 214 us: sums over channels kept per lane in LDS instead of folded
+// over the wave (15% fewer instructions, but 84 KB of LDS: 239 us), 8 waves to
+// a workgroup up to 32 states (248 us: twice the turns), two waves to a SIMD
+// without the few spilled registers of three (220 us).
 
 // Chunk sums: H, Q [N] and sum dt of 4 channels to a wave.
 template <int IOT>

@@ -407,7 +407,9 @@ def scaled_matmul(q, scales, wq, wscales, bias=None, out_dtype=None, channel_maj
     rms_norm_quantized): left [..., K] times right [N, K] transposed, plus bias
     [N] (float32), in out_dtype (bfloat16 by default, or float32).  Returns
     [..., N], with channel_major [N, M] of a left [M, K], or [B, N, L] of a
-    left [B, L, K], the layout of the convolutions and the scan."""
+    left [B, L, K], the layout of the convolutions and the scan.  Sums are fp32;
+    for bfloat16 outputs of more than 64 rows those of 8 neighbouring products
+    lose what is below 2^-13 of the largest one."""
     torch = _torch()
     e4m3, f32 = torch.float8_e4m3fn, torch.float32
     _H._need_cuda(q, "q", e4m3)

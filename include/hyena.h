@@ -399,7 +399,8 @@ hyena_status hyena_nd_forward(const void* v, const void* const* x, const void* s
  * lengths (device int32 [B], or NULL): sequence b holds min(max(lengths[b],
  * 0), L) steps.  Whatever stands behind them (NaN included) is not read into
  * any result; outputs of activation shape are zero there, and the state left
- * behind is the one at the sequence's own end.
+ * behind is the one at the sequence's own end.  A sequence of no steps hands
+ * its state on, whatever it holds, and adds nothing to a parameter's gradient.
  * ---------------------------------------------------------------------- */
 
 /*
@@ -521,7 +522,8 @@ hyena_status hyena_selective_scan_backward(const hyena_selective_scan_params* p,
  *   as stored; s = x and s_out NULL where residual is NULL),
  *   y = s / sqrt(mean(s^2) + eps) * weight.
  * x, residual, s_out, y [rows][D] I/O dtype, weight [D] fp32; rows <= 2^31,
- * eps >= 0 (a row of zeros with eps = 0 gives NaN).
+ * eps >= 0 (a row of zeros with eps = 0 gives NaN).  The squares are summed in
+ * fp32, whose range they must not leave.
  *
  * hyena_rms_norm_quantized stores y in 8 bits instead: q [rows][D] e4m3 codes
  * (OCP, largest value 448) and scales [rows][ceil(D/128)] fp32, one for each
@@ -553,7 +555,8 @@ hyena_status hyena_rms_norm_backward(const void* s, const float* weight, const v
  * for M <= 64; for a bf16 output of more rows by the 8-bit instructions, which
  * add up each 8 neighbouring products with less than 2^-13 of the largest one
  * lost of each of the others, cut towards zero (an fp32 output avoids it where
- * sums cancel).  M = B * L rows of
+ * sums cancel).  A row's and a block's scales are multiplied in fp32, whose
+ * normal range that product must not leave.  M = B * L rows of
  * tokens; out is [B][L][N], or with channel_major [B][N][L], the layout of
  * the operators above, in the I/O dtype.  M <= 2^31, whatever B and L are
  * unless channel_major; K a multiple of 16 (UNSUPPORTED
