@@ -226,3 +226,57 @@ def test_scaled_matmul_more_rows_than_a_sequence_holds():
     with pytest.raises(H.HyenaError) as e:
         H.scaled_matmul(q, s, wq, ws, channel_major=True)     # there the rows are one sequence
     assert e.value.code == 2
+
+
+@pytest.mark.parametrize("io", ["fp32", "bf16"])
+@pytest.mark.parametrize("B,L,N,K", [(300, 1, 130, 272), (97, 3, 200, 128), (41, 7, 77, 400), (600, 13, 300, 144),
+                                     (9000, 1, 3400, 128), (30, 2, 40, 64), (1, 64, 33, 48), (64, 1, 33, 48)])
+def test_scaled_matmul_channel_major_of_short_sequences(B, L, N, K, io):
+    """Sequences shorter than a word of outputs: the row-major call's bits, in the other order."""
+    r = gen(B + L)
+    q, s = H.quantize(dev(r(B, L, K)))
+    wq, ws = H.quantize(dev(r(N, K)), 128)
+    call = lambda cm: H.scaled_matmul(q, s, wq, ws, bias=bias, out_dtype=TYPES[io], channel_major=cm)  # noqa: E731
+    bias = dev(r(N))
+    same(call(True), call(False).transpose(1, 2), "channel-major")
+
+
+@pytest.mark.parametrize("L,at", [(60, 33), (300, 171), (2100, 1500)])
+@pytest.mark.parametrize("key", ["u", "delta", "z", "Bm", "Cm", "gy"])
+def test_selective_scan_bad_value_reaches_its_own_terms(key, L, at):
+    """A NaN at a step changes no bit of another sequence, of a channel that does not read it, of the steps before it
+    (forward), or of the steps behind it (gradients that come from later steps only)."""
+    B, D, G, N = 2, 20, 2, 16
+    a, _, _ = scan_inputs((B, D, G, N, L, True, True, True, True, True, None), torch.float32, 9)
+    a["gy"], a["gstate_out"] = gen(4)(B, D, L), gen(5)(B, D, N)
+
+    def run(v):
+        on = scan_on_gpu({k: t for k, t in v.items() if not k.startswith("g")}, None, True)
+        y, h = H.selective_scan(**on, return_state=True)
+        return dict(H.selective_scan_backward(**on, gy=dev(v["gy"]), gstate_out=dev(v["gstate_out"])), y=y, h=h)
+
+    clean = run(a)
+    bad = dict(a, **{key: a[key].clone()})
+    of_group = key in ("Bm", "Cm")
+    bad[key][(1, 1, 3, at) if of_group else (1, 13, at)] = NAN
+    got = run(bad)
+    mine = list(range(10, 20)) if of_group else [13]
+    other = [d for d in range(D) if d not in mine]
+    for k in ("y", "h", "gu", "gdelta", "gz", "gstate"):
+        same(got[k][0], clean[k][0], k)
+        same(got[k][1, other], clean[k][1, other], k)
+    for k in ("gB", "gC"):
+        same(got[k][0], clean[k][0], k)
+        same(got[k][1, 0], clean[k][1, 0], k)
+    for k in ("gA", "gskip", "gdelta_bias"):
+        same(got[k][other], clean[k][other], k)
+    same(got["y"][1, :, :at], clean["y"][1, :, :at], "y before")
+    if key in ("z", "Cm"):
+        same(got["y"][..., at + 1:], clean["y"][..., at + 1:], "y behind")
+        same(got["h"], clean["h"], "the state")
+    if key == "u":
+        same(got["gu"], clean["gu"], "gu")
+        same(got["gstate"], clean["gstate"], "gstate")
+    if key in ("z", "gy"):
+        for k in ("gu", "gB", "gz"):
+            same(got[k][..., at + 1:], clean[k][..., at + 1:], k)

@@ -25,6 +25,7 @@ SCAN = {
     "segments": ((1, 768, 1, 16, 8192), dict(split=1, segs=32, chunks_per_seg=2, tiles_per=3)),
     "shared_states": ((1, 1000, 1, 32, 600), dict(split=4, segs=1, chunks_per_seg=5)),
     "shared_states_64": ((4, 250, 1, 64, 500), dict(split=4, segs=1, chunks_per_seg=4, waves=8, splits=8)),
+    "a_channel_to_a_group": ((2, 40, 40, 40, 300), dict(tiles_per=1, chunks=3)),
     "parts": ((48, 20, 1, 4, 384), dict(parts=144)),
 }
 
