@@ -35,7 +35,10 @@ __all__ = ["HyenaError", "lib", "plan", "filter_gen", "filter_spectrum", "spectr
            "short_conv", "short_conv_step", "short_conv_backward", "short_conv_backward_workspace_bytes",
            "selective_scan", "selective_scan_step", "selective_scan_backward", "selective_scan_workspace_bytes",
            "selective_scan_backward_workspace_bytes", "rms_norm", "rms_norm_quantized", "rms_norm_backward",
-           "rms_norm_backward_workspace_bytes", "quantize", "scaled_matmul"]
+           "rms_norm_backward_workspace_bytes", "quantize", "scaled_matmul",
+           "linear_attention", "linear_attention_step", "linear_attention_backward",
+           "linear_attention_workspace_bytes", "linear_attention_backward_workspace_bytes", "rotary",
+           "rotary_frequencies", "group_norm", "group_norm_backward", "group_norm_backward_workspace_bytes"]
 
 # HYENA_LIB names another build of the same library (tuning variants, the
 # host-sanitized build of the argument checks); the in-tree build otherwise.
@@ -176,6 +179,7 @@ def lib() -> ctypes.CDLL:
                                    vp]
     L.hyena_nd_forward.restype = i32
     ssm.declare(L)
+    linattn.declare(L)
     L.hyena_status_str.argtypes = [i32]
     L.hyena_status_str.restype = ctypes.c_char_p
     _lib = L
@@ -668,3 +672,11 @@ from .ssm import (quantize, rms_norm, rms_norm_backward, rms_norm_backward_works
                   rms_norm_quantized, scaled_matmul, selective_scan, selective_scan_backward,
                   selective_scan_backward_workspace_bytes, selective_scan_step, selective_scan_workspace_bytes,
                   short_conv, short_conv_backward, short_conv_backward_workspace_bytes, short_conv_step)
+
+
+# ------------------------------------------------ the linear-attention block
+
+from . import linattn  # noqa: E402
+from .linattn import (group_norm, group_norm_backward, group_norm_backward_workspace_bytes,  # noqa: E402
+                      linear_attention, linear_attention_backward, linear_attention_backward_workspace_bytes,
+                      linear_attention_step, linear_attention_workspace_bytes, rotary, rotary_frequencies)

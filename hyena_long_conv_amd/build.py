@@ -23,7 +23,8 @@ LIB = os.path.join(PKG, "libhyena_mi355x.so")
 
 SOURCES = ["api.cpp", "kernels_single.hip", "kernels_fourstep.hip", "kernels_filter.hip", "kernels_proj.hip",
            "kernels_fir.hip", "kernels_nd.hip", "kernels_bwd_long.hip", "scratch.hip", "api_ssm.cpp",
-           "kernels_conv.hip", "kernels_scan.hip", "kernels_norm.hip", "kernels_scaled_mm.hip"]
+           "kernels_conv.hip", "kernels_scan.hip", "kernels_norm.hip", "kernels_scaled_mm.hip",
+           "api_linattn.cpp", "kernels_linattn.hip", "kernels_rotary.hip", "kernels_group_norm.hip"]
 ARCH = os.environ.get("HYENA_OFFLOAD_ARCH", "gfx950")
 
 
@@ -77,8 +78,8 @@ HOSTCHECK_LIB = os.path.join(BUILD, "libhyena_hostcheck.so")
 
 
 def build_hostcheck(out: str = HOSTCHECK_LIB) -> str:
-    """Host-only build of the C ABI for the sanitizers: api.cpp and api_ssm.cpp
-    (argument checks, planning, size queries) and stand-ins for the kernel launchers
+    """Host-only build of the C ABI for the sanitizers: api.cpp, api_ssm.cpp and
+    api_linattn.cpp (argument checks, planning, size queries) and stand-ins for the kernel launchers
     (csrc/hostcheck_stubs.cpp), compiled by g++ with AddressSanitizer and
     UndefinedBehaviorSanitizer.  No device code is involved.  Load it with
     the sanitizer runtimes preloaded (tests/test_hostcheck.py)."""
@@ -87,7 +88,7 @@ def build_hostcheck(out: str = HOSTCHECK_LIB) -> str:
            "-fsanitize=address,undefined", "-fno-sanitize-recover=undefined",
            "-D__HIP_PLATFORM_AMD__", "-I", "/opt/rocm/include", "-I", INCLUDE, "-I", CSRC,
            os.path.join(CSRC, "api.cpp"), os.path.join(CSRC, "api_ssm.cpp"),
-           os.path.join(CSRC, "hostcheck_stubs.cpp"), "-o", out]
+           os.path.join(CSRC, "api_linattn.cpp"), os.path.join(CSRC, "hostcheck_stubs.cpp"), "-o", out]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"host-check build failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")

@@ -1,11 +1,12 @@
 // hostcheck_stubs.cpp -- stand-ins for the kernel launchers, linked with
-// api.cpp and api_ssm.cpp into a host-only build of the C ABI (g++, AddressSanitizer and
+// api.cpp, api_ssm.cpp and api_linattn.cpp into a host-only build of the C ABI (g++, AddressSanitizer and
 // UndefinedBehaviorSanitizer; no GPU code).  That build exercises argument
 // validation, planning and the size queries on the CPU.  A call with bad
 // arguments must return its status before it reaches a launcher; a call
 // that gets this far receives hipErrorNoDevice, which the entry points
 // report as HYENA_ERR_HIP, the status a GPU-less host would see anyway.
 #include "launch.hpp"
+#include "linattn.hpp"
 #include "ssm.hpp"
 
 namespace hyena {
@@ -49,5 +50,12 @@ hipError_t rms_norm(const NormArgs&, hipStream_t) { return kNoKernels; }
 hipError_t rms_norm_backward(const NormArgs&, hipStream_t) { return kNoKernels; }
 hipError_t quantize(const NormArgs&, hipStream_t) { return kNoKernels; }
 hipError_t scaled_matmul(const ScaledArgs&, hipStream_t) { return kNoKernels; }
+
+hipError_t linear_attention(const LinArgs&, hipStream_t) { return kNoKernels; }
+hipError_t linear_attention_step(const LinStepArgs&, hipStream_t) { return kNoKernels; }
+hipError_t fold_heads(const FoldArgs&, hipStream_t) { return kNoKernels; }
+hipError_t rotary(const RotaryArgs&, hipStream_t) { return kNoKernels; }
+hipError_t group_norm(const GroupNormArgs&, hipStream_t) { return kNoKernels; }
+hipError_t group_norm_backward(const GroupNormArgs&, hipStream_t) { return kNoKernels; }
 
 }  // namespace hyena

@@ -1,0 +1,172 @@
+// linattn.hpp -- internal launch interface of the linear-attention block's
+// operators (linear attention with decays, rotary positions, group norm)
+// between their C ABI (api_linattn.cpp) and the kernel translation units.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace hyena {
+
+// An activation [B][L][heads][D]: elements between sequences, tokens and
+// heads; a head's D values are contiguous.  Head h of the operator's H reads
+// head h / share.
+struct HeadView {
+  const void* p;
+  int64_t batch, token, head;
+  int share;
+};
+
+// ------------------------------------------------------- linear attention
+//
+// One pass of the recurrence
+//   S[t] = lambda S[t-1] + su k[t] v[t]^T,   out[t] = so S[t]^T q[t]
+// over tokens in order, or from a sequence's last one to its first.  The
+// forward is one pass, the backward three (LinArgs.pass).
+struct LinPass {
+  HeadView q, k, v;        // q, k of DK values to a head, v and out of DV
+  void* out;               // [B][L][H][DV], I/O dtype or fp32 (out_f32)
+  int out_f32;
+  int DK, DV;
+  float so, su;
+  int reverse;             // from the last token; the first one finds the state undecayed
+  const float* s0;         // [B][H][..] state or nullptr: element (dk, dv) at dk s0_k + dv s0_v
+  int s0_k, s0_v;
+  float* seg;              // split time axis: states behind all segments but the last, [B][H][segs - 1][..], element
+  int seg_k, seg_v;        // (dk, dv) at dk seg_k + dv seg_v; seg_fills: this pass forms them, another one otherwise
+  int seg_fills;
+  float* s_out;            // state after the last token ([DK][DV]), times lambda if reverse; or nullptr
+};
+
+struct LinArgs {
+  LinPass pass[3];
+  int passes;
+  const float* log_decay;  // [H] or nullptr
+  const int32_t* lengths;  // [B] or nullptr
+  int B, H, io;
+  int64_t L;
+  int segs;                // the time axis in segments of `seg` tokens
+  int64_t seg;
+};
+
+// How a pass fills the chip.
+struct LinPlan {
+  int segs;
+  int64_t seg;
+};
+inline LinPlan lin_plan(int64_t B, int64_t L, int64_t H, int64_t DK, int64_t DV) {
+  LinPlan p{1, L};
+  (void)B, (void)H, (void)DK, (void)DV;
+  return p;
+}
+
+inline LinPlan lin_backward_plan(int64_t B, int64_t L, int64_t H, int64_t Dk, int64_t Dv) {
+  return lin_plan(B, L, H, Dk, Dv);
+}
+// The most workgroups of a launch of one pass.
+inline int64_t lin_groups(const LinPlan& p, int64_t B, int64_t H) { return B * H * p.segs * 4; }
+
+struct LinStepArgs {
+  HeadView q, k, v;        // token strides unused
+  const float* log_decay;  // or nullptr
+  float* state;            // [B][H][Dk][Dv]
+  void* o;                 // [B][H][Dv]
+  int B, H, Dk, Dv, io;
+  float scale;
+};
+
+// Sums over the heads that share one: out[t][j][d] = sum of x[t][j share ..][d].
+struct FoldArgs {
+  const float* x[3];       // [tokens][heads share][D], or nullptr
+  void* out[3];            // [tokens][heads][D]
+  int heads[3], share[3], D[3];
+  int64_t tokens;
+  int io;
+};
+
+hipError_t linear_attention(const LinArgs& a, hipStream_t s);
+hipError_t linear_attention_step(const LinStepArgs& a, hipStream_t s);
+hipError_t fold_heads(const FoldArgs& a, hipStream_t s);
+
+// -------------------------------------------------------- rotary positions
+struct RotaryArgs {
+  HeadView x, out;
+  const double* freq;        // [R / 2]
+  const int32_t* positions;  // or nullptr: the token's index
+  int64_t pos_batch, pos_token;
+  int64_t tokens, L;         // B L, L
+  int H, D, R, interleaved, io, in_place;
+  float scale, sine;         // sine: 1, or -1 for the inverse
+};
+
+// A launch: words of a head (8 pairs that are turned, then 8 values that are
+// copied), and threads that share a token's heads, enough for half a million
+// threads in all.
+inline int64_t rotary_turning(const RotaryArgs& a) { return (a.R / 2 + 7) / 8; }
+inline int64_t rotary_words(const RotaryArgs& a) { return rotary_turning(a) + (a.in_place ? 0 : (a.D - a.R + 7) / 8); }
+inline int64_t rotary_shares(const RotaryArgs& a) {
+  const int64_t want = ((int64_t)1 << 19) / (a.tokens * rotary_words(a)) + 1;
+  return want < a.H ? want : a.H;
+}
+inline int64_t rotary_groups(const RotaryArgs& a) {
+  return (a.tokens * rotary_words(a) * rotary_shares(a) + 255) / 256;
+}
+
+hipError_t rotary(const RotaryArgs& a, hipStream_t s);
+
+// --------------------------------------------------------------- group norm
+struct GroupNormArgs {
+  const void *x, *z;           // [rows][G Dg]; z: or nullptr
+  const float *weight, *bias;  // [G Dg] or nullptr
+  void* y;
+  int64_t rows;
+  int G, Dg, silu, io;
+  float eps;
+  // backward
+  const void* gy;
+  void *gx, *gz;               // gz: or nullptr
+  float *gw, *gb;              // or nullptr
+  float* partial;              // workspace, [parts][2][G Dg]
+};
+
+hipError_t group_norm(const GroupNormArgs& a, hipStream_t s);
+hipError_t group_norm_backward(const GroupNormArgs& a, hipStream_t s);
+
+// How a launch covers rows of G groups of Dg values: `lanes` threads (a power
+// of two up to 256) to a group, `words` words of 8 values to a thread; a
+// workgroup of 256 threads takes `per` neighbouring groups of `rows` rows at
+// a time.  Groups beyond 256 x 4 words are read twice (`words` 0).
+struct GroupNormPlan {
+  int lanes, words, per, rows;
+  int64_t blocks;              // workgroups across a row's groups
+};
+inline GroupNormPlan group_norm_plan(int64_t G, int64_t Dg) {
+  GroupNormPlan p;
+  const int64_t w = (Dg + 7) / 8;
+  if (w <= 64) {
+    p.lanes = 1;
+    while (p.lanes < w) p.lanes *= 2;
+    p.words = 1;
+  } else if (w <= 128) {
+    p.lanes = 64, p.words = 2;
+  } else if (w <= 256) {
+    p.lanes = 256, p.words = 1;
+  } else if (w <= 512) {
+    p.lanes = 256, p.words = 2;
+  } else {
+    p.lanes = 256, p.words = w <= 1024 ? 4 : 0;
+  }
+  const int units = 256 / p.lanes;
+  p.per = (int)(G < units ? G : units);
+  p.rows = units / p.per;
+  p.blocks = (G + p.per - 1) / p.per;
+  return p;
+}
+// Workgroups of the backward, which leave a partial each, along the rows.
+inline int64_t group_norm_backward_parts(int64_t rows, int64_t G, int64_t Dg) {
+  const GroupNormPlan p = group_norm_plan(G, Dg);
+  const int64_t n = (rows + p.rows - 1) / p.rows, most = (2048 + p.blocks - 1) / p.blocks;
+  return n < most ? n : most;
+}
+
+}  // namespace hyena

@@ -574,6 +574,148 @@ hyena_status hyena_scaled_matmul(const void* q, const float* scales, const void*
                                  const float* bias, void* out, int64_t B, int64_t L, int32_t N, int32_t K,
                                  int32_t channel_major, hyena_dtype io, void* stream);
 
+/* ------------------------------------------------------------------------
+ * The linear-attention block: the operators of a token mixer that stands in
+ * the place of the selective scan -- rotary positions on queries and keys,
+ * linear attention with a decay for each head, and a norm of each head's
+ * outputs with a gate.  The conventions of the state-space block hold (sizes,
+ * lengths, aliases, order of sums, workspaces), with activations token-major:
+ * [B][L][heads][D], as a row-major projection leaves them.  Activations that
+ * are read may be parts of wider rows: a stride[3] holds the elements between
+ * sequences, tokens and heads (0 repeats one; each in 0..2^38; a head's D
+ * values are contiguous), and their alignment is that of an element.
+ * ---------------------------------------------------------------------- */
+
+/*
+ * Linear attention with a decay for each head.  Per sequence b and head h,
+ * with lambda = exp(log_decay[h]) (1 where log_decay is NULL):
+ *   S[t] = lambda S[t-1] + k[b][t][h] v[b][t][h]^T      (Dk x Dv, fp32),
+ *   o[b][t][h] = scale S[t]^T q[b][t][h],
+ * S[-1] = state[b][h] (or zeros).  state_out (NULL: not wanted) is S at the
+ * sequence's end.  q has Hq heads, k Hk and v Hv, each a divisor of H: head h
+ * reads head h / (H/Hq) of q, and so on.  q, k [B][L][..][Dk], v [B][L][Hv][Dv]
+ * with strides, o [B][L][H][Dv] contiguous, I/O dtype; log_decay [H], state,
+ * state_out [B][H][Dk][Dv], fp32; Dk, Dv in 1..HYENA_MAX_HEAD.
+ *
+ * Decays: log_decay is not positive (minus infinity: S[t] = k[t] v[t]^T); a
+ * positive one grows the state, exp(log_decay t) not to overflow.  It is a
+ * constant of the head: the backward forms no gradient of it.
+ * workspace: hyena_linear_attention_workspace_bytes() (0 where the time axis
+ * is not split).
+ */
+#define HYENA_MAX_HEAD 256
+
+typedef struct {
+  int64_t B;
+  int64_t L;
+  int32_t H;
+  int32_t Hq;
+  int32_t Hk;
+  int32_t Hv;
+  int32_t Dk;
+  int32_t Dv;
+  float scale;              /* finite                    */
+  int32_t reserved;         /* 0                         */
+  const void* q;
+  const void* k;
+  const void* v;
+  int64_t q_stride[3];
+  int64_t k_stride[3];
+  int64_t v_stride[3];
+  const float* log_decay;   /* or NULL                   */
+  const float* state;       /* or NULL                   */
+  const int32_t* lengths;   /* or NULL                   */
+} hyena_linear_attention_params;
+
+int64_t hyena_linear_attention_workspace_bytes(int64_t B, int64_t L, int32_t H, int32_t Dk, int32_t Dv);
+hyena_status hyena_linear_attention(const hyena_linear_attention_params* p, void* o, float* state_out,
+                                    hyena_dtype io, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* One token for each sequence: q, k, v [B][..][D] (the strides between tokens
+ * are not used), o [B][H][Dv]; state [B][H][Dk][Dv] is moved on by one in
+ * place.  p->L, p->state and p->lengths are not used. */
+hyena_status hyena_linear_attention_step(const hyena_linear_attention_params* p, float* state, void* o,
+                                         hyena_dtype io, void* stream);
+
+/* Gradients of a loss with dloss/do = go ([B][L][H][Dv], contiguous) and
+ * dloss/dstate_out = gstate_out (NULL: zero): gq [B][L][Hq][Dk], gk
+ * [B][L][Hk][Dk], gv [B][L][Hv][Dv] contiguous, I/O dtype, summed in fp32
+ * over the heads that share one; gstate [B][H][Dk][Dv] fp32 (NULL: not
+ * wanted).  workspace: hyena_linear_attention_backward_workspace_bytes(). */
+typedef struct {
+  void* gq;
+  void* gk;
+  void* gv;
+  float* gstate;
+} hyena_linear_attention_grads;
+
+int64_t hyena_linear_attention_backward_workspace_bytes(int64_t B, int64_t L, int32_t H, int32_t Hq, int32_t Hk,
+                                                        int32_t Hv, int32_t Dk, int32_t Dv);
+hyena_status hyena_linear_attention_backward(const hyena_linear_attention_params* p, const void* go,
+                                             const float* gstate_out, const hyena_linear_attention_grads* g,
+                                             hyena_dtype io, void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * Rotary positions: the first R values of each head are turned in pairs by
+ * angles position * freq[i], i = 0..R/2-1, the others copied:
+ *   (a, b) -> scale (a cos - b sin, a sin + b cos),
+ * with (a, b) = values (i, i + R/2), or (2i, 2i + 1) with interleaved;
+ * inverse turns the other way, which with the same scale is the gradient.
+ * Angles are formed and reduced in double precision, so positions may be far
+ * (any int32).  positions[b pos_stride[0] + t pos_stride[1]] (int32, or NULL:
+ * t) is shared by the token's heads; freq [R/2] double, 8-byte aligned (radians a step, plain or
+ * stretched for a longer context).  R even, 2 <= R <= D <= 2^16.
+ * x [B][L][H][D] with strides; out is contiguous, or x itself: turned in
+ * place, with x's strides, which then must keep its heads apart (ALIAS).
+ */
+typedef struct {
+  int64_t B;
+  int64_t L;
+  int32_t H;
+  int32_t D;
+  int32_t R;
+  int32_t interleaved;      /* 0 or 1                    */
+  int32_t inverse;          /* 0 or 1                    */
+  float scale;              /* finite                    */
+  int64_t x_stride[3];
+  const double* freq;
+  const int32_t* positions; /* or NULL                   */
+  int64_t pos_stride[2];    /* sequences, tokens         */
+} hyena_rotary_params;
+
+hyena_status hyena_rotary(const hyena_rotary_params* p, const void* x, void* out, hyena_dtype io, void* stream);
+
+/*
+ * Norm of groups of a row with an activation: each of the G groups of D/G
+ * neighbouring values of a row (a head's output) is normed by itself,
+ *   n = (x - mean) / sqrt(var + eps),   m = n weight + bias,
+ *   y = m, with silu m / (1 + exp(-m)), or with z m z / (1 + exp(-z));
+ * silu and z exclude each other (UNSUPPORTED).  x, z, y [rows][D] I/O dtype,
+ * weight, bias [D] fp32 or NULL (1, 0); rows <= 2^31, eps >= 0 (a group of
+ * equal values with eps = 0 gives NaN).  var is the mean of (x - mean)^2.
+ *
+ * hyena_group_norm_backward: from x and gy = dloss/dy the gradients gx, gz
+ * (required with z, NULL without it) and gweight, gbias [D] fp32 (NULL: not
+ * wanted), summed over the rows; mean and var are computed again.
+ */
+typedef struct {
+  int64_t rows;
+  int32_t D;
+  int32_t G;
+  int32_t silu;             /* 0 or 1                    */
+  float eps;
+  const void* x;
+  const void* z;            /* or NULL                   */
+  const float* weight;      /* or NULL                   */
+  const float* bias;        /* or NULL                   */
+} hyena_group_norm_params;
+
+hyena_status hyena_group_norm(const hyena_group_norm_params* p, void* y, hyena_dtype io, void* stream);
+int64_t hyena_group_norm_backward_workspace_bytes(int64_t rows, int32_t D, int32_t G);
+hyena_status hyena_group_norm_backward(const hyena_group_norm_params* p, const void* gy, void* gx, float* gweight,
+                                       float* gbias, void* gz, hyena_dtype io, void* workspace,
+                                       int64_t workspace_bytes, void* stream);
+
 /* Static description of a status code. */
 const char* hyena_status_str(hyena_status s);
 
