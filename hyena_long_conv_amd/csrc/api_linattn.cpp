@@ -25,11 +25,13 @@ int64_t extent(const int64_t (&stride)[3], int64_t B, int64_t L, int64_t heads, 
   return (B - 1) * stride[0] + (L - 1) * stride[1] + (heads - 1) * stride[2] + D;
 }
 
-HeadView view(const void* p, const int64_t (&stride)[3], int share) {
-  return HeadView{p, stride[0], stride[1], stride[2], share};
+HeadView view(const void* p, const int64_t (&stride)[3], int share, int64_t total) {
+  return HeadView{p, stride[0], stride[1], stride[2], share, total};
 }
 
-HeadView dense(const void* p, int64_t L, int64_t H, int64_t D) { return HeadView{p, L * H * D, H * D, D, 1}; }
+HeadView dense(const void* p, int64_t B, int64_t L, int64_t H, int64_t D) {
+  return HeadView{p, L * H * D, H * D, D, 1, B * L * H * D};
+}
 
 bool heads_ok(int64_t B, int64_t L, int64_t H, int64_t Hq, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv) {
   if (!batch_ok(B, H, L) || Dk < 1 || Dk > HYENA_MAX_HEAD || Dv < 1 || Dv > HYENA_MAX_HEAD) return false;
@@ -101,9 +103,9 @@ hyena_status hyena_linear_attention(const hyena_linear_attention_params* p, void
   if (const hyena_status s = check_spans(out, in)) return s;
   LinArgs a{};
   LinPass& f = a.pass[0];
-  f.q = view(p->q, p->q_stride, p->H / p->Hq);
-  f.k = view(p->k, p->k_stride, p->H / p->Hk);
-  f.v = view(p->v, p->v_stride, p->H / p->Hv);
+  f.q = view(p->q, p->q_stride, p->H / p->Hq, ext[0]);
+  f.k = view(p->k, p->k_stride, p->H / p->Hk, ext[1]);
+  f.v = view(p->v, p->v_stride, p->H / p->Hv, ext[2]);
   f.out = o;
   f.out_f32 = io == HYENA_FP32;
   f.DK = p->Dk;
@@ -139,9 +141,9 @@ hyena_status hyena_linear_attention_step(const hyena_linear_attention_params* p,
   const Span in[] = {{p->q, ext[0] * e, e}, {p->k, ext[1] * e, e}, {p->v, ext[2] * e, e}, {p->log_decay, p->H * 4, 4}};
   if (const hyena_status s = check_spans(out, in)) return s;
   LinStepArgs a{};
-  a.q = view(p->q, p->q_stride, p->H / p->Hq);
-  a.k = view(p->k, p->k_stride, p->H / p->Hk);
-  a.v = view(p->v, p->v_stride, p->H / p->Hv);
+  a.q = view(p->q, p->q_stride, p->H / p->Hq, ext[0]);
+  a.k = view(p->k, p->k_stride, p->H / p->Hk, ext[1]);
+  a.v = view(p->v, p->v_stride, p->H / p->Hv, ext[2]);
   a.log_decay = p->log_decay;
   a.state = state;
   a.o = o;
@@ -179,8 +181,8 @@ hyena_status hyena_linear_attention_backward(const hyena_linear_attention_params
                      {p->state, st, 16}, {gstate_out, st, 16}, {p->log_decay, p->H * 4, 4}, {p->lengths, p->B * 4, 4}};
   if (const hyena_status s = check_spans(out, in)) return s;
   char* const ws = static_cast<char*>(workspace);
-  const HeadView q = view(p->q, p->q_stride, p->H / p->Hq), k = view(p->k, p->k_stride, p->H / p->Hk),
-                 v = view(p->v, p->v_stride, p->H / p->Hv), d = dense(go, p->L, p->H, p->Dv);
+  const HeadView q = view(p->q, p->q_stride, p->H / p->Hq, ext[0]), k = view(p->k, p->k_stride, p->H / p->Hk, ext[1]),
+                 v = view(p->v, p->v_stride, p->H / p->Hv, ext[2]), d = dense(go, p->B, p->L, p->H, p->Dv);
   void* const grads[3] = {g->gq, g->gk, g->gv};
   LinArgs a{};
   FoldArgs f{};
@@ -271,8 +273,8 @@ hyena_status hyena_rotary(const hyena_rotary_params* p, const void* x, void* out
   const Span outs[] = {{out, in_place ? ext * e : tokens * p->H * p->D * e, in_place ? e : 16}};
   const Span in[] = {{in_place ? nullptr : x, ext * e, e}, {p->freq, (int64_t)p->R * 4, 8}, {p->positions, pos * 4, 4}};
   if (const hyena_status s = check_spans(outs, in)) return s;
-  a.x = view(x, p->x_stride, 1);
-  a.out = in_place ? a.x : dense(out, p->L, p->H, p->D);
+  a.x = view(x, p->x_stride, 1, ext);
+  a.out = in_place ? a.x : dense(out, p->B, p->L, p->H, p->D);
   a.out.p = out;
   a.freq = p->freq;
   a.positions = p->positions;

@@ -27,8 +27,7 @@ __device__ __forceinline__ void turn(double position, double freq, float scale, 
 // Thread -> token, share of its heads, word: words of 8 pairs, then, out of
 // place, words of 8 copied values.  Neighbours take neighbouring words, then heads.
 template <int IOT, bool IL>
-__global__ __launch_bounds__(256) void k_rotary(RotaryArgs a, int words, int turning, int groups, int64_t x_total,
-                                                int64_t out_total) {
+__global__ __launch_bounds__(256) void k_rotary(RotaryArgs a, int words, int turning, int groups) {
   const uint32_t at = blockIdx.x * 256u + threadIdx.x;   // a launch holds fewer than 2^32 threads
   const uint32_t rest = at / (uint32_t)words, token = rest / (uint32_t)groups;
   if (token >= a.tokens) return;
@@ -41,7 +40,7 @@ __global__ __launch_bounds__(256) void k_rotary(RotaryArgs a, int words, int tur
     const int d = a.R + 8 * (w - turning), n = min(a.D - d, 8);
     for (int h = h0; h < a.H; h += groups) {
       float v[8];
-      widen8<IOT>(ld8n<IOT>(a.x.p, xi + h * a.x.head + d, n, x_total), v);
+      widen8<IOT>(ld8n<IOT>(a.x.p, xi + h * a.x.head + d, n, a.x.total), v);
       st8n<IOT>(const_cast<void*>(a.out.p), oi + h * a.out.head + d, v, n);
     }
     return;
@@ -56,8 +55,8 @@ __global__ __launch_bounds__(256) void k_rotary(RotaryArgs a, int words, int tur
   const int n0 = IL ? min(2 * n, 8) : n, n1 = IL ? 2 * n - 8 : n;
   for (int h = h0; h < a.H; h += groups) {
     float u[8], v[8], p[8], q[8];
-    widen8<IOT>(ld8n<IOT>(a.x.p, xi + h * a.x.head + d0, n0, x_total), u);
-    widen8<IOT>(ld8n<IOT>(a.x.p, xi + h * a.x.head + d1, n1, x_total), v);
+    widen8<IOT>(ld8n<IOT>(a.x.p, xi + h * a.x.head + d0, n0, a.x.total), u);
+    widen8<IOT>(ld8n<IOT>(a.x.p, xi + h * a.x.head + d1, n1, a.x.total), v);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       if constexpr (!IL) {
@@ -79,16 +78,13 @@ __global__ __launch_bounds__(256) void k_rotary(RotaryArgs a, int words, int tur
 
 hipError_t rotary(const RotaryArgs& a, hipStream_t s) {
   const int turning = (int)rotary_turning(a), words = (int)rotary_words(a), groups = (int)rotary_shares(a);
-  const auto extent = [&](const HeadView& v) {
-    return (a.tokens / a.L - 1) * v.batch + (a.L - 1) * v.token + (a.H - 1) * v.head + a.D;
-  };
   const dim3 grid((unsigned)rotary_groups(a));
   if (a.io) {
-    if (a.interleaved) k_rotary<1, true><<<grid, 256, 0, s>>>(a, words, turning, groups, extent(a.x), extent(a.out));
-    else k_rotary<1, false><<<grid, 256, 0, s>>>(a, words, turning, groups, extent(a.x), extent(a.out));
+    if (a.interleaved) k_rotary<1, true><<<grid, 256, 0, s>>>(a, words, turning, groups);
+    else k_rotary<1, false><<<grid, 256, 0, s>>>(a, words, turning, groups);
   } else {
-    if (a.interleaved) k_rotary<0, true><<<grid, 256, 0, s>>>(a, words, turning, groups, extent(a.x), extent(a.out));
-    else k_rotary<0, false><<<grid, 256, 0, s>>>(a, words, turning, groups, extent(a.x), extent(a.out));
+    if (a.interleaved) k_rotary<0, true><<<grid, 256, 0, s>>>(a, words, turning, groups);
+    else k_rotary<0, false><<<grid, 256, 0, s>>>(a, words, turning, groups);
   }
   return hipGetLastError();
 }

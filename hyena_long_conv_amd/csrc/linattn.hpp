@@ -15,6 +15,7 @@ struct HeadView {
   const void* p;
   int64_t batch, token, head;
   int share;
+  int64_t total;           // elements from the first to behind the last
 };
 
 // ------------------------------------------------------- linear attention
@@ -49,17 +50,23 @@ struct LinArgs {
   int64_t seg;
 };
 
-// How a pass fills the chip.
+// How a pass fills the chip: the time axis in segments, so that B H segments
+// (of 64 or 128 columns of the state each) are some `kLinFill` workgroups.
+constexpr int kLinFill = 768;
+constexpr int64_t kLinSegment = 256;   // the fewest tokens of a segment; a multiple of the kernels' blocks
 struct LinPlan {
   int segs;
   int64_t seg;
 };
 inline LinPlan lin_plan(int64_t B, int64_t L, int64_t H, int64_t DK, int64_t DV) {
-  LinPlan p{1, L};
-  (void)B, (void)H, (void)DK, (void)DV;
-  return p;
+  const int64_t cols = DK > 128 || DV <= 64 ? 64 : 128, groups = B * H * ((DV + cols - 1) / cols);
+  int64_t segs = kLinFill / groups, most = (L + kLinSegment - 1) / kLinSegment;
+  if (segs > most) segs = most;
+  if (segs < 1) segs = 1;
+  int64_t seg = (L + segs - 1) / segs;
+  seg = (seg + 63) / 64 * 64;
+  return LinPlan{(int)((L + seg - 1) / seg), seg};
 }
-
 inline LinPlan lin_backward_plan(int64_t B, int64_t L, int64_t H, int64_t Dk, int64_t Dv) {
   return lin_plan(B, L, H, Dk, Dv);
 }
