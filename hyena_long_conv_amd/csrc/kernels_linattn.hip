@@ -22,14 +22,21 @@ __device__ __forceinline__ Decay decay_of(float g, int64_t n) {
 }
 __device__ __forceinline__ float decayed(float s, Decay d, float add) { return fmaf(s, d.f, fmaf(s, d.keep, add)); }
 
-// lambda^n with g2 = log2(e) log_decay
-__device__ __forceinline__ float power_of(float g2, int n) { return n == 0 ? 1.f : exp2_fast(g2 * (float)n); }
+// lambda^n.  The exponent's product with log2(e) is kept in two parts: its
+// rounding, and log2(e)'s, would cost |log_decay n| units of the last place,
+// alike in every block.
+__device__ __forceinline__ float power_of(float g, int n) {
+  if (n == 0) return 1.f;
+  const float x = g * (float)n, hi = x * kLog2e;
+  const float lo = fmaf(x, 1.92596299e-8f, fmaf(x, kLog2e, -hi)) + fmaf(g, (float)n, -x) * kLog2e;
+  return x < -87.f ? 0.f : exp2_fast(hi) * fmaf(lo, 0.6931471805599453f, 1.f);
+}
 
 // -------------------------------------------------- passes over sequences
 //
-// A workgroup of 4 waves walks over a sequence (or a segment of it) in blocks
-// of C tokens and keeps DVT columns of a head's state, 16 NC for each wave, in
-// the accumulators of its matrix instructions.  For a block with the state S
+// A workgroup of 4 or 8 waves walks over a sequence (or a segment of it) in blocks
+// of C tokens and keeps 16 columns of a head's state for each wave in the
+// accumulators of its matrix instructions.  For a block with the state S
 // in front of it, weights W = tril(lambda^(i-j)) and the rows k, q, v in LDS:
 //   P   = so su W * (q k^T)                     shared out by tiles of 16 x 16,
 //   out = so lambda^(i+1) (q S) + P v,
@@ -63,34 +70,60 @@ __device__ __forceinline__ f32x4v mma(const Frag<0>& x, const Frag<0>& y, f32x4v
   return c;
 }
 
-// Rows of LDS hold D values and a gap that keeps the reads below on all banks:
-// 8 rows of 32 bytes (bf16, transposed), 4 rows of 64 (fp32, transposed).
-template <int IOT> struct Lds;
-template <> struct Lds<0> {
+// Rows of D values in LDS.  Word w of 16 bytes of row r lies in slot w ^ twist(r),
+// so that reads keep to different banks: by rows, 16 rows of a word or half a
+// word (8 bytes of bf16 for each group of lanes), and transposed, 8 rows of 4
+// halves (bf16) or 4 rows, 4 apart, of 4 words (fp32).  twist takes the row's
+// last four bits and D is a power of two, so value d of row r0 + r, r0 a
+// multiple of 16 and r < 16, is at r0 D + (base(r) ^ d).
+template <int IOT, int D> struct Lds;
+template <int D> struct Lds<0, D> {
   typedef float T;
-  static constexpr int GAP = 4;
-  static __device__ __forceinline__ f32x4v four(const float* p) { return *reinterpret_cast<const f32x4v*>(p); }
-  // values of four rows at one column: lane l of its 16 gets column l
-  static __device__ __forceinline__ f32x4v four_rows(const float* p, int stride, int l) {
-    p += l;
-    return f32x4v{p[0], p[stride], p[2 * stride], p[3 * stride]};
+  typedef f32x4v Four;
+  static __device__ __forceinline__ int base(int r) { return (r * D) ^ (r << 2); }
+  // four values of row r0 + r from d, a multiple of 4
+  static __device__ __forceinline__ Four row(const T* p, int r0, int base_r, int d) {
+    return *reinterpret_cast<const Four*>(p + r0 * D + (base_r ^ d));
   }
-  static __device__ __forceinline__ f32x4v narrow(f32x4v v) { return v; }
-  static __device__ __forceinline__ float one(float v) { return v; }
+  // values of rows r .. r + 3 behind r0 (r a multiple of 4) at columns d .. d + 15 (a multiple of 16): with
+  // base_c = column_base(r, l), lane l of its 16 gets column l's
+  static __device__ __forceinline__ int column_base(int r, int l) { return base(r) ^ l; }
+  static __device__ __forceinline__ Four column(const T* p, int r0, int base_c, int d) {
+    p += r0 * D;
+    return Four{p[base_c ^ d], p[base_c ^ d ^ base(1)], p[base_c ^ d ^ base(2)], p[base_c ^ d ^ base(3)]};
+  }
 };
-template <> struct Lds<1> {
+template <int D> struct Lds<1, D> {
   typedef uint16_t T;
-  static constexpr int GAP = 16;
-  static __device__ __forceinline__ u32x2v four(const uint16_t* p) { return *reinterpret_cast<const u32x2v*>(p); }
-  // the transposing read: lane l gives the address of row l / 4, columns 4 (l % 4), and gets column l
-  static __device__ __forceinline__ u32x2v four_rows(const uint16_t* p, int stride, int l) {
-    const uint16_t* at = p + (l >> 2) * stride + 4 * (l & 3);
-    return __builtin_bit_cast(u32x2v, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)at));
+  typedef u32x2v Four;
+  static __device__ __forceinline__ int base(int r) {
+    const int twist = D >= 128 ? ((r & 7) << 1) | ((r >> 3) & 1) : (r & 6) | ((r >> 3) & 1);
+    return (r * D) ^ (twist << 3);
   }
-  static __device__ __forceinline__ u32x2v narrow(f32x4v v) { return u32x2v{bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3])}; }
-  static __device__ __forceinline__ float one(uint16_t v) { return bf16_bits_to_f32(v); }
+  static __device__ __forceinline__ Four row(const T* p, int r0, int base_r, int d) {
+    return *reinterpret_cast<const Four*>(p + r0 * D + (base_r ^ d));
+  }
+  // the transposing read: lane l gives the address of row l / 4, columns 4 (l % 4), and gets column l
+  static __device__ __forceinline__ int column_base(int r, int l) { return base(r + (l >> 2)) ^ (4 * (l & 3)); }
+  static __device__ __forceinline__ Four column(const T* p, int r0, int base_c, int d) {
+    return __builtin_bit_cast(Four, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(p + r0 * D + (base_c ^ d))));
+  }
 };
 
+// The same value, which the compiler cannot tell: what is computed from it is
+// computed where it is used, instead of once and kept in registers.
+__device__ __forceinline__ int here(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
+__device__ __forceinline__ u32x2v narrow4(f32x4v v) { return u32x2v{bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3])}; }
+template <int IOT> __device__ __forceinline__ auto as_operand(f32x4v v) {
+  if constexpr (IOT == 0) return v;
+  else return narrow4(v);
+}
+__device__ __forceinline__ float one(float v) { return v; }
+__device__ __forceinline__ float one(uint16_t v) { return bf16_bits_to_f32(v); }
 __device__ __forceinline__ f32x4v widen4(f32x4v v) { return v; }
 __device__ __forceinline__ f32x4v widen4(u32x2v v) {
   return f32x4v{__uint_as_float(v[0] << 16), __uint_as_float(v[0] & 0xffff0000u), __uint_as_float(v[1] << 16),
@@ -105,59 +138,89 @@ __device__ __forceinline__ void parts_of(f32x4v a, f32x4v b, Frag<0> (&o)[1]) { 
 __device__ __forceinline__ void parts_of(f32x4v a, f32x4v b, Frag<1> (&o)[3]) {
 #pragma unroll
   for (int k = 0; k < 3; ++k) {
-    o[k] = {Lds<1>::narrow(a), Lds<1>::narrow(b)};
+    o[k] = {narrow4(a), narrow4(b)};
     if (k < 2) a -= widen4(o[k].a), b -= widen4(o[k].b);
   }
 }
 
 // A block's rows of one operand on their way from global memory to LDS: W
 // words of 8 values to a row, NW words to a thread, in one column of words.
-template <int IOT, int C, int D>
+// EVEN: heads of whole words, and rows near enough to each other for offsets
+// of 32 bits inside a block; a word behind the block's tokens or the head's
+// values is then read from the row or the head's start and set to zero on
+// its way, so that no load waits for a condition.
+template <int IOT, int C, int D, int THREADS, bool EVEN>
 struct Rows {
-  static constexpr int W = D / 8, NW = C * W / 256, STEP = 256 / W, STRIDE = D + Lds<IOT>::GAP;
-  static_assert(NW >= 1 && NW * 256 == C * W, "whole words for each thread");
+  static constexpr int W = D / 8, NW = C * W > THREADS ? C * W / THREADS : 1, STEP = THREADS / W,
+                       E = IOT == 0 ? 4 : 2;
+  typedef Lds<IOT, D> M;
+  static_assert(C * W % THREADS == 0 || THREADS % (C * W) == 0, "whole words for each thread, or one for some");
   Raw8<IOT> word[NW];
-  const char* base;      // the head's first value of the sequence
-  int64_t first, step;   // elements to the walk's first token, and from one token to the next
-  int64_t total;         // elements behind base
+  const char* base;              // the head's first value of the sequence
+  int64_t token;                 // elements between tokens
+  int64_t last;                  // backward in time: the sequence's last token; otherwise -1
+  int64_t total;                 // elements behind base
   int d, row, col;
   bool live;
-  __device__ __forceinline__ void init(const HeadView& v, int64_t b, int h, int d_, int64_t n, bool reverse) {
-    constexpr int E = IOT == 0 ? 4 : 2;
-    const int64_t at = b * v.batch + h / v.share * v.head;
+  __device__ __forceinline__ void init(const HeadView& v, int64_t b, int h, int c0, int d_, int64_t n, bool reverse) {
+    const int64_t at = b * v.batch + h / v.share * v.head + c0;
     base = static_cast<const char*>(v.p) + at * E;
     total = v.total - at;
-    first = reverse ? (n - 1) * v.token : 0;
-    step = reverse ? -v.token : v.token;
-    d = d_;
-    row = threadIdx.x / W;
+    token = v.token;
+    last = reverse ? n - 1 : -1;
+    d = d_ - c0;
+    row = threadIdx.x / W % C;
     col = 8 * (threadIdx.x % W);
     live = col < d;
   }
-  // The block at token t0 of the walk, zeros from token `end` on.
-  __device__ __forceinline__ void load(int64_t t0, int64_t end) {
-    if (t0 + C <= end && d % 8 == 0) {
-      const int64_t at = first + (t0 + row) * step + (live ? col : 0);
+  // The block's `now` tokens from t0 on.
+  __device__ __forceinline__ void load(int64_t t0, int now) {
+    const bool back = last >= 0;
+    if constexpr (EVEN) {
+      const char* at = base + (back ? last - t0 - (now - 1) : t0) * token * E;   // its first value in memory
+      const uint32_t inside = live ? col * E : 0, step = (uint32_t)token * E;
+      if (now == C) {
+        const uint32_t off = (uint32_t)(back ? C - 1 - row : row) * step + inside;
+        if (!back) {
 #pragma unroll
-      for (int m = 0; m < NW; ++m) word[m] = ld8<IOT>(base, at + m * STEP * step);
+          for (int m = 0; m < NW; ++m) word[m] = ld8<IOT>(at + m * STEP * (int64_t)step + off, 0);
+        } else {
+#pragma unroll
+          for (int m = 0; m < NW; ++m) word[m] = ld8<IOT>(at - m * STEP * (int64_t)step + off, 0);
+        }
+      } else {
+#pragma unroll
+        for (int m = 0; m < NW; ++m) {
+          const int r = min(row + m * STEP, now - 1);
+          word[m] = ld8<IOT>(at + (uint32_t)(back ? now - 1 - r : r) * step + inside, 0);
+        }
+      }
     } else {
 #pragma unroll
       for (int m = 0; m < NW; ++m) {
-        const int64_t t = t0 + row + m * STEP;
-        word[m] = ld8n<IOT>(base, t < end ? first + t * step + col : 0, t < end ? d - col : 0, total);
+        const int r = row + m * STEP;
+        const int64_t t = back ? last - t0 - r : t0 + r;
+        word[m] = ld8n<IOT>(base, r < now ? t * token + col : 0, r < now ? d - col : 0, total);
       }
     }
   }
-  __device__ __forceinline__ void store(typename Lds<IOT>::T* lds) const {
+  // The words of the last load, `had` tokens of them.
+  __device__ __forceinline__ void store(typename M::T* lds, int had) const {
+    if (THREADS > C * W && threadIdx.x >= C * W) return;
+    if (!EVEN || (had == C && d >= D)) put<false>(lds, had);
+    else put<true>(lds, had);
+  }
+  template <bool MASK>
+  __device__ __forceinline__ void put(typename M::T* lds, int had) const {
 #pragma unroll
     for (int m = 0; m < NW; ++m) {
-      const Raw8<IOT> w = live ? word[m] : zero8<IOT>();
-      auto* to = lds + (row + m * STEP) * STRIDE + col;
+      const Raw8<IOT> w = !MASK || (live && row + m * STEP < had) ? word[m] : zero8<IOT>();
+      const int r = row + m * STEP, b = M::base(r & 15), r0 = (r & ~15) * D;
       if constexpr (IOT == 0) {
-        *reinterpret_cast<f32x4v*>(to) = w.a;
-        *reinterpret_cast<f32x4v*>(to + 4) = w.b;
+        *reinterpret_cast<f32x4v*>(lds + r0 + (b ^ col)) = w.a;
+        *reinterpret_cast<f32x4v*>(lds + r0 + (b ^ (col + 4))) = w.b;
       } else {
-        *reinterpret_cast<u32x4v*>(to) = w.a;
+        *reinterpret_cast<u32x4v*>(lds + r0 + (b ^ col)) = w.a;
       }
     }
   }
@@ -175,7 +238,7 @@ __device__ __forceinline__ void st4n(void* p, int64_t i, f32x4v v, int n) {
   } else {
     typedef uint32_t u2 __attribute__((ext_vector_type(2), aligned(2)));
     if (n >= 4) {
-      const u32x2v w = Lds<1>::narrow(v);
+      const u32x2v w = narrow4(v);
       *reinterpret_cast<u2*>(static_cast<uint16_t*>(p) + i) = u2{w[0], w[1]};
       return;
     }
@@ -185,26 +248,35 @@ __device__ __forceinline__ void st4n(void* p, int64_t i, f32x4v v, int n) {
     if (e < n) st1<IOT>(p, i + e, v[e]);
 }
 
+#ifndef HYENA_LIN_EU
+#define HYENA_LIN_EU (DK >= 256 || (DK >= 128 && WAVES == 4) ? 2 : 4)
+#endif
 template <int IOT> constexpr int kBlock = IOT == 1 ? 64 : 32;   // tokens of a block
 
-template <int IOT, int DK, int NC, bool FILL>
+template <int IOT, int DK, int WAVES, bool FILL>
 constexpr int lin_lds_bytes() {
-  constexpr int C = kBlock<IOT>, E = sizeof(typename Lds<IOT>::T), G = Lds<IOT>::GAP;
-  return (C * ((FILL ? 1 : 2) * (DK + G) + 64 * NC + G) + (FILL ? 0 : C * C)) * E;
+  constexpr int C = kBlock<IOT>, E = IOT == 0 ? 4 : 2;
+  return (C * ((FILL ? 1 : 2) * DK + 16 * WAVES) + (FILL ? 0 : C * C)) * E + (3 * C + 16) * 4;
 }
 
 // FILL: the state behind a segment alone, from nothing, for all but the last segment.
-template <int IOT, int DK, int NC, bool FILL>
-__global__ __launch_bounds__(256, 2) void k_lin(LinArgs a, int first_pass) {
-  typedef typename Lds<IOT>::T T;
-  constexpr int C = kBlock<IOT>, IT = C / 16, JJ = C / 32, KT = DK / 16, DVT = 64 * NC, NP = kParts<IOT>;
+template <int IOT, int DK, int WAVES, bool FILL, bool EVEN, bool OUT32>
+__global__ __launch_bounds__(64 * WAVES, HYENA_LIN_EU) void k_lin(LinArgs a, int first_pass) {
+  constexpr int C = kBlock<IOT>, IT = C / 16, JJ = C / 32, KT = DK / 16, DVT = 16 * WAVES, NP = kParts<IOT>;
+  typedef Lds<IOT, DK> MK;
+  typedef Lds<IOT, DVT> MV;
+  typedef typename MK::T T;
+  typedef typename MK::Four Four;
   const LinPass& p = a.pass[first_pass + blockIdx.y];
   if (FILL && !p.seg_fills) return;
   extern __shared__ __attribute__((aligned(16))) unsigned char shared[];
-  T* const lk = reinterpret_cast<T*>(shared);
-  T* const lv = lk + C * Rows<IOT, C, DK>::STRIDE;
-  T* const lq = lv + C * Rows<IOT, C, DVT>::STRIDE;
-  T* const lp = lq + C * Rows<IOT, C, DK>::STRIDE;   // tiles (i, j) of 16 x 16 at i IT + j, 4 values to a lane
+  float* const weight = reinterpret_cast<float*>(shared);   // su lambda^(count-1-j) of a block's tokens,
+  float* const through = weight + C;                         // and so lambda^(i+1)
+  float* const apart = through + C;                          // so su lambda^n at C - 1 - n, zeros behind it
+  T* const lk = reinterpret_cast<T*>(apart + C + 16);
+  T* const lv = lk + C * DK;
+  T* const lq = lv + C * DVT;
+  T* const lp = lq + C * DK;   // tiles (i, j) of 16 x 16 at i IT + j, 4 values to a lane
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = lane & 15, g = lane >> 4;
 
   const int tiles = (p.DV + DVT - 1) / DVT, segs = FILL ? a.segs - 1 : a.segs;
@@ -212,12 +284,12 @@ __global__ __launch_bounds__(256, 2) void k_lin(LinArgs a, int first_pass) {
   const int bh = rest / segs, sg = rest - bh * segs, b = bh / a.H, h = bh - b * a.H, c0 = tile * DVT;
   const int64_t n = a.lengths ? min(max((int64_t)a.lengths[b], (int64_t)0), a.L) : a.L;
   const int64_t t0 = sg * a.seg, end = min(n, t0 + a.seg), size = (int64_t)p.DK * p.DV;
-  const float gd = a.log_decay ? a.log_decay[h] : 0.f, g2 = gd * kLog2e;
+  const float gd = a.log_decay ? a.log_decay[h] : 0.f;
   if (FILL && t0 >= n) return;
 
-  // the state: rows 16 kt + 4 g + r, column 16 (NC wave + c) + l of the tile
-  const int mine = c0 + 16 * NC * wave;
-  f32x4v S[KT][NC];
+  // the state: rows 16 k + 4 g + r, column 16 wave + l of the tile
+  const int dv = c0 + 16 * wave + l;
+  f32x4v S[KT];
   {
     const float* s0 = nullptr;
     int sk = 0, sv = 0;
@@ -226,212 +298,172 @@ __global__ __launch_bounds__(256, 2) void k_lin(LinArgs a, int first_pass) {
       else if (p.s0) s0 = p.s0 + bh * size, sk = p.s0_k, sv = p.s0_v;
     }
 #pragma unroll
-    for (int kt = 0; kt < KT; ++kt)
+    for (int k = 0; k < KT; ++k)
 #pragma unroll
-      for (int c = 0; c < NC; ++c)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int dk = 16 * kt + 4 * g + r, dv = mine + 16 * c + l;
-          S[kt][c][r] = s0 && t0 < max(n, (int64_t)1) && dk < p.DK && dv < p.DV ? s0[(int64_t)dk * sk + (int64_t)dv * sv] : 0.f;
-        }
+      for (int r = 0; r < 4; ++r) {
+        const int dk = 16 * k + 4 * g + r;
+        S[k][r] = s0 && t0 < max(n, (int64_t)1) && dk < p.DK && dv < p.DV ? s0[(int64_t)dk * sk + (int64_t)dv * sv] : 0.f;
+      }
   }
 
   if (t0 < end) {
-    Rows<IOT, C, DK> rk, rq;
-    Rows<IOT, C, DVT> rv;
-    rk.init(p.k, b, h, p.DK, n, p.reverse);
-    rv.init(p.v, b, h, p.DV, n, p.reverse);
-    // this workgroup's columns of v
-    rv.base += (int64_t)c0 * sizeof(T);
-    rv.total -= c0;
-    rv.d -= c0;
-    rv.live = rv.col < rv.d;
-    rk.load(t0, end);
-    rv.load(t0, end);
+    Rows<IOT, C, DK, 64 * WAVES, EVEN> rk, rq;
+    Rows<IOT, C, DVT, 64 * WAVES, EVEN> rv;
+    const int first = (int)min(end - t0, (int64_t)C);
+    rk.init(p.k, b, h, 0, p.DK, n, p.reverse);
+    rv.init(p.v, b, h, c0, p.DV, n, p.reverse);
+    rk.load(t0, first);
+    rv.load(t0, first);
     if (!FILL) {
-      rq.init(p.q, b, h, p.DK, n, p.reverse);
-      rq.load(t0, end);
+      rq.init(p.q, b, h, 0, p.DK, n, p.reverse);
+      rq.load(t0, first);
     }
-    // what depends on the tokens of a block and on whether the state decays before its first one
-    float weight[JJ][8], through[IT];
     Decay whole{0.f, 1.f};
-    auto powers = [&](int count, int lead) {
-#pragma unroll
-      for (int j = 0; j < JJ; ++j)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int left = count - 1 - (32 * j + 16 * (e >> 2) + 4 * g + (e & 3));
-          weight[j][e] = left >= 0 ? p.su * power_of(g2, left) : 0.f;
-        }
-#pragma unroll
-      for (int i = 0; i < IT; ++i) through[i] = p.so * power_of(g2, 16 * i + l + lead);
-      whole = decay_of(gd, count - 1 + lead);
-    };
-    // P's tiles of this wave: number wave, wave + 4, .. of those on and below the diagonal
-    constexpr int TILES = IT * (IT + 1) / 2, MINE = (TILES + 3) / 4;
-    auto tile_at = [](int k, int& i, int& j) {
-      i = k < 1 ? 0 : k < 3 ? 1 : k < 6 ? 2 : 3;
-      j = k - i * (i + 1) / 2;
-    };
-    float pair[MINE][4];
-    if (!FILL) {
-#pragma unroll
-      for (int m = 0; m < MINE; ++m) {
-        int i, j;
-        tile_at(wave + 4 * m, i, j);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int apart = 16 * (i - j) + l - 4 * g - r;
-          pair[m][r] = apart >= 0 ? p.so * p.su * power_of(g2, apart) : 0.f;
-        }
-      }
-    }
-    int lead = p.reverse && sg == 0 ? 0 : 1, count = 0;
+    // P's tiles of this wave: number wave, wave + WAVES, .. of those on and below the diagonal
+    constexpr int TILES = IT * (IT + 1) / 2, MINE = (TILES + WAVES - 1) / WAVES;
+    if (!FILL && threadIdx.x < C + 16) apart[threadIdx.x] = threadIdx.x < C ? p.so * p.su * power_of(gd, C - 1 - threadIdx.x) : 0.f;
+    // this lane's outputs: token l of a tile, values d0 .. d0 + 3
+    const int d0 = c0 + 16 * wave + 4 * g;
+    const int64_t out_step = (p.reverse ? -1 : 1) * (int64_t)a.H * p.DV * (OUT32 ? 4 : 2);
+    char* out = nullptr;
+    if (!FILL)
+      out = static_cast<char*>(p.out) + (((b * a.L + (p.reverse ? n - 1 - t0 : t0)) * a.H + h) * p.DV + d0) * (OUT32 ? 4 : 2) + l * out_step;
+    int count = 0;
     for (int64_t t = t0; t < end; t += C) {
       const int now = (int)min(end - t, (int64_t)C);
-      if (now != count || t <= t0 + C) {
-        count = now;
-        powers(count, t == t0 ? lead : 1);
-      }
       __syncthreads();                                // the block before has been read
-      rk.store(lk);
-      rv.store(lv);
-      if (!FILL) rq.store(lq);
+      if (now != count || t <= t0 + C) {              // from the last token on, the first one finds the state undecayed
+        const int lead = p.reverse && t == 0 ? 0 : 1, i = threadIdx.x;
+        count = now;
+        if (i < C) {
+          weight[i] = i < count ? p.su * power_of(gd, count - 1 - i) : 0.f;
+          through[i] = p.so * power_of(gd, i + lead);
+        }
+        whole = decay_of(gd, count - 1 + lead);
+      }
+      rk.store(lk, now);
+      rv.store(lv, now);
+      if (!FILL) rq.store(lq, now);
       __syncthreads();
       if (t + C < end) {
-        rk.load(t + C, end);
-        rv.load(t + C, end);
-        if (!FILL) rq.load(t + C, end);
+        const int next = (int)min(end - t - C, (int64_t)C);
+        rk.load(t + C, next);
+        rv.load(t + C, next);
+        if (!FILL) rq.load(t + C, next);
       }
       if constexpr (!FILL) {
 #pragma unroll
         for (int m = 0; m < MINE; ++m) {
-          const int k = wave + 4 * m;
+          const int k = wave + WAVES * m;
           if (k >= TILES) break;
-          int i, j;
-          tile_at(k, i, j);
+          const int i = k < 1 ? 0 : k < 3 ? 1 : k < 6 ? 2 : 3, j = k - i * (i + 1) / 2;
           f32x4v acc = {0.f, 0.f, 0.f, 0.f};
-          const T* kr = lk + (16 * j + l) * (DK + Lds<IOT>::GAP) + 4 * g;
-          const T* qr = lq + (16 * i + l) * (DK + Lds<IOT>::GAP) + 4 * g;
+          const int at = here(MK::base(l) ^ (4 * g));
 #pragma unroll
-          for (int kk = 0; kk < DK / 32; ++kk)
-            acc = mma(Frag<IOT>{Lds<IOT>::four(kr + 32 * kk), Lds<IOT>::four(kr + 32 * kk + 16)},
-                      Frag<IOT>{Lds<IOT>::four(qr + 32 * kk), Lds<IOT>::four(qr + 32 * kk + 16)}, acc);
+          for (int d = 0; d < DK; d += 32)
+            acc = mma(Frag<IOT>{MK::row(lk, 16 * j, at, d), MK::row(lk, 16 * j, at, d + 16)},
+                      Frag<IOT>{MK::row(lq, 16 * i, at, d), MK::row(lq, 16 * i, at, d + 16)}, acc);
 #pragma unroll
-          for (int r = 0; r < 4; ++r) acc[r] = 16 * (i - j) + l >= 4 * g + r ? acc[r] * pair[m][r] : 0.f;
+          for (int r = 0; r < 4; ++r) acc[r] *= apart[C - 1 - 16 * (i - j) - l + 4 * g + r];
+          if (i == j) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[r] = l >= 4 * g + r ? acc[r] : 0.f;
+          }
           // bf16: a pair's weight is rounded once, as an output is
-          const auto w = Lds<IOT>::narrow(acc);
-          *reinterpret_cast<decltype(Lds<IOT>::narrow(acc))*>(lp + ((i * IT + j) * 64 + lane) * 4) = w;
+          *reinterpret_cast<Four*>(lp + ((i * IT + j) * 64 + lane) * 4) = as_operand<IOT>(acc);
         }
         __syncthreads();
       }
-      // v transposed: columns of this wave, 8 tokens to a lane
-      Frag<IOT> vt[JJ][NC];
+      // v transposed: this wave's columns, 8 tokens to a lane
+      Frag<IOT> vt[JJ];
 #pragma unroll
-      for (int j = 0; j < JJ; ++j)
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          const T* at = lv + (32 * j + 4 * g) * Rows<IOT, C, DVT>::STRIDE + 16 * (NC * wave + c);
-          vt[j][c] = {Lds<IOT>::four_rows(at, Rows<IOT, C, DVT>::STRIDE, l),
-                      Lds<IOT>::four_rows(at + 16 * Rows<IOT, C, DVT>::STRIDE, Rows<IOT, C, DVT>::STRIDE, l)};
-        }
+      for (int j = 0; j < JJ; ++j) {
+        const int at = here(MV::column_base(4 * g, l));
+        vt[j] = {MV::column(lv, 32 * j, at, 16 * wave), MV::column(lv, 32 * j + 16, at, 16 * wave)};
+      }
       if constexpr (!FILL) {
         // bf16: the state is rounded once for its product with q, and stays fp32
-        Frag<IOT> sf[KT / 2][NC];
+        Frag<IOT> sf[KT / 2];
 #pragma unroll
-        for (int k = 0; k < KT / 2; ++k)
-#pragma unroll
-          for (int c = 0; c < NC; ++c) sf[k][c] = {Lds<IOT>::narrow(S[2 * k][c]), Lds<IOT>::narrow(S[2 * k + 1][c])};
-#pragma unroll
-        for (int i = 0; i < IT; ++i) {
-          if (16 * i >= count) break;
-          f32x4v acc[NC];
+        for (int k = 0; k < KT / 2; ++k) sf[k] = {as_operand<IOT>(S[2 * k]), as_operand<IOT>(S[2 * k + 1])};
+#pragma unroll 1
+        for (int i = 0; i < IT && 16 * i < count; ++i) {
+          f32x4v acc;
           // A value that is not finite meets the zeros of P above the diagonal; where an output shows one, the
           // tile is formed again with the diagonal's products one by one (`careful`), so that it reaches no earlier token.
           for (bool careful = false;; careful = true) {
+            acc = f32x4v{0.f, 0.f, 0.f, 0.f};
+            const int at = here(MK::base(l) ^ (4 * g));
 #pragma unroll
-            for (int c = 0; c < NC; ++c) acc[c] = f32x4v{0.f, 0.f, 0.f, 0.f};
-            const T* qr = lq + (16 * i + l) * (DK + Lds<IOT>::GAP) + 4 * g;
-#pragma unroll
-            for (int k = 0; k < KT / 2; ++k) {
-              const Frag<IOT> qf{Lds<IOT>::four(qr + 32 * k), Lds<IOT>::four(qr + 32 * k + 16)};
-#pragma unroll
-              for (int c = 0; c < NC; ++c) acc[c] = mma(sf[k][c], qf, acc[c]);
-            }
-#pragma unroll
-            for (int c = 0; c < NC; ++c) acc[c] *= through[i];
+            for (int k = 0; k < KT / 2; ++k)
+              acc = mma(sf[k], Frag<IOT>{MK::row(lq, 16 * i, at, 32 * k), MK::row(lq, 16 * i, at, 32 * k + 16)}, acc);
+            acc *= through[16 * i + l];
             const T* pt = lp + (i * IT * 64 + lane) * 4;
+            const Frag<IOT> zero{};
 #pragma unroll
             for (int j = 0; j < JJ; ++j) {
               if (2 * j > i) break;
-              Frag<IOT> pf{Lds<IOT>::four(pt + 2 * j * 256), {}}, zero{};
-              if (2 * j + 1 <= i) pf.b = Lds<IOT>::four(pt + (2 * j + 1) * 256);
-              else pf.b = zero.b;
+              Frag<IOT> pf{*reinterpret_cast<const Four*>(pt + 2 * j * 256), zero.b};
+              if (2 * j + 1 <= i) pf.b = *reinterpret_cast<const Four*>(pt + (2 * j + 1) * 256);
               if (careful) {
                 if (2 * j == i) continue;
                 if (2 * j + 1 == i) pf.b = zero.b;
               }
-#pragma unroll
-              for (int c = 0; c < NC; ++c)
-                acc[c] = mma(careful && 2 * j + 1 == i ? Frag<IOT>{vt[j][c].a, zero.b} : vt[j][c], pf, acc[c]);
+              acc = mma(careful && 2 * j + 1 == i ? Frag<IOT>{vt[j].a, zero.b} : vt[j], pf, acc);
             }
             if (careful) {
+#pragma unroll 1
               for (int j = 0; j < 16; ++j) {
-                const float w = Lds<IOT>::one(lp[((i * IT + i) * 64 + (j >> 2) * 16 + l) * 4 + (j & 3)]);
+                const float w = one(lp[((i * IT + i) * 64 + (j >> 2) * 16 + l) * 4 + (j & 3)]);
 #pragma unroll
-                for (int c = 0; c < NC; ++c)
-#pragma unroll
-                  for (int r = 0; r < 4; ++r) {
-                    const float v = Lds<IOT>::one(lv[(16 * i + j) * Rows<IOT, C, DVT>::STRIDE + 16 * (NC * wave + c) + 4 * g + r]);
-                    acc[c][r] = j <= l ? fmaf(w, v, acc[c][r]) : acc[c][r];
-                  }
+                for (int r = 0; r < 4; ++r) {
+                  const float v = one(lv[16 * i * DVT + (MV::base(j) ^ (16 * wave + 4 * g + r))]);
+                  acc[r] = j <= l ? fmaf(w, v, acc[r]) : acc[r];
+                }
               }
               break;
             }
             float bad = 0.f;
 #pragma unroll
-            for (int c = 0; c < NC; ++c)
-#pragma unroll
-              for (int r = 0; r < 4; ++r) bad = fmaf(acc[c][r], 0.f, bad);
+            for (int r = 0; r < 4; ++r) bad = fmaf(acc[r], 0.f, bad);
             if (!__any(bad != 0.f)) break;
           }
-          const int64_t to = t + 16 * i + l;
           if (16 * i + l < count) {
-            const int64_t at = ((b * a.L + (p.reverse ? n - 1 - to : to)) * a.H + h) * p.DV;
-#pragma unroll
-            for (int c = 0; c < NC; ++c) {
-              const int dv = mine + 16 * c + 4 * g;
-              if (p.out_f32) st4n<0>(p.out, at + dv, acc[c], p.DV - dv);
-              else st4n<1>(p.out, at + dv, acc[c], p.DV - dv);
-            }
+            if (OUT32) st4n<0>(out, 0, acc, p.DV - d0);
+            else st4n<1>(out, 0, acc, p.DV - d0);
           }
+          out += 16 * out_step;
         }
       }
+      const int at = here(MK::column_base(4 * g, l));
+      if (whole.keep != 0.f) {
 #pragma unroll
-      for (int k = 0; k < KT; ++k)
+        for (int k = 0; k < KT; ++k)
 #pragma unroll
-        for (int c = 0; c < NC; ++c)
+          for (int r = 0; r < 4; ++r) S[k][r] = fmaf(S[k][r], whole.f, S[k][r]);
+      } else {
 #pragma unroll
-          for (int r = 0; r < 4; ++r) S[k][c][r] = decayed(S[k][c][r], whole, 0.f);
+        for (int k = 0; k < KT; ++k) S[k] *= whole.f;
+      }
 #pragma unroll
       for (int j = 0; j < JJ; ++j) {
-        Frag<IOT> vw[NC][NP];
+        Frag<IOT> vw[NP];
+        const float* at_j = weight + 32 * j + 4 * g;
+        const f32x4v x = widen4(vt[j].a) * *reinterpret_cast<const f32x4v*>(at_j);
+        const f32x4v y = widen4(vt[j].b) * *reinterpret_cast<const f32x4v*>(at_j + 16);
+        parts_of(x, y, vw);
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          f32x4v x = widen4(vt[j][c].a), y = widen4(vt[j][c].b);
+        for (int k0 = 0; k0 < KT; k0 += 4) {
+          Frag<IOT> kt[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) x[e] *= weight[j][e], y[e] *= weight[j][4 + e];
-          parts_of(x, y, vw[c]);
-        }
+          for (int k = 0; k < 4; ++k) {
+            kt[k] = {MK::column(lk, 32 * j, at, 16 * (k0 + k)), MK::column(lk, 32 * j + 16, at, 16 * (k0 + k))};
+          }
 #pragma unroll
-        for (int k = 0; k < KT; ++k) {
-          const T* at = lk + (32 * j + 4 * g) * (DK + Lds<IOT>::GAP) + 16 * k;
-          const Frag<IOT> kt{Lds<IOT>::four_rows(at, DK + Lds<IOT>::GAP, l),
-                             Lds<IOT>::four_rows(at + 16 * (DK + Lds<IOT>::GAP), DK + Lds<IOT>::GAP, l)};
+          for (int q = NP - 1; q >= 0; --q)
 #pragma unroll
-          for (int c = 0; c < NC; ++c)
-#pragma unroll
-            for (int q = NP - 1; q >= 0; --q) S[k][c] = mma(kt, vw[c][q], S[k][c]);
+            for (int k = 0; k < 4; ++k) S[k0 + k] = mma(kt[k], vw[q], S[k0 + k]);
+          __builtin_amdgcn_sched_barrier(0);          // no more operands in flight than registers for them
         }
       }
     }
@@ -439,33 +471,27 @@ __global__ __launch_bounds__(256, 2) void k_lin(LinArgs a, int first_pass) {
 
   // the state behind the segment, or behind the sequence
   float* to = nullptr;
-  if (FILL) {
-    to = p.seg + ((int64_t)bh * (a.segs - 1) + sg) * size;
-  } else if (p.s_out && (n == 0 ? sg == 0 : t0 < n && n <= t0 + a.seg)) {
-    to = p.s_out + bh * size;
-  }
+  if (FILL) to = p.seg + ((int64_t)bh * (a.segs - 1) + sg) * size;
+  else if (p.s_out && (n == 0 ? sg == 0 : t0 < n && n <= t0 + a.seg)) to = p.s_out + bh * size;
   if (to) {
     const int sk = FILL ? p.seg_k : p.DV, sv = FILL ? p.seg_v : 1;
     const bool as_is = FILL || !p.reverse || n == 0;
     const Decay last = decay_of(gd, 1);
 #pragma unroll
-    for (int kt = 0; kt < KT; ++kt)
+    for (int k = 0; k < KT; ++k)
 #pragma unroll
-      for (int c = 0; c < NC; ++c)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int dk = 16 * kt + 4 * g + r, dv = mine + 16 * c + l;
-          if (dk < p.DK && dv < p.DV)
-            to[(int64_t)dk * sk + (int64_t)dv * sv] = as_is ? S[kt][c][r] : decayed(S[kt][c][r], last, 0.f);
-        }
+      for (int r = 0; r < 4; ++r) {
+        const int dk = 16 * k + 4 * g + r;
+        if (dk < p.DK && dv < p.DV) to[(int64_t)dk * sk + (int64_t)dv * sv] = as_is ? S[k][r] : decayed(S[k][r], last, 0.f);
+      }
   }
   if (FILL) return;
   // zeros behind the sequence
   const int64_t z0 = max(n, t0), z1 = min(a.L, t0 + a.seg);
   const int cols = min(DVT, p.DV - c0);
-  for (int64_t i = threadIdx.x; i < (z1 - z0) * cols; i += 256) {
+  for (int64_t i = threadIdx.x; i < (z1 - z0) * cols; i += 64 * WAVES) {
     const int64_t t = z0 + i / cols, at = ((b * a.L + t) * a.H + h) * p.DV + c0 + i % cols;
-    if (p.out_f32) static_cast<float*>(p.out)[at] = 0.f;
+    if (OUT32) static_cast<float*>(p.out)[at] = 0.f;
     else static_cast<uint16_t*>(p.out)[at] = 0;
   }
 }
@@ -501,34 +527,51 @@ __global__ __launch_bounds__(256) void k_lin_join(LinArgs a, int first_pass) {
 }
 
 // One launch for passes [first, first + count), which share their sizes.
-template <int IOT, int DK, int NC>
+template <int IOT, int DK, int WAVES, bool EVEN>
 hipError_t launch_tiles(const LinArgs& a, int first, int count, hipStream_t s) {
   const LinPass& p = a.pass[first];
-  const int64_t tiles = (p.DV + 64 * NC - 1) / (64 * NC), bh = (int64_t)a.B * a.H;
+  const int64_t tiles = (p.DV + 16 * WAVES - 1) / (16 * WAVES), bh = (int64_t)a.B * a.H;
   bool fills = false;
   for (int i = first; i < first + count; ++i) fills = fills || a.pass[i].seg_fills;
   hipError_t e;
   if (a.segs > 1 && fills) {
-    constexpr int bytes = lin_lds_bytes<IOT, DK, NC, true>();
+    constexpr int bytes = lin_lds_bytes<IOT, DK, WAVES, true>();
     static_assert(bytes <= 160 * 1024, "");
-    k_lin<IOT, DK, NC, true><<<dim3((unsigned)(bh * (a.segs - 1) * tiles), count), 256, bytes, s>>>(a, first);
+    k_lin<IOT, DK, WAVES, true, EVEN, false><<<dim3((unsigned)(bh * (a.segs - 1) * tiles), count), 64 * WAVES, bytes, s>>>(a, first);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     const int64_t blocks = (p.DK * p.DV + 255) / 256;
     k_lin_join<<<dim3((unsigned)(bh * blocks), count), 256, 0, s>>>(a, first);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
-  constexpr int bytes = lin_lds_bytes<IOT, DK, NC, false>();
+  constexpr int bytes = lin_lds_bytes<IOT, DK, WAVES, false>();
   static_assert(bytes <= 160 * 1024, "");
-  k_lin<IOT, DK, NC, false><<<dim3((unsigned)(bh * a.segs * tiles), count), 256, bytes, s>>>(a, first);
+  const dim3 grid((unsigned)(bh * a.segs * tiles), count);
+  if (p.out_f32) k_lin<IOT, DK, WAVES, false, EVEN, true><<<grid, 64 * WAVES, bytes, s>>>(a, first);
+  else if constexpr (IOT == 1) k_lin<IOT, DK, WAVES, false, EVEN, false><<<grid, 64 * WAVES, bytes, s>>>(a, first);
   return hipGetLastError();
+}
+
+template <int IOT, bool EVEN>
+hipError_t launch_sizes(const LinArgs& a, int first, int count, hipStream_t s) {
+  const int dk = a.pass[first].DK, dv = a.pass[first].DV;
+  if (dv <= 64) {
+    if (dk > 128) return launch_tiles<IOT, 256, 4, EVEN>(a, first, count, s);
+    return dk > 64 ? launch_tiles<IOT, 128, 4, EVEN>(a, first, count, s) : launch_tiles<IOT, 64, 4, EVEN>(a, first, count, s);
+  }
+  if (dk > 128) return launch_tiles<IOT, 256, 8, EVEN>(a, first, count, s);
+  return dk > 64 ? launch_tiles<IOT, 128, 8, EVEN>(a, first, count, s) : launch_tiles<IOT, 64, 8, EVEN>(a, first, count, s);
 }
 
 template <int IOT>
 hipError_t launch_pass(const LinArgs& a, int first, int count, hipStream_t s) {
-  const int dk = a.pass[first].DK, dv = a.pass[first].DV;
-  if (dk > 128) return launch_tiles<IOT, 256, 1>(a, first, count, s);
-  if (dk > 64) return dv > 64 ? launch_tiles<IOT, 128, 2>(a, first, count, s) : launch_tiles<IOT, 128, 1>(a, first, count, s);
-  return dv > 64 ? launch_tiles<IOT, 64, 2>(a, first, count, s) : launch_tiles<IOT, 64, 1>(a, first, count, s);
+  bool even = true;
+  for (int i = first; i < first + count; ++i) {
+    const LinPass& p = a.pass[i];
+    even = even && p.DK % 8 == 0 && p.DV % 8 == 0;
+    // 64 rows of them, in bytes, and a head's values fit 32 bits
+    for (const HeadView* v : {&p.q, &p.k, &p.v}) even = even && v->token <= (1 << 23);
+  }
+  return even ? launch_sizes<IOT, true>(a, first, count, s) : launch_sizes<IOT, false>(a, first, count, s);
 }
 
 template <int IOT>
@@ -536,7 +579,9 @@ hipError_t launch(const LinArgs& a, hipStream_t s) {
   if (a.passes == 1) return launch_pass<IOT>(a, 0, 1, s);
   // gv's states behind the segments are gk's too
   if (const hipError_t e = launch_pass<IOT>(a, 2, 1, s)) return e;
-  return launch_pass<IOT>(a, 0, 2, s);
+  if (a.pass[0].out_f32 == a.pass[1].out_f32) return launch_pass<IOT>(a, 0, 2, s);
+  if (const hipError_t e = launch_pass<IOT>(a, 0, 1, s)) return e;
+  return launch_pass<IOT>(a, 1, 1, s);
 }
 
 // ------------------------------------------------------------ single tokens

@@ -52,14 +52,15 @@ struct LinArgs {
 
 // How a pass fills the chip: the time axis in segments, so that B H segments
 // (of 64 or 128 columns of the state each) are some `kLinFill` workgroups.
-constexpr int kLinFill = 768;
+constexpr int kLinFill = 512;
 constexpr int64_t kLinSegment = 256;   // the fewest tokens of a segment; a multiple of the kernels' blocks
 struct LinPlan {
   int segs;
   int64_t seg;
 };
 inline LinPlan lin_plan(int64_t B, int64_t L, int64_t H, int64_t DK, int64_t DV) {
-  const int64_t cols = DK > 128 || DV <= 64 ? 64 : 128, groups = B * H * ((DV + cols - 1) / cols);
+  (void)DK;
+  const int64_t cols = DV <= 64 ? 64 : 128, groups = B * H * ((DV + cols - 1) / cols);
   int64_t segs = kLinFill / groups, most = (L + kLinSegment - 1) / kLinSegment;
   if (segs > most) segs = most;
   if (segs < 1) segs = 1;
