@@ -35,7 +35,7 @@ __device__ __forceinline__ float power_of(float g, int n) {
 // -------------------------------------------------- passes over sequences
 //
 // A workgroup of 4 or 8 waves walks over a sequence (or a segment of it) in blocks
-// of C tokens and keeps 16 columns of a head's state for each wave in the
+// of C tokens and keeps 16 NC columns of a head's state for each wave in the
 // accumulators of its matrix instructions.  For a block with the state S
 // in front of it, weights W = tril(lambda^(i-j)) and the rows k, q, v in LDS:
 //   P   = so su W * (q k^T)                     shared out by tiles of 16 x 16,
@@ -44,9 +44,11 @@ __device__ __forceinline__ float power_of(float g, int n) {
 // All products are formed transposed, with the state's and P's accumulators
 // as operands of the next product as they lie: lane l of group g = l / 16
 // holds rows 4 g .. 4 g + 3 of a tile's column l % 16, and two tiles make the
-// 8 values of k that an operand holds for its row or column, in the order
-// 4 g .. 4 g + 3, 16 + 4 g .. 16 + 4 g + 3, in which the other operand is read.
-// So the state never goes through LDS, and P does once, lane by lane.
+// 8 values that an operand holds for its row or column.  Tokens are taken in
+// that order, 4 g .. 4 g + 3, 16 + 4 g .. 16 + 4 g + 3 of 32, and the state's
+// rows are dealt to two tiles so that the 8 are 8 g .. 8 g + 7 of 32: what q
+// and k hold in 16 bytes.  So the state never goes through LDS, and P does
+// once, lane by lane.
 
 typedef __bf16 bf16x8v __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -70,26 +72,38 @@ __device__ __forceinline__ f32x4v mma(const Frag<0>& x, const Frag<0>& y, f32x4v
   return c;
 }
 
+// The product of the operands' first halves alone.
+__device__ __forceinline__ f32x4v mma_half(const Frag<1>& x, u32x2v y, f32x4v c) {
+  return mma(Frag<1>{x.a, u32x2v{0u, 0u}}, Frag<1>{y, u32x2v{0u, 0u}}, c);
+}
+__device__ __forceinline__ f32x4v mma_half(const Frag<0>& x, f32x4v y, f32x4v c) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(x.a[e], y[e], c, 0, 0, 0);
+  return c;
+}
+
 // Rows of D values in LDS.  Word w of 16 bytes of row r lies in slot w ^ twist(r),
-// so that reads keep to different banks: by rows, 16 rows of a word or half a
-// word (8 bytes of bf16 for each group of lanes), and transposed, 8 rows of 4
-// halves (bf16) or 4 rows, 4 apart, of 4 words (fp32).  twist takes the row's
-// last four bits and D is a power of two, so value d of row r0 + r, r0 a
-// multiple of 16 and r < 16, is at r0 D + (base(r) ^ d).
+// which keeps 16 rows of a word apart, 8 rows of 4 neighbouring halves (v,
+// transposed) and, in fp32, 4 rows, 4 apart, of 4 words that are neighbours or
+// 2 apart; 8 rows of 4 halves, 16 bytes apart (k, transposed), meet in pairs.
+// twist takes the row's last four bits and D is a power of two, so value d of
+// row r0 + r, r0 a multiple of 16 and r < 16, is at (r0 D + base(r)) ^ d.
 template <int IOT, int D> struct Lds;
 template <int D> struct Lds<0, D> {
   typedef float T;
   typedef f32x4v Four;
-  static __device__ __forceinline__ int base(int r) { return (r * D) ^ (r << 2); }
-  // four values of row r0 + r from d, a multiple of 4
-  static __device__ __forceinline__ Four row(const T* p, int r0, int base_r, int d) {
-    return *reinterpret_cast<const Four*>(p + r0 * D + (base_r ^ d));
+  static __device__ __forceinline__ int base(int r) {
+    return (r * D) ^ (((r & 3) << 1 | (r >> 2 & 1) | (r >> 3 & 1) << 3) << 2);
   }
-  // values of rows r .. r + 3 behind r0 (r a multiple of 4) at columns d .. d + 15 (a multiple of 16): with
-  // base_c = column_base(r, l), lane l of its 16 gets column l's
-  static __device__ __forceinline__ int column_base(int r, int l) { return base(r) ^ l; }
-  static __device__ __forceinline__ Four column(const T* p, int r0, int base_c, int d) {
-    p += r0 * D;
+  // eight values of a row from d, a multiple of 8
+  static __device__ __forceinline__ Frag<0> row(const T* p, int base_r, int d) {
+    return {*reinterpret_cast<const Four*>(p + (base_r ^ d)), *reinterpret_cast<const Four*>(p + (base_r ^ d ^ 4))};
+  }
+  // values of rows r .. r + 3 (a multiple of 4) at a column for each lane, which base_c = base(r) ^ column holds
+  static __device__ __forceinline__ int next(int l) { return l; }             // 16 neighbouring columns
+  static __device__ __forceinline__ int dealt(int l) { return 8 * (l >> 2) + (l & 3); }   // rows of a tile of the state
+  static __device__ __forceinline__ int column_base(int r, int l, int column) { return base(r) ^ column; }
+  static __device__ __forceinline__ Four column(const T* p, int base_c, int d) {
     return Four{p[base_c ^ d], p[base_c ^ d ^ base(1)], p[base_c ^ d ^ base(2)], p[base_c ^ d ^ base(3)]};
   }
 };
@@ -100,15 +114,36 @@ template <int D> struct Lds<1, D> {
     const int twist = D >= 128 ? ((r & 7) << 1) | ((r >> 3) & 1) : (r & 6) | ((r >> 3) & 1);
     return (r * D) ^ (twist << 3);
   }
-  static __device__ __forceinline__ Four row(const T* p, int r0, int base_r, int d) {
-    return *reinterpret_cast<const Four*>(p + r0 * D + (base_r ^ d));
+  static __device__ __forceinline__ Frag<1> row(const T* p, int base_r, int d) {
+    const u32x4v v = *reinterpret_cast<const u32x4v*>(p + (base_r ^ d));
+    return {u32x2v{v[0], v[1]}, u32x2v{v[2], v[3]}};
   }
-  // the transposing read: lane l gives the address of row l / 4, columns 4 (l % 4), and gets column l
-  static __device__ __forceinline__ int column_base(int r, int l) { return base(r + (l >> 2)) ^ (4 * (l & 3)); }
-  static __device__ __forceinline__ Four column(const T* p, int r0, int base_c, int d) {
-    return __builtin_bit_cast(Four, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(p + r0 * D + (base_c ^ d))));
+  // the transposing read: lane l gives the address of row l / 4 and of columns that lanes 4 (l % 4) .. get
+  static __device__ __forceinline__ int next(int l) { return 4 * (l & 3); }
+  static __device__ __forceinline__ int dealt(int l) { return 8 * (l & 3); }
+  static __device__ __forceinline__ int column_base(int r, int l, int column) { return base(r + (l >> 2)) ^ column; }
+  static __device__ __forceinline__ Four column(const T* p, int base_c, int d) {
+    return __builtin_bit_cast(Four, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(p + (base_c ^ d))));
   }
 };
+
+// Eight values behind an address that all lanes share, which is held in scalar
+// registers, at a lane's own offset in bytes.
+template <int IOT>
+__device__ __forceinline__ Raw8<IOT> ld8_from(const char* p, uint32_t off) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  typedef const __attribute__((address_space(1))) char* global;
+  const global q = reinterpret_cast<global>((uint64_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32 |
+                                            (uint32_t)__builtin_amdgcn_readfirstlane((int)v)) + off;
+  Raw8<IOT> r;
+  if constexpr (IOT == 0) {
+    r.a = *reinterpret_cast<const __attribute__((address_space(1))) f32x4_e4*>(q);
+    r.b = *reinterpret_cast<const __attribute__((address_space(1))) f32x4_e4*>(q + 16);
+  } else {
+    r.a = *reinterpret_cast<const __attribute__((address_space(1))) u32x4_e2*>(q);
+  }
+  return r;
+}
 
 // The same value, which the compiler cannot tell: what is computed from it is
 // computed where it is used, instead of once and kept in registers.
@@ -180,19 +215,19 @@ struct Rows {
       const char* at = base + (back ? last - t0 - (now - 1) : t0) * token * E;   // its first value in memory
       const uint32_t inside = live ? col * E : 0, step = (uint32_t)token * E;
       if (now == C) {
-        const uint32_t off = (uint32_t)(back ? C - 1 - row : row) * step + inside;
+        const uint32_t off = here((back ? C - 1 - row : row) * step + inside);
         if (!back) {
 #pragma unroll
-          for (int m = 0; m < NW; ++m) word[m] = ld8<IOT>(at + m * STEP * (int64_t)step + off, 0);
+          for (int m = 0; m < NW; ++m) word[m] = ld8_from<IOT>(at + m * STEP * (int64_t)step, off);
         } else {
 #pragma unroll
-          for (int m = 0; m < NW; ++m) word[m] = ld8<IOT>(at - m * STEP * (int64_t)step + off, 0);
+          for (int m = 0; m < NW; ++m) word[m] = ld8_from<IOT>(at - m * STEP * (int64_t)step, off);
         }
       } else {
 #pragma unroll
         for (int m = 0; m < NW; ++m) {
           const int r = min(row + m * STEP, now - 1);
-          word[m] = ld8<IOT>(at + (uint32_t)(back ? now - 1 - r : r) * step + inside, 0);
+          word[m] = ld8_from<IOT>(at, (uint32_t)(back ? now - 1 - r : r) * step + inside);
         }
       }
     } else {
@@ -249,20 +284,21 @@ __device__ __forceinline__ void st4n(void* p, int64_t i, f32x4v v, int n) {
 }
 
 #ifndef HYENA_LIN_EU
-#define HYENA_LIN_EU (DK >= 256 || (DK >= 128 && WAVES == 4) ? 2 : 4)
+#define HYENA_LIN_EU (DK >= 128 || NC == 2 ? 2 : 3)
 #endif
 template <int IOT> constexpr int kBlock = IOT == 1 ? 64 : 32;   // tokens of a block
 
-template <int IOT, int DK, int WAVES, bool FILL>
+template <int IOT, int DK, int WAVES, int NC, bool FILL>
 constexpr int lin_lds_bytes() {
   constexpr int C = kBlock<IOT>, E = IOT == 0 ? 4 : 2;
-  return (C * ((FILL ? 1 : 2) * DK + 16 * WAVES) + (FILL ? 0 : C * C)) * E + (3 * C + 16) * 4;
+  return (C * ((FILL ? 1 : 2) * DK + 16 * NC * WAVES) + (FILL ? 0 : C * C)) * E + (3 * C + 16) * 4;
 }
 
 // FILL: the state behind a segment alone, from nothing, for all but the last segment.
-template <int IOT, int DK, int WAVES, bool FILL, bool EVEN, bool OUT32>
+template <int IOT, int DK, int WAVES, int NC, bool FILL, bool EVEN, bool OUT32>
 __global__ __launch_bounds__(64 * WAVES, HYENA_LIN_EU) void k_lin(LinArgs a, int first_pass) {
-  constexpr int C = kBlock<IOT>, IT = C / 16, JJ = C / 32, KT = DK / 16, DVT = 16 * WAVES, NP = kParts<IOT>;
+  constexpr int C = kBlock<IOT>, IT = C / 16, JJ = C / 32, KT = DK / 16, DVT = 16 * NC * WAVES, NP = kParts<IOT>;
+  constexpr int HELD = 4;                              // tiles of k's rows at a time
   typedef Lds<IOT, DK> MK;
   typedef Lds<IOT, DVT> MV;
   typedef typename MK::T T;
@@ -287,9 +323,9 @@ __global__ __launch_bounds__(64 * WAVES, HYENA_LIN_EU) void k_lin(LinArgs a, int
   const float gd = a.log_decay ? a.log_decay[h] : 0.f;
   if (FILL && t0 >= n) return;
 
-  // the state: rows 16 k + 4 g + r, column 16 wave + l of the tile
-  const int dv = c0 + 16 * wave + l;
-  f32x4v S[KT];
+  // the state: rows 32 (k / 2) + 8 g + 4 (k % 2) + r, column 16 (NC wave + c) + l of the tile
+  const int mine = 16 * NC * wave, dv = c0 + mine + l;
+  f32x4v S[KT][NC];
   {
     const float* s0 = nullptr;
     int sk = 0, sv = 0;
@@ -300,10 +336,12 @@ __global__ __launch_bounds__(64 * WAVES, HYENA_LIN_EU) void k_lin(LinArgs a, int
 #pragma unroll
     for (int k = 0; k < KT; ++k)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int dk = 16 * k + 4 * g + r;
-        S[k][r] = s0 && t0 < max(n, (int64_t)1) && dk < p.DK && dv < p.DV ? s0[(int64_t)dk * sk + (int64_t)dv * sv] : 0.f;
-      }
+      for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int dk = 32 * (k / 2) + 8 * g + 4 * (k & 1) + r, d = dv + 16 * c;
+          S[k][c][r] = s0 && t0 < max(n, (int64_t)1) && dk < p.DK && d < p.DV ? s0[(int64_t)dk * sk + (int64_t)d * sv] : 0.f;
+        }
   }
 
   if (t0 < end) {
@@ -319,11 +357,12 @@ __global__ __launch_bounds__(64 * WAVES, HYENA_LIN_EU) void k_lin(LinArgs a, int
       rq.load(t0, first);
     }
     Decay whole{0.f, 1.f};
-    // P's tiles of this wave: number wave, wave + WAVES, .. of those on and below the diagonal
+    const bool busy = c0 + mine < p.DV;                 // this wave has columns; all waves load, and form P
+    // P's tiles on and below the diagonal, MINE at most for a wave
     constexpr int TILES = IT * (IT + 1) / 2, MINE = (TILES + WAVES - 1) / WAVES;
     if (!FILL && threadIdx.x < C + 16) apart[threadIdx.x] = threadIdx.x < C ? p.so * p.su * power_of(gd, C - 1 - threadIdx.x) : 0.f;
-    // this lane's outputs: token l of a tile, values d0 .. d0 + 3
-    const int d0 = c0 + 16 * wave + 4 * g;
+    // this lane's outputs: token l of a tile, values d0 + 16 c .. + 3
+    const int d0 = c0 + mine + 4 * g;
     const int64_t out_step = (p.reverse ? -1 : 1) * (int64_t)a.H * p.DV * (OUT32 ? 4 : 2);
     char* out = nullptr;
     if (!FILL)
@@ -354,15 +393,14 @@ __global__ __launch_bounds__(64 * WAVES, HYENA_LIN_EU) void k_lin(LinArgs a, int
       if constexpr (!FILL) {
 #pragma unroll
         for (int m = 0; m < MINE; ++m) {
-          const int k = wave + WAVES * m;
+          // turned by the workgroup, so that the idle waves of a compute unit's workgroups are not all on one SIMD
+          const int k = ((wave + (int)blockIdx.x) & (WAVES - 1)) + WAVES * m;
           if (k >= TILES) break;
           const int i = k < 1 ? 0 : k < 3 ? 1 : k < 6 ? 2 : 3, j = k - i * (i + 1) / 2;
           f32x4v acc = {0.f, 0.f, 0.f, 0.f};
-          const int at = here(MK::base(l) ^ (4 * g));
+          const int at = MK::base(l) ^ (8 * g), of_k = here(at + 16 * j * DK), of_q = here(at + 16 * i * DK);
 #pragma unroll
-          for (int d = 0; d < DK; d += 32)
-            acc = mma(Frag<IOT>{MK::row(lk, 16 * j, at, d), MK::row(lk, 16 * j, at, d + 16)},
-                      Frag<IOT>{MK::row(lq, 16 * i, at, d), MK::row(lq, 16 * i, at, d + 16)}, acc);
+          for (int d = 0; d < DK; d += 32) acc = mma(MK::row(lk, of_k, d), MK::row(lq, of_q, d), acc);
 #pragma unroll
           for (int r = 0; r < 4; ++r) acc[r] *= apart[C - 1 - 16 * (i - j) - l + 4 * g + r];
           if (i == j) {
@@ -374,95 +412,143 @@ __global__ __launch_bounds__(64 * WAVES, HYENA_LIN_EU) void k_lin(LinArgs a, int
         }
         __syncthreads();
       }
+      if (!busy) continue;
       // v transposed: this wave's columns, 8 tokens to a lane
-      Frag<IOT> vt[JJ];
-#pragma unroll
-      for (int j = 0; j < JJ; ++j) {
-        const int at = here(MV::column_base(4 * g, l));
-        vt[j] = {MV::column(lv, 32 * j, at, 16 * wave), MV::column(lv, 32 * j + 16, at, 16 * wave)};
-      }
+      const auto values = [&](int j, int c) {
+        const int at = here(MV::column_base(4 * g, l, MV::next(l) + mine));
+        return Frag<IOT>{MV::column(lv + 32 * j * DVT, at, 16 * c), MV::column(lv + (32 * j + 16) * DVT, at, 16 * c)};
+      };
       if constexpr (!FILL) {
         // bf16: the state is rounded once for its product with q, and stays fp32
-        Frag<IOT> sf[KT / 2];
+        Frag<IOT> sf[KT / 2][NC];
 #pragma unroll
-        for (int k = 0; k < KT / 2; ++k) sf[k] = {as_operand<IOT>(S[2 * k]), as_operand<IOT>(S[2 * k + 1])};
+        for (int k = 0; k < KT / 2; ++k)
+#pragma unroll
+          for (int c = 0; c < NC; ++c) sf[k][c] = {as_operand<IOT>(S[2 * k][c]), as_operand<IOT>(S[2 * k + 1][c])};
+        const T* const pt = lp + lane * 4;
+        const auto weights = [&](int i, int j) { return *reinterpret_cast<const Four*>(pt + (i * IT + j) * 256); };
+        const auto put = [&](int i, int c, f32x4v o) {
+          if (16 * i + l < count) {
+            if (OUT32) st4n<0>(out + 16 * i * out_step, 16 * c, o, p.DV - d0 - 16 * c);
+            else st4n<1>(out + 16 * i * out_step, 16 * c, o, p.DV - d0 - 16 * c);
+          }
+        };
+        f32x4v acc[IT][NC];
+#pragma unroll
+        for (int i = 0; i < IT; ++i)
+#pragma unroll
+          for (int c = 0; c < NC; ++c) acc[i][c] = f32x4v{0.f, 0.f, 0.f, 0.f};
+        const int at = here(MK::base(l) ^ (8 * g));
+#pragma unroll
+        for (int k = 0; k < KT / 2; ++k)
+#pragma unroll
+          for (int i = 0; i < IT; ++i) {
+            const Frag<IOT> q = MK::row(lq + 16 * i * DK, at, 32 * k);
+#pragma unroll
+            for (int c = 0; c < NC; ++c) acc[i][c] = mma(sf[k][c], q, acc[i][c]);
+          }
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+          const float w = through[16 * i + l];
+#pragma unroll
+          for (int c = 0; c < NC; ++c) acc[i][c] *= w;
+        }
+#pragma unroll
+        for (int j = 0; j < JJ; ++j) {
+          Frag<IOT> vt[NC];
+#pragma unroll
+          for (int c = 0; c < NC; ++c) vt[c] = values(j, c);
+#pragma unroll
+          for (int i = 2 * j; i < IT; ++i) {
+            Frag<IOT> w;
+            w.a = weights(i, 2 * j);
+            if (i > 2 * j) w.b = weights(i, 2 * j + 1);
+#pragma unroll
+            for (int c = 0; c < NC; ++c) acc[i][c] = i == 2 * j ? mma_half(vt[c], w.a, acc[i][c]) : mma(vt[c], w, acc[i][c]);
+          }
+        }
+        float bad = 0.f;
+#pragma unroll
+        for (int i = 0; i < IT; ++i)
+#pragma unroll
+          for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) bad = fmaf(acc[i][c][r], 0.f, bad);
+        if (!__any(bad != 0.f)) {
+#pragma unroll
+          for (int i = 0; i < IT; ++i)
+#pragma unroll
+            for (int c = 0; c < NC; ++c) put(i, c, acc[i][c]);
+        } else {
+          // A value that is not finite has met the zeros of P above the diagonal: the tiles again, with the
+          // diagonal's products one by one, so that it reaches no earlier token.
 #pragma unroll 1
-        for (int i = 0; i < IT && 16 * i < count; ++i) {
-          f32x4v acc;
-          // A value that is not finite meets the zeros of P above the diagonal; where an output shows one, the
-          // tile is formed again with the diagonal's products one by one (`careful`), so that it reaches no earlier token.
-          for (bool careful = false;; careful = true) {
-            acc = f32x4v{0.f, 0.f, 0.f, 0.f};
-            const int at = here(MK::base(l) ^ (4 * g));
+          for (int i = 0; i < IT; ++i) {
 #pragma unroll
-            for (int k = 0; k < KT / 2; ++k)
-              acc = mma(sf[k], Frag<IOT>{MK::row(lq, 16 * i, at, 32 * k), MK::row(lq, 16 * i, at, 32 * k + 16)}, acc);
-            acc *= through[16 * i + l];
-            const T* pt = lp + (i * IT * 64 + lane) * 4;
-            const Frag<IOT> zero{};
+            for (int c = 0; c < NC; ++c) {
+              f32x4v o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int j = 0; j < JJ; ++j) {
-              if (2 * j > i) break;
-              Frag<IOT> pf{*reinterpret_cast<const Four*>(pt + 2 * j * 256), zero.b};
-              if (2 * j + 1 <= i) pf.b = *reinterpret_cast<const Four*>(pt + (2 * j + 1) * 256);
-              if (careful) {
-                if (2 * j == i) continue;
-                if (2 * j + 1 == i) pf.b = zero.b;
+              for (int k = 0; k < KT / 2; ++k) o = mma(sf[k][c], MK::row(lq + 16 * i * DK, at, 32 * k), o);
+              o *= through[16 * i + l];
+#pragma unroll
+              for (int j = 0; j < JJ; ++j) {
+                if (2 * j + 1 == i) o = mma_half(values(j, c), weights(i, 2 * j), o);
+                else if (2 * j + 1 < i) o = mma(values(j, c), Frag<IOT>{weights(i, 2 * j), weights(i, 2 * j + 1)}, o);
               }
-              acc = mma(careful && 2 * j + 1 == i ? Frag<IOT>{vt[j].a, zero.b} : vt[j], pf, acc);
-            }
-            if (careful) {
 #pragma unroll 1
               for (int j = 0; j < 16; ++j) {
                 const float w = one(lp[((i * IT + i) * 64 + (j >> 2) * 16 + l) * 4 + (j & 3)]);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                  const float v = one(lv[16 * i * DVT + (MV::base(j) ^ (16 * wave + 4 * g + r))]);
-                  acc[r] = j <= l ? fmaf(w, v, acc[r]) : acc[r];
+                  const float v = one(lv[16 * i * DVT + (MV::base(j) ^ (mine + 16 * c + 4 * g + r))]);
+                  o[r] = j <= l ? fmaf(w, v, o[r]) : o[r];
                 }
               }
-              break;
+              put(i, c, o);
             }
-            float bad = 0.f;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) bad = fmaf(acc[r], 0.f, bad);
-            if (!__any(bad != 0.f)) break;
           }
-          if (16 * i + l < count) {
-            if (OUT32) st4n<0>(out, 0, acc, p.DV - d0);
-            else st4n<1>(out, 0, acc, p.DV - d0);
-          }
-          out += 16 * out_step;
         }
+        out += C * out_step;
       }
-      const int at = here(MK::column_base(4 * g, l));
       if (whole.keep != 0.f) {
 #pragma unroll
         for (int k = 0; k < KT; ++k)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) S[k][r] = fmaf(S[k][r], whole.f, S[k][r]);
+          for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) S[k][c][r] = fmaf(S[k][c][r], whole.f, S[k][c][r]);
       } else {
 #pragma unroll
-        for (int k = 0; k < KT; ++k) S[k] *= whole.f;
+        for (int k = 0; k < KT; ++k)
+#pragma unroll
+          for (int c = 0; c < NC; ++c) S[k][c] *= whole.f;
       }
+      const int at = here(MK::column_base(4 * g, l, MK::dealt(l)));
 #pragma unroll
       for (int j = 0; j < JJ; ++j) {
-        Frag<IOT> vw[NP];
+        Frag<IOT> vw[NC][NP];
         const float* at_j = weight + 32 * j + 4 * g;
-        const f32x4v x = widen4(vt[j].a) * *reinterpret_cast<const f32x4v*>(at_j);
-        const f32x4v y = widen4(vt[j].b) * *reinterpret_cast<const f32x4v*>(at_j + 16);
-        parts_of(x, y, vw);
 #pragma unroll
-        for (int k0 = 0; k0 < KT; k0 += 4) {
-          Frag<IOT> kt[4];
+        for (int c = 0; c < NC; ++c) {
+          const Frag<IOT> vt = values(j, c);
+          const f32x4v x = widen4(vt.a) * *reinterpret_cast<const f32x4v*>(at_j);
+          const f32x4v y = widen4(vt.b) * *reinterpret_cast<const f32x4v*>(at_j + 16);
+          parts_of(x, y, vw[c]);
+        }
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            kt[k] = {MK::column(lk, 32 * j, at, 16 * (k0 + k)), MK::column(lk, 32 * j + 16, at, 16 * (k0 + k))};
+        for (int k0 = 0; k0 < KT; k0 += HELD) {
+          Frag<IOT> kt[HELD];
+#pragma unroll
+          for (int k = 0; k < HELD; ++k) {
+            const int d = 32 * ((k0 + k) / 2) + 4 * (k & 1);
+            kt[k] = {MK::column(lk + 32 * j * DK, at, d), MK::column(lk + (32 * j + 16) * DK, at, d)};
           }
 #pragma unroll
           for (int q = NP - 1; q >= 0; --q)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) S[k0 + k] = mma(kt[k], vw[q], S[k0 + k]);
+            for (int k = 0; k < HELD; ++k)
+#pragma unroll
+              for (int c = 0; c < NC; ++c) S[k0 + k][c] = mma(kt[k], vw[c][q], S[k0 + k][c]);
           __builtin_amdgcn_sched_barrier(0);          // no more operands in flight than registers for them
         }
       }
@@ -475,15 +561,19 @@ __global__ __launch_bounds__(64 * WAVES, HYENA_LIN_EU) void k_lin(LinArgs a, int
   else if (p.s_out && (n == 0 ? sg == 0 : t0 < n && n <= t0 + a.seg)) to = p.s_out + bh * size;
   if (to) {
     const int sk = FILL ? p.seg_k : p.DV, sv = FILL ? p.seg_v : 1;
+    const int dk0 = here(8 * g);
     const bool as_is = FILL || !p.reverse || n == 0;
     const Decay last = decay_of(gd, 1);
 #pragma unroll
     for (int k = 0; k < KT; ++k)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int dk = 16 * k + 4 * g + r;
-        if (dk < p.DK && dv < p.DV) to[(int64_t)dk * sk + (int64_t)dv * sv] = as_is ? S[k][r] : decayed(S[k][r], last, 0.f);
-      }
+      for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int dk = 32 * (k / 2) + dk0 + 4 * (k & 1) + r, d = dv + 16 * c;
+          if (dk < p.DK && d < p.DV)
+            to[(int64_t)dk * sk + (int64_t)d * sv] = as_is ? S[k][c][r] : decayed(S[k][c][r], last, 0.f);
+        }
   }
   if (FILL) return;
   // zeros behind the sequence
@@ -510,7 +600,7 @@ __global__ __launch_bounds__(256) void k_lin_join(LinArgs a, int first_pass) {
   float s = p.s0 ? p.s0[(int64_t)bh * size + (int64_t)dk * p.s0_k + (int64_t)dv * p.s0_v] : 0.f;
   float* at = p.seg + (int64_t)bh * (a.segs - 1) * size + i;
   const Decay whole = decay_of(gd, a.seg);
-  constexpr int U = 8;                                // loads in flight
+  constexpr int U = 32;                                // loads in flight
   for (int s0 = 0; s0 < a.segs - 1; s0 += U) {
     float own[U];
 #pragma unroll
@@ -527,39 +617,38 @@ __global__ __launch_bounds__(256) void k_lin_join(LinArgs a, int first_pass) {
 }
 
 // One launch for passes [first, first + count), which share their sizes.
-template <int IOT, int DK, int WAVES, bool EVEN>
+template <int IOT, int DK, int WAVES, int NC, bool EVEN>
 hipError_t launch_tiles(const LinArgs& a, int first, int count, hipStream_t s) {
   const LinPass& p = a.pass[first];
-  const int64_t tiles = (p.DV + 16 * WAVES - 1) / (16 * WAVES), bh = (int64_t)a.B * a.H;
+  const int64_t tiles = (p.DV + 16 * NC * WAVES - 1) / (16 * NC * WAVES), bh = (int64_t)a.B * a.H;
   bool fills = false;
   for (int i = first; i < first + count; ++i) fills = fills || a.pass[i].seg_fills;
   hipError_t e;
   if (a.segs > 1 && fills) {
-    constexpr int bytes = lin_lds_bytes<IOT, DK, WAVES, true>();
+    constexpr int bytes = lin_lds_bytes<IOT, DK, WAVES, NC, true>();
     static_assert(bytes <= 160 * 1024, "");
-    k_lin<IOT, DK, WAVES, true, EVEN, false><<<dim3((unsigned)(bh * (a.segs - 1) * tiles), count), 64 * WAVES, bytes, s>>>(a, first);
+    k_lin<IOT, DK, WAVES, NC, true, EVEN, false><<<dim3((unsigned)(bh * (a.segs - 1) * tiles), count), 64 * WAVES, bytes, s>>>(a, first);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     const int64_t blocks = (p.DK * p.DV + 255) / 256;
     k_lin_join<<<dim3((unsigned)(bh * blocks), count), 256, 0, s>>>(a, first);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
-  constexpr int bytes = lin_lds_bytes<IOT, DK, WAVES, false>();
+  constexpr int bytes = lin_lds_bytes<IOT, DK, WAVES, NC, false>();
   static_assert(bytes <= 160 * 1024, "");
   const dim3 grid((unsigned)(bh * a.segs * tiles), count);
-  if (p.out_f32) k_lin<IOT, DK, WAVES, false, EVEN, true><<<grid, 64 * WAVES, bytes, s>>>(a, first);
-  else if constexpr (IOT == 1) k_lin<IOT, DK, WAVES, false, EVEN, false><<<grid, 64 * WAVES, bytes, s>>>(a, first);
+  if (p.out_f32) k_lin<IOT, DK, WAVES, NC, false, EVEN, true><<<grid, 64 * WAVES, bytes, s>>>(a, first);
+  else if constexpr (IOT == 1) k_lin<IOT, DK, WAVES, NC, false, EVEN, false><<<grid, 64 * WAVES, bytes, s>>>(a, first);
   return hipGetLastError();
 }
 
 template <int IOT, bool EVEN>
 hipError_t launch_sizes(const LinArgs& a, int first, int count, hipStream_t s) {
   const int dk = a.pass[first].DK, dv = a.pass[first].DV;
-  if (dv <= 64) {
-    if (dk > 128) return launch_tiles<IOT, 256, 4, EVEN>(a, first, count, s);
-    return dk > 64 ? launch_tiles<IOT, 128, 4, EVEN>(a, first, count, s) : launch_tiles<IOT, 64, 4, EVEN>(a, first, count, s);
-  }
-  if (dk > 128) return launch_tiles<IOT, 256, 8, EVEN>(a, first, count, s);
-  return dk > 64 ? launch_tiles<IOT, 128, 8, EVEN>(a, first, count, s) : launch_tiles<IOT, 64, 8, EVEN>(a, first, count, s);
+  if (dk > 128)
+    return dv <= 64 ? launch_tiles<IOT, 256, 4, 1, EVEN>(a, first, count, s) : launch_tiles<IOT, 256, 8, 1, EVEN>(a, first, count, s);
+  if (dk > 64)
+    return dv <= 64 ? launch_tiles<IOT, 128, 4, 1, EVEN>(a, first, count, s) : launch_tiles<IOT, 128, 4, 2, EVEN>(a, first, count, s);
+  return dv <= 64 ? launch_tiles<IOT, 64, 4, 1, EVEN>(a, first, count, s) : launch_tiles<IOT, 64, 4, 2, EVEN>(a, first, count, s);
 }
 
 template <int IOT>
