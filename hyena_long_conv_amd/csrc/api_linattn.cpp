@@ -116,9 +116,9 @@ hyena_status hyena_linear_attention(const hyena_linear_attention_params* p, void
   f.s0_k = f.seg_k = p->Dv;
   f.s0_v = f.seg_v = 1;
   f.seg = static_cast<float*>(workspace);
-  f.seg_fills = 1;
   f.s_out = state_out;
-  a.passes = 1;
+  a.passes = a.fills = 1;
+  a.fill[0] = f;
   a.log_decay = p->log_decay;
   a.lengths = p->lengths;
   a.B = (int)p->B;
@@ -201,9 +201,8 @@ hyena_status hyena_linear_attention_backward(const hyena_linear_attention_params
     r.s0_k = i == 2 ? p->Dv : 1;
     r.s0_v = i == 2 ? 1 : p->Dv;
     r.seg = reinterpret_cast<float*>(ws + (i == 0 ? w.before : w.behind));
-    r.seg_k = i == 1 ? 1 : r.DV;                        // gk's are gv's, transposed
-    r.seg_v = i == 1 ? p->Dv : 1;
-    r.seg_fills = i != 1;
+    r.seg_k = r.s0_k;
+    r.seg_v = r.s0_v;
     f.x[i] = shared ? static_cast<const float*>(r.out) : nullptr;
     f.out[i] = grads[i];
     f.heads[i] = (int)heads[i];
@@ -216,6 +215,14 @@ hyena_status hyena_linear_attention_backward(const hyena_linear_attention_params
   a.pass[2].q = k, a.pass[2].k = q, a.pass[2].v = d;    // gv[t] = G[t]^T k[t]
   a.pass[2].s_out = g->gstate;
   a.passes = 3;
+  a.fill[1] = a.pass[2];                                // G
+  a.fill[0] = a.pass[2];                                // S, from k and v
+  a.fill[0].k = k, a.fill[0].v = v;
+  a.fill[0].su = 1.f;
+  a.fill[0].reverse = 0;
+  a.fill[0].s0 = p->state;
+  a.fill[0].seg = a.pass[0].seg;
+  a.fills = 2;
   a.log_decay = p->log_decay;
   a.lengths = p->lengths;
   a.B = (int)p->B;

@@ -283,9 +283,6 @@ __device__ __forceinline__ void st4n(void* p, int64_t i, f32x4v v, int n) {
     if (e < n) st1<IOT>(p, i + e, v[e]);
 }
 
-#ifndef HYENA_LIN_EU
-#define HYENA_LIN_EU (DK >= 128 || NC == 2 ? 2 : 3)
-#endif
 template <int IOT> constexpr int kBlock = IOT == 1 ? 64 : 32;   // tokens of a block
 
 template <int IOT, int DK, int WAVES, int NC, bool FILL>
@@ -294,17 +291,16 @@ constexpr int lin_lds_bytes() {
   return (C * ((FILL ? 1 : 2) * DK + 16 * NC * WAVES) + (FILL ? 0 : C * C)) * E + (3 * C + 16) * 4;
 }
 
-// FILL: the state behind a segment alone, from nothing, for all but the last segment.
+// FILL: the state behind a segment alone, from nothing, for all but the last segment (LinArgs.fill).
 template <int IOT, int DK, int WAVES, int NC, bool FILL, bool EVEN, bool OUT32>
-__global__ __launch_bounds__(64 * WAVES, HYENA_LIN_EU) void k_lin(LinArgs a, int first_pass) {
+__global__ __launch_bounds__(64 * WAVES, DK >= 256 || NC == 2 || (DK >= 128 && WAVES == 4 && !FILL) ? 2 : 4) void k_lin(LinArgs a, int first_pass) {
   constexpr int C = kBlock<IOT>, IT = C / 16, JJ = C / 32, KT = DK / 16, DVT = 16 * NC * WAVES, NP = kParts<IOT>;
   constexpr int HELD = 4;                              // tiles of k's rows at a time
   typedef Lds<IOT, DK> MK;
   typedef Lds<IOT, DVT> MV;
   typedef typename MK::T T;
   typedef typename MK::Four Four;
-  const LinPass& p = a.pass[first_pass + blockIdx.y];
-  if (FILL && !p.seg_fills) return;
+  const LinPass& p = FILL ? a.fill[blockIdx.y] : a.pass[first_pass + blockIdx.y];
   extern __shared__ __attribute__((aligned(16))) unsigned char shared[];
   float* const weight = reinterpret_cast<float*>(shared);   // su lambda^(count-1-j) of a block's tokens,
   float* const through = weight + C;                         // and so lambda^(i+1)
@@ -317,7 +313,9 @@ __global__ __launch_bounds__(64 * WAVES, HYENA_LIN_EU) void k_lin(LinArgs a, int
 
   const int tiles = (p.DV + DVT - 1) / DVT, segs = FILL ? a.segs - 1 : a.segs;
   const int tile = (int)(blockIdx.x % (unsigned)tiles), rest = (int)(blockIdx.x / (unsigned)tiles);
-  const int bh = rest / segs, sg = rest - bh * segs, b = bh / a.H, h = bh - b * a.H, c0 = tile * DVT;
+  // the last segments first: what the fill read last is what the Infinity Cache still holds (65536 fp32 tokens of 12
+  // heads 64 x 64: 207 -> 199 us)
+  const int bh = rest / segs, nth = rest - bh * segs, sg = FILL ? nth : segs - 1 - nth, b = bh / a.H, h = bh - b * a.H, c0 = tile * DVT;
   const int64_t n = a.lengths ? min(max((int64_t)a.lengths[b], (int64_t)0), a.L) : a.L;
   const int64_t t0 = sg * a.seg, end = min(n, t0 + a.seg), size = (int64_t)p.DK * p.DV;
   const float gd = a.log_decay ? a.log_decay[h] : 0.f;
@@ -587,90 +585,124 @@ __global__ __launch_bounds__(64 * WAVES, HYENA_LIN_EU) void k_lin(LinArgs a, int
 }
 
 // The states behind the segments one after the other: a segment's own, which
-// stands in p.seg, and the state in front of it, decayed.
-__global__ __launch_bounds__(256) void k_lin_join(LinArgs a, int first_pass) {
-  const LinPass& p = a.pass[first_pass + blockIdx.y];
-  if (!p.seg_fills) return;
-  const int size = p.DK * p.DV, blocks = (size + 255) / 256;
-  const int bh = (int)(blockIdx.x / (unsigned)blocks), i = (int)(blockIdx.x - bh * blocks) * 256 + threadIdx.x;
+// stands in p.seg, and the state in front of it, decayed.  VEC neighbouring
+// values to a thread; the loads wait for no condition (a segment without
+// tokens left its slot as it was, and it stays so).
+template <int VEC>
+__global__ __launch_bounds__(256) void k_lin_join(LinArgs a) {
+  typedef float vec __attribute__((ext_vector_type(VEC)));
+  const LinPass& p = a.fill[blockIdx.y];
+  const int size = p.DK * p.DV, blocks = (size / VEC + 255) / 256, slots = a.segs - 1;
+  const int bh = (int)(blockIdx.x / (unsigned)blocks), i = ((int)(blockIdx.x - bh * blocks) * 256 + threadIdx.x) * VEC;
   if (i >= size) return;
   const int b = bh / a.H, h = bh - b * a.H, dk = i / p.seg_k, dv = i - dk * p.seg_k;   // seg_v is 1 where a pass fills
+  float* const at = p.seg + (int64_t)bh * slots * size + i;
+  constexpr int U = 8;                                // loads in flight
+  vec own[U];
+  const auto load = [&](int s0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) own[u] = *reinterpret_cast<const vec*>(at + (int64_t)min(s0 + u, slots - 1) * size);
+  };
+  load(0);
   const int64_t n = a.lengths ? min(max((int64_t)a.lengths[b], (int64_t)0), a.L) : a.L;
   const float gd = a.log_decay ? a.log_decay[h] : 0.f;
-  float s = p.s0 ? p.s0[(int64_t)bh * size + (int64_t)dk * p.s0_k + (int64_t)dv * p.s0_v] : 0.f;
-  float* at = p.seg + (int64_t)bh * (a.segs - 1) * size + i;
-  const Decay whole = decay_of(gd, a.seg);
-  constexpr int U = 32;                                // loads in flight
-  for (int s0 = 0; s0 < a.segs - 1; s0 += U) {
-    float own[U];
+  vec s = {};
+  if (p.s0) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) own[u] = s0 + u < a.segs - 1 && (s0 + u) * a.seg < n ? at[(int64_t)(s0 + u) * size] : 0.f;
+    for (int e = 0; e < VEC; ++e) s[e] = p.s0[(int64_t)bh * size + (int64_t)dk * p.s0_k + (int64_t)(dv + e) * p.s0_v];
+  }
+  // tokens of the segments in front, whole ones but for the last; from a sequence's last token on, the first finds its state undecayed
+  const int used = (int)min((n + a.seg - 1) / a.seg, (int64_t)slots);
+  const Decay whole = decay_of(gd, a.seg), first = decay_of(gd, min(n, a.seg) - (p.reverse ? 1 : 0));
+  const Decay part = decay_of(gd, n - (used - 1) * a.seg < a.seg ? n - (used - 1) * a.seg : a.seg);
+  for (int s0 = 0; s0 < used; s0 += U) {
+    vec now[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) now[u] = own[u];
+    if (s0 + U < used) load(s0 + U);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t have = n - (s0 + u) * a.seg;
-      if (s0 + u >= a.segs - 1 || have <= 0) continue;
-      const bool full = have >= a.seg && (s0 + u > 0 || !p.reverse);
-      s = decayed(s, full ? whole : decay_of(gd, min(have, a.seg) - (p.reverse && s0 + u == 0 ? 1 : 0)), own[u]);
-      at[(int64_t)(s0 + u) * size] = s;
+      const int k = s0 + u;
+      if (k < used) {
+        const Decay d = k == 0 ? first : k == used - 1 ? part : whole;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) s[e] = decayed(s[e], d, now[u][e]);
+        *reinterpret_cast<vec*>(at + (int64_t)k * size) = s;
+      }
     }
   }
 }
 
-// One launch for passes [first, first + count), which share their sizes.
-template <int IOT, int DK, int WAVES, int NC, bool EVEN>
+// Launches: `sizes` names the heads' sizes, passes [first, first + count) of
+// a.pass, or with FILL all of a.fill, share them.
+template <int IOT, int DK, int WAVES, int NC, bool FILL, bool EVEN>
 hipError_t launch_tiles(const LinArgs& a, int first, int count, hipStream_t s) {
-  const LinPass& p = a.pass[first];
+  const LinPass& p = FILL ? a.fill[0] : a.pass[first];
   const int64_t tiles = (p.DV + 16 * NC * WAVES - 1) / (16 * NC * WAVES), bh = (int64_t)a.B * a.H;
-  bool fills = false;
-  for (int i = first; i < first + count; ++i) fills = fills || a.pass[i].seg_fills;
-  hipError_t e;
-  if (a.segs > 1 && fills) {
-    constexpr int bytes = lin_lds_bytes<IOT, DK, WAVES, NC, true>();
-    static_assert(bytes <= 160 * 1024, "");
-    k_lin<IOT, DK, WAVES, NC, true, EVEN, false><<<dim3((unsigned)(bh * (a.segs - 1) * tiles), count), 64 * WAVES, bytes, s>>>(a, first);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-    const int64_t blocks = (p.DK * p.DV + 255) / 256;
-    k_lin_join<<<dim3((unsigned)(bh * blocks), count), 256, 0, s>>>(a, first);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-  }
-  constexpr int bytes = lin_lds_bytes<IOT, DK, WAVES, NC, false>();
+  constexpr int bytes = lin_lds_bytes<IOT, DK, WAVES, NC, FILL>();
   static_assert(bytes <= 160 * 1024, "");
-  const dim3 grid((unsigned)(bh * a.segs * tiles), count);
-  if (p.out_f32) k_lin<IOT, DK, WAVES, NC, false, EVEN, true><<<grid, 64 * WAVES, bytes, s>>>(a, first);
-  else if constexpr (IOT == 1) k_lin<IOT, DK, WAVES, NC, false, EVEN, false><<<grid, 64 * WAVES, bytes, s>>>(a, first);
+  const dim3 grid((unsigned)(bh * (FILL ? a.segs - 1 : a.segs) * tiles), count);
+  if constexpr (FILL) {
+    k_lin<IOT, DK, WAVES, NC, true, EVEN, false><<<grid, 64 * WAVES, bytes, s>>>(a, 0);
+    if (const hipError_t e = hipGetLastError()) return e;
+    const int vec = p.DV % 4 ? 1 : 4;
+    const dim3 joins((unsigned)(bh * ((p.DK * p.DV / vec + 255) / 256)), count);
+    if (vec == 4) k_lin_join<4><<<joins, 256, 0, s>>>(a);
+    else k_lin_join<1><<<joins, 256, 0, s>>>(a);
+  } else if (p.out_f32) {
+    k_lin<IOT, DK, WAVES, NC, false, EVEN, true><<<grid, 64 * WAVES, bytes, s>>>(a, first);
+  } else if constexpr (IOT == 1) {
+    k_lin<IOT, DK, WAVES, NC, false, EVEN, false><<<grid, 64 * WAVES, bytes, s>>>(a, first);
+  }
   return hipGetLastError();
 }
 
-template <int IOT, bool EVEN>
+// Columns of the state to a workgroup: 64 in 4 waves, or 128.  Those in 8
+// waves of 16, four of which a SIMD holds, or in 4 of 32, which read the rows
+// of q and k half as often but leave two to a SIMD.  bf16, 8 x 2048 tokens of 12 heads
+// 64 x 128: 43 us in 8 waves, 46 in 4 (the fill 23 and 25); 65536 tokens of 6 heads
+// 128 x 128: 107 in 4, 145 in 8, whose registers spill there (the fill, which
+// needs fewer: 60 in 8, 63 in 4).
+template <int IOT, bool FILL, bool EVEN>
 hipError_t launch_sizes(const LinArgs& a, int first, int count, hipStream_t s) {
-  const int dk = a.pass[first].DK, dv = a.pass[first].DV;
+  const LinPass& p = FILL ? a.fill[0] : a.pass[first];
+  const int dk = p.DK, dv = p.DV;
   if (dk > 128)
-    return dv <= 64 ? launch_tiles<IOT, 256, 4, 1, EVEN>(a, first, count, s) : launch_tiles<IOT, 256, 8, 1, EVEN>(a, first, count, s);
+    return dv <= 64 ? launch_tiles<IOT, 256, 4, 1, FILL, EVEN>(a, first, count, s)
+                    : launch_tiles<IOT, 256, 8, 1, FILL, EVEN>(a, first, count, s);
   if (dk > 64)
-    return dv <= 64 ? launch_tiles<IOT, 128, 4, 1, EVEN>(a, first, count, s) : launch_tiles<IOT, 128, 4, 2, EVEN>(a, first, count, s);
-  return dv <= 64 ? launch_tiles<IOT, 64, 4, 1, EVEN>(a, first, count, s) : launch_tiles<IOT, 64, 4, 2, EVEN>(a, first, count, s);
+    return dv <= 64 ? launch_tiles<IOT, 128, 4, 1, FILL, EVEN>(a, first, count, s)
+                    : launch_tiles<IOT, 128, FILL ? 8 : 4, FILL ? 1 : 2, FILL, EVEN>(a, first, count, s);
+  return dv <= 64 ? launch_tiles<IOT, 64, 4, 1, FILL, EVEN>(a, first, count, s)
+                  : launch_tiles<IOT, 64, 8, 1, FILL, EVEN>(a, first, count, s);
 }
 
-template <int IOT>
-hipError_t launch_pass(const LinArgs& a, int first, int count, hipStream_t s) {
+template <int IOT, bool FILL>
+hipError_t launch_passes(const LinArgs& a, int first, int count, hipStream_t s) {
   bool even = true;
   for (int i = first; i < first + count; ++i) {
-    const LinPass& p = a.pass[i];
+    const LinPass& p = FILL ? a.fill[i] : a.pass[i];
     even = even && p.DK % 8 == 0 && p.DV % 8 == 0;
     // 64 rows of them, in bytes, and a head's values fit 32 bits
     for (const HeadView* v : {&p.q, &p.k, &p.v}) even = even && v->token <= (1 << 23);
   }
-  return even ? launch_sizes<IOT, true>(a, first, count, s) : launch_sizes<IOT, false>(a, first, count, s);
+  return even ? launch_sizes<IOT, FILL, true>(a, first, count, s) : launch_sizes<IOT, FILL, false>(a, first, count, s);
 }
 
 template <int IOT>
 hipError_t launch(const LinArgs& a, hipStream_t s) {
-  if (a.passes == 1) return launch_pass<IOT>(a, 0, 1, s);
-  // gv's states behind the segments are gk's too
-  if (const hipError_t e = launch_pass<IOT>(a, 2, 1, s)) return e;
-  if (a.pass[0].out_f32 == a.pass[1].out_f32) return launch_pass<IOT>(a, 0, 2, s);
-  if (const hipError_t e = launch_pass<IOT>(a, 0, 1, s)) return e;
-  return launch_pass<IOT>(a, 1, 1, s);
+  if (a.segs > 1)
+    if (const hipError_t e = launch_passes<IOT, true>(a, 0, a.fills, s)) return e;
+  // neighbouring passes of the same sizes go together
+  for (int i = 0; i < a.passes;) {
+    int n = 1;
+    while (i + n < a.passes && a.pass[i + n].DK == a.pass[i].DK && a.pass[i + n].DV == a.pass[i].DV &&
+           a.pass[i + n].out_f32 == a.pass[i].out_f32)
+      ++n;
+    if (const hipError_t e = launch_passes<IOT, false>(a, i, n, s)) return e;
+    i += n;
+  }
+  return hipSuccess;
 }
 
 // ------------------------------------------------------------ single tokens

@@ -33,15 +33,16 @@ struct LinPass {
   int reverse;             // from the last token; the first one finds the state undecayed
   const float* s0;         // [B][H][..] state or nullptr: element (dk, dv) at dk s0_k + dv s0_v
   int s0_k, s0_v;
-  float* seg;              // split time axis: states behind all segments but the last, [B][H][segs - 1][..], element
-  int seg_k, seg_v;        // (dk, dv) at dk seg_k + dv seg_v; seg_fills: this pass forms them, another one otherwise
-  int seg_fills;
+  float* seg;              // split time axis: states behind all segments but the last, [B][H][segs - 1][..],
+  int seg_k, seg_v;        // element (dk, dv) at dk seg_k + dv seg_v
   float* s_out;            // state after the last token ([DK][DV]), times lambda if reverse; or nullptr
 };
 
 struct LinArgs {
   LinPass pass[3];
   int passes;
+  LinPass fill[2];         // what forms the states behind the segments: q, so and out unused, seg_v 1, all of the same sizes
+  int fills;
   const float* log_decay;  // [H] or nullptr
   const int32_t* lengths;  // [B] or nullptr
   int B, H, io;
@@ -50,18 +51,19 @@ struct LinArgs {
   int64_t seg;
 };
 
-// How a pass fills the chip: the time axis in segments, so that B H segments
-// (of 64 or 128 columns of the state each) are some `kLinFill` workgroups.
-constexpr int kLinFill = 512;
+// How a pass fills the chip: the time axis in segments, so that there are as
+// many workgroups (of 64 or 128 columns of the state) as the compute units
+// hold at once.
 constexpr int64_t kLinSegment = 256;   // the fewest tokens of a segment; a multiple of the kernels' blocks
 struct LinPlan {
   int segs;
   int64_t seg;
 };
+inline int64_t lin_columns(int64_t DV) { return DV <= 64 ? 64 : 128; }
+inline int64_t lin_resident(int64_t DK, int64_t DV) { return DK > 128 ? 256 : DK > 64 || DV > 64 ? 512 : 1024; }
 inline LinPlan lin_plan(int64_t B, int64_t L, int64_t H, int64_t DK, int64_t DV) {
-  (void)DK;
-  const int64_t cols = DV <= 64 ? 64 : 128, groups = B * H * ((DV + cols - 1) / cols);
-  int64_t segs = kLinFill / groups, most = (L + kLinSegment - 1) / kLinSegment;
+  const int64_t cols = lin_columns(DV), groups = B * H * ((DV + cols - 1) / cols);
+  int64_t segs = lin_resident(DK, DV) / groups, most = (L + kLinSegment - 1) / kLinSegment;
   if (segs > most) segs = most;
   if (segs < 1) segs = 1;
   int64_t seg = (L + segs - 1) / segs;
