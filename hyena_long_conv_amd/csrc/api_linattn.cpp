@@ -263,6 +263,7 @@ hyena_status hyena_rotary(const hyena_rotary_params* p, const void* x, void* out
   a.D = p->D;
   a.R = p->R;
   a.in_place = in_place;
+  a.io = io == HYENA_BF16;
   if (rotary_groups(a) > kMaxGroups) return HYENA_ERR_UNSUPPORTED;
   if (in_place) {                                      // heads apart from each other: every stride beyond what is inside it
     int64_t n[3] = {p->B, p->L, p->H}, span = p->D;
@@ -288,7 +289,6 @@ hyena_status hyena_rotary(const hyena_rotary_params* p, const void* x, void* out
   a.pos_batch = p->pos_stride[0];
   a.pos_token = p->pos_stride[1];
   a.interleaved = p->interleaved;
-  a.io = io == HYENA_BF16;
   a.scale = p->scale;
   a.sine = p->inverse ? -1.f : 1.f;
   return from_hip(rotary(a, (hipStream_t)stream));

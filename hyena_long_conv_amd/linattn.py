@@ -26,13 +26,17 @@ import hyena_long_conv_amd as _H
 from .ssm import _call, _like, _new, _rows, _take, _torch, _workspace
 
 i32, i64, vp, f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_float
-_Stride = i64 * 3
+
+
+def _stride3(name):
+    """The members of an int64_t[3], each a field of its own: plain numbers are quicker to hand over than an array."""
+    return [(f"{name}_{of}", i64) for of in ("sequence", "token", "head")]
 
 
 class LinearAttentionParams(ctypes.Structure):
     _fields_ = [("B", i64), ("L", i64), ("H", i32), ("Hq", i32), ("Hk", i32), ("Hv", i32), ("Dk", i32), ("Dv", i32),
-                ("scale", f32), ("reserved", i32), ("q", vp), ("k", vp), ("v", vp), ("q_stride", _Stride),
-                ("k_stride", _Stride), ("v_stride", _Stride), ("log_decay", vp), ("state", vp), ("lengths", vp)]
+                ("scale", f32), ("reserved", i32), ("q", vp), ("k", vp), ("v", vp), *_stride3("q_stride"),
+                *_stride3("k_stride"), *_stride3("v_stride"), ("log_decay", vp), ("state", vp), ("lengths", vp)]
 
 
 class LinearAttentionGrads(ctypes.Structure):
@@ -41,7 +45,8 @@ class LinearAttentionGrads(ctypes.Structure):
 
 class RotaryParams(ctypes.Structure):
     _fields_ = [("B", i64), ("L", i64), ("H", i32), ("D", i32), ("R", i32), ("interleaved", i32), ("inverse", i32),
-                ("scale", f32), ("x_stride", _Stride), ("freq", vp), ("positions", vp), ("pos_stride", i64 * 2)]
+                ("scale", f32), *_stride3("x_stride"), ("freq", vp), ("positions", vp), ("pos_sequence", i64),
+                ("pos_token", i64)]
 
 
 class GroupNormParams(ctypes.Structure):
@@ -88,35 +93,44 @@ def _heads(t, name, dims, like=None):
             raise ValueError(f"{name} shape {tuple(t.shape)} does not start with {tuple(like.shape[:dims - 2])}")
 
 
-def _stride(t):
-    """A view's strides between sequences, tokens and heads; 0 where there is but one."""
-    s, n = t.stride(), t.shape
+def _strides(s, n):
+    """Strides s of sizes n between sequences, tokens and heads; 0 where there is but one."""
     if len(n) == 4:
-        return _Stride(s[0] if n[0] > 1 else 0, s[1] if n[1] > 1 else 0, s[2] if n[2] > 1 else 0)
-    return _Stride(s[0] if n[0] > 1 else 0, 0, s[1] if n[1] > 1 else 0)
+        return (s[0] if n[0] > 1 else 0, s[1] if n[1] > 1 else 0, s[2] if n[2] > 1 else 0)
+    return (s[0] if n[0] > 1 else 0, 0, s[1] if n[1] > 1 else 0)
 
 
 # ---------------------------------------------------------- linear attention
 
 def _attention(q, k, v, log_decay, scale, state, lengths, dims):
     """(io, B, L, H, Dk, Dv, the parameters) of a call; heads as many as q, k or v has most of."""
-    torch = _torch()
-    _heads(q, "q", dims)
+    import torch
+    try:                                              # one expression for a single token's call, where this counts
+        t, dev, nq, nk, nv, sq, sk, sv = q.dtype, q.device, q.shape, k.shape, v.shape, q.stride(), k.stride(), v.stride()
+        fine = (len(nq) == len(nk) == len(nv) == dims and k.dtype is t and v.dtype is t and q.is_cuda and k.device == dev
+                and v.device == dev and sq[-1] == sk[-1] == sv[-1] == 1 and nq[0] == nk[0] == nv[0]
+                and (dims == 3 or nq[1] == nk[1] == nv[1]))
+    except AttributeError:
+        fine = False
+    if not fine:                                      # what is wrong, if anything is
+        _heads(q, "q", dims)
+        _heads(k, "k", dims, q)
+        _heads(v, "v", dims, q)
     io = _H._io_of(q)
-    _heads(k, "k", dims, q)
-    _heads(v, "v", dims, q)
-    B, L = q.shape[0], q.shape[1] if dims == 4 else 1
-    Hq, Hk, Hv, Dk, Dv = q.shape[-2], k.shape[-2], v.shape[-2], q.shape[-1], v.shape[-1]
-    if k.shape[-1] != Dk:
-        raise ValueError(f"q and k have heads of {Dk} and {k.shape[-1]} values")
+    B, L = nq[0], nq[1] if dims == 4 else 1
+    Hq, Hk, Hv, Dk, Dv = nq[-2], nk[-2], nv[-2], nq[-1], nv[-1]
+    if nk[-1] != Dk:
+        raise ValueError(f"q and k have heads of {Dk} and {nk[-1]} values")
     H = max(Hq, Hk, Hv)
     if not (Hq and Hk and Hv) or H % Hq or H % Hk or H % Hv:
         raise ValueError(f"{Hq}, {Hk} and {Hv} heads of q, k and v do not divide the most of them")
-    dev = q.device
+    if scale is None:
+        scale = Dk ** -0.5 if Dk else 0.0
     p = LinearAttentionParams(
-        B, L, H, Hq, Hk, Hv, Dk, Dv, Dk ** -0.5 if scale is None and Dk else scale or 0.0, 0, q.data_ptr(), k.data_ptr(),
-        v.data_ptr(), _stride(q), _stride(k), _stride(v), _take(log_decay, "log_decay", (H,), torch.float32, dev),
-        _take(state, "state", (B, H, Dk, Dv), torch.float32, dev), _take(lengths, "lengths", (B,), torch.int32, dev))
+        B, L, H, Hq, Hk, Hv, Dk, Dv, scale, 0, q.data_ptr(), k.data_ptr(), v.data_ptr(), *_strides(sq, nq), *_strides(sk, nk),
+        *_strides(sv, nv), None if log_decay is None else _take(log_decay, "log_decay", (H,), torch.float32, dev),
+        None if state is None else _take(state, "state", (B, H, Dk, Dv), torch.float32, dev),
+        None if lengths is None else _take(lengths, "lengths", (B,), torch.int32, dev))
     return io, B, L, H, Dk, Dv, p
 
 
@@ -151,7 +165,7 @@ def linear_attention_step(q, k, v, state, log_decay=None, scale=None, out=None):
     """One token for each sequence: q [B, Hq, Dk], k [B, Hk, Dk], v [B, Hv,
     Dv] -> o [B, H, Dv]; state [B, H, Dk, Dv] float32 moves on by one in
     place."""
-    torch = _torch()
+    import torch
     io, B, _, H, Dk, Dv, p = _attention(q, k, v, log_decay, scale, None, None, 3)
     dev, shape = q.device, (B, H, Dv)
     o = _new(shape, q.dtype, dev) if out is None else out
@@ -230,17 +244,17 @@ def rotary(x, freq, positions=None, scale: float = 1.0, interleaved: bool = Fals
     freq float64; positions int32 [B, L] or [L] (0, 1, .. by default), for a
     token [B].  inverse turns back: rotary(gy, .., inverse=True) is the
     gradient.  out: x itself (in place) or a contiguous tensor."""
-    torch = _torch()
+    import torch
     dims = 3 if isinstance(x, torch.Tensor) and x.dim() == 3 else 4
     _heads(x, "x", dims)
-    io, dev = _H._io_of(x), x.device
-    B, L, (H, D) = x.shape[0], x.shape[1] if dims == 4 else 1, x.shape[-2:]
+    io, dev, n = _H._io_of(x), x.device, x.shape
+    B, L, H, D = n[0], n[1] if dims == 4 else 1, n[-2], n[-1]
     if not isinstance(freq, torch.Tensor) or freq.dim() != 1:
         raise TypeError("freq must be a CUDA (ROCm) tensor of one dimension")
     R = 2 * freq.shape[0]
     if positions is None and dims == 3:
         raise ValueError("a token needs its positions")
-    pos_stride = (0, 0)
+    pos, pos_stride = None, (0, 0)
     if positions is not None:
         shape = (B,) if dims == 3 else (L,) if isinstance(positions, torch.Tensor) and positions.dim() == 1 else (B, L)
         pos = _take(positions, "positions", shape, torch.int32, dev)
@@ -252,9 +266,8 @@ def rotary(x, freq, positions=None, scale: float = 1.0, interleaved: bool = Fals
         op = out.data_ptr()
     else:
         op = _take(out, "out", x.shape, x.dtype, dev)
-    p = RotaryParams(B, L, H, D, R, int(bool(interleaved)), int(bool(inverse)), scale, _stride(x),
-                     _take(freq, "freq", freq.shape, torch.float64, dev), pos if positions is not None else None,
-                     (i64 * 2)(*pos_stride))
+    p = RotaryParams(B, L, H, D, R, int(bool(interleaved)), int(bool(inverse)), scale, *_strides(x.stride(), n),
+                     _take(freq, "freq", freq.shape, torch.float64, dev), pos, *pos_stride)
     _call("hyena_rotary", dev, ctypes.byref(p), x.data_ptr(), op, io)
     return out
 
