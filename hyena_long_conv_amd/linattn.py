@@ -266,6 +266,8 @@ def rotary(x, freq, positions=None, scale: float = 1.0, interleaved: bool = Fals
         op = out.data_ptr()
     else:
         op = _take(out, "out", x.shape, x.dtype, dev)
+        if op == x.data_ptr() and not x.is_contiguous():
+            raise ValueError("out is x's memory in another layout")
     p = RotaryParams(B, L, H, D, R, int(bool(interleaved)), int(bool(inverse)), scale, *_strides(x.stride(), n),
                      _take(freq, "freq", freq.shape, torch.float64, dev), pos, *pos_stride)
     _call("hyena_rotary", dev, ctypes.byref(p), x.data_ptr(), op, io)
