@@ -157,12 +157,29 @@ template <int IOT> __device__ __forceinline__ auto as_operand(f32x4v v) {
   if constexpr (IOT == 0) return v;
   else return narrow4(v);
 }
-__device__ __forceinline__ float one(float v) { return v; }
-__device__ __forceinline__ float one(uint16_t v) { return bf16_bits_to_f32(v); }
 __device__ __forceinline__ f32x4v widen4(f32x4v v) { return v; }
 __device__ __forceinline__ f32x4v widen4(u32x2v v) {
   return f32x4v{__uint_as_float(v[0] << 16), __uint_as_float(v[0] & 0xffff0000u), __uint_as_float(v[1] << 16),
                 __uint_as_float(v[1] & 0xffff0000u)};
+}
+
+// The first of four values that is not finite, or 4; and zeros in the place of all of them.
+__device__ __forceinline__ bool is_bad(float v) { return (__float_as_uint(v) & 0x7f800000u) == 0x7f800000u; }
+template <class Four>
+__device__ __forceinline__ int first_bad(const Four& f) {
+  const f32x4v v = widen4(f);
+  return is_bad(v[0]) ? 0 : is_bad(v[1]) ? 1 : is_bad(v[2]) ? 2 : is_bad(v[3]) ? 3 : 4;
+}
+__device__ __forceinline__ void clear_bad(f32x4v& f) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) f[e] = is_bad(f[e]) ? 0.f : f[e];
+}
+__device__ __forceinline__ void clear_bad(u32x2v& f) {
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    if ((f[e] & 0x7f80u) == 0x7f80u) f[e] &= 0xffff0000u;
+    if ((f[e] & 0x7f800000u) == 0x7f800000u) f[e] &= 0xffffu;
+  }
 }
 
 // The state's addends are products in fp32 of bf16 values and fp32 weights.
@@ -472,37 +489,45 @@ __global__ __launch_bounds__(64 * WAVES, DK >= 256 || NC == 2 || (DK >= 128 && W
           for (int c = 0; c < NC; ++c)
 #pragma unroll
             for (int r = 0; r < 4; ++r) bad = fmaf(acc[i][c][r], 0.f, bad);
-        if (!__any(bad != 0.f)) {
 #pragma unroll
-          for (int i = 0; i < IT; ++i)
+        for (int i = 0; i < IT; ++i)
 #pragma unroll
-            for (int c = 0; c < NC; ++c) put(i, c, acc[i][c]);
-        } else {
-          // A value that is not finite has met the zeros of P above the diagonal: the tiles again, with the
-          // diagonal's products one by one, so that it reaches no earlier token.
+          for (int c = 0; c < NC; ++c) put(i, c, acc[i][c]);
+        if (__any(bad != 0.f)) {
+          // A value of v that is not finite has met the zeros of P above the diagonal.  The diagonal's tiles again
+          // with zeros in its place, for the tokens in front of it, which then hold what they would without it.
 #pragma unroll 1
           for (int i = 0; i < IT; ++i) {
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
+              Frag<IOT> own = values(i / 2, c);
+              int from = 16;                          // the first such token of column l
+              if (i & 1) from = first_bad(own.b);
+              else from = first_bad(own.a);
+              from = from < 4 ? 4 * g + from : 16;
+              from = min(from, __shfl_xor(from, 16));
+              from = min(from, __shfl_xor(from, 32));
+              if (!__any(from < 16)) continue;
               f32x4v o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
               for (int k = 0; k < KT / 2; ++k) o = mma(sf[k][c], MK::row(lq + 16 * i * DK, at, 32 * k), o);
               o *= through[16 * i + l];
 #pragma unroll
-              for (int j = 0; j < JJ; ++j) {
-                if (2 * j + 1 == i) o = mma_half(values(j, c), weights(i, 2 * j), o);
-                else if (2 * j + 1 < i) o = mma(values(j, c), Frag<IOT>{weights(i, 2 * j), weights(i, 2 * j + 1)}, o);
+              for (int j = 0; j < JJ; ++j)
+                if (2 * j + 1 < i) o = mma(values(j, c), Frag<IOT>{weights(i, 2 * j), weights(i, 2 * j + 1)}, o);
+              if (i & 1) {
+                clear_bad(own.b);
+                o = mma(own, Frag<IOT>{weights(i, i - 1), weights(i, i)}, o);
+              } else {
+                clear_bad(own.a);
+                o = mma_half(own, weights(i, i), o);
               }
-#pragma unroll 1
-              for (int j = 0; j < 16; ++j) {
-                const float w = one(lp[((i * IT + i) * 64 + (j >> 2) * 16 + l) * 4 + (j & 3)]);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                  const float v = one(lv[16 * i * DVT + (MV::base(j) ^ (mine + 16 * c + 4 * g + r))]);
-                  o[r] = j <= l ? fmaf(w, v, o[r]) : o[r];
-                }
+              for (int r = 0; r < 4; ++r) {
+                const int behind = __shfl(from, 4 * g + r);
+                if (l < behind && behind < 16 && 16 * i + l < count && d0 + 16 * c + r < p.DV)
+                  st1<OUT32 ? 0 : 1>(out + 16 * i * out_step, 16 * c + r, o[r]);
               }
-              put(i, c, o);
             }
           }
         }
