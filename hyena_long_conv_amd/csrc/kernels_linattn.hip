@@ -2,6 +2,22 @@
 // over whole sequences, single tokens, and sums over shared heads.
 //
 //   S[t] = lambda S[t-1] + su k[t] v[t]^T,  out[t] = so S[t]^T q[t].
+//
+// The forward is one pass.  With G[t] the loss's gradient with respect to
+// S[t], gq[t] = S[t] go[t], gk[t] = G[t] v[t] and gv[t] = G[t]^T k[t], and G
+// runs from the last token to the first as S does from the first to the last:
+// the backward is three passes of the same kernel.
+//
+// What bounds them: the bytes of q, k, v and out at a copy's rate (5 TB/s)
+// would take 31 us for 8 x 2048 tokens of 12 heads 64 x 128 in bf16, 81 us for
+// 65536 tokens of 6 heads 128 x 128, 161 us for 65536 of 12 heads 64 x 64 in
+// fp32.  So few heads do not fill the chip one token after the other; the time
+// axis is split, and k and v are read twice, once for the states behind the
+// segments (k_lin with FILL, then k_lin_join) and once for the outputs: 43 +
+// 23 + 4, 110 + 55 + 6 and 205 + 100 + 4 us.  The main passes lose to their
+// memory what the barriers between a block's phases leave idle (vector units
+// 41% and matrix units 26% busy at 128 x 128; in fp32, whose matrix
+// instructions take 16 times as long, 66% of those).
 #include <hip/hip_runtime.h>
 
 #include "linattn.hpp"

@@ -1,7 +1,10 @@
 // kernels_rotary.hip -- rotary positions: pairs of a head's first R values
 // turned by position * frequency, the rest copied.
 //
-// Bound by its bytes: every value is read and written once.  What could cost
+// Bound by its bytes: every value is read and written once (8 x 2048 x 24 heads
+// of 64 in bf16: 18.5 us, 5.4 TB/s, part of it from the Infinity Cache; 65536
+// x 12 of 64 in fp32, half of each head turned: 84 us, 4.8 TB/s, a copy's rate;
+// 104 with words of 32 bytes to a lane and the copies in a branch of their own).  What could cost
 // more are the angles.  A thread forms the sines and cosines of 8 pairs (fp32: 4) of
 // a token once and turns those pairs in several heads, which share them.
 #include <hip/hip_runtime.h>
