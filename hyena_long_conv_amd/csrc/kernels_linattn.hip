@@ -198,16 +198,26 @@ __device__ __forceinline__ void clear_bad(u32x2v& f) {
   }
 }
 
-// The state's addends are products in fp32 of bf16 values and fp32 weights.
-// As matrix operands they go in three bf16 parts, 2^-24 of them left: with two
-// the state would be off by 2.7e-6 of its norm, with one by 1.7e-3.
-template <int IOT> constexpr int kParts = IOT == 1 ? 3 : 1;
-__device__ __forceinline__ void parts_of(f32x4v a, f32x4v b, Frag<0> (&o)[1]) { o[0] = {a, b}; }
-__device__ __forceinline__ void parts_of(f32x4v a, f32x4v b, Frag<1> (&o)[3]) {
+// fp32 values as operands: themselves in fp32, and in bf16 as a sum of bf16
+// parts, each rounded from what the ones before leave: after two parts 2^-18
+// of a value, after three less than its own last place.  The state's addends
+// go in three, since their sum is an fp32 output (two would leave it off by
+// 2.7e-6 of its norm and take 5 to 9% off the time); a pair's weight in two, which
+// costs 1 to 3 us of 70 and 176 in a forward and 6 of 97 in a backward; the state in its product
+// with q is rounded once, as the output is, since a second part of it costs 7
+// us there and, in spilled registers, 60 of 110 at 128 x 128.  So an output's
+// error is its own rounding's where its block's tokens make it up, and 1.4
+// times that where the tokens before them do.
+template <int IOT> constexpr int kParts = IOT == 1 ? 3 : 1;     // of the state's addends
+template <int IOT> constexpr int kFactors = IOT == 1 ? 2 : 1;   // of the pairs' weights
+template <int N>
+__device__ __forceinline__ void parts_of(f32x4v a, f32x4v b, Frag<0> (&o)[N]) { o[0] = {a, b}; }
+template <int N>
+__device__ __forceinline__ void parts_of(f32x4v a, f32x4v b, Frag<1> (&o)[N]) {
 #pragma unroll
-  for (int k = 0; k < 3; ++k) {
+  for (int k = 0; k < N; ++k) {
     o[k] = {narrow4(a), narrow4(b)};
-    if (k < 2) a -= widen4(o[k].a), b -= widen4(o[k].b);
+    if (k < N - 1) a -= widen4(o[k].a), b -= widen4(o[k].b);
   }
 }
 
@@ -320,14 +330,14 @@ template <int IOT> constexpr int kBlock = IOT == 1 ? 64 : 32;   // tokens of a b
 
 template <int IOT, int DK, int WAVES, int NC, bool FILL>
 constexpr int lin_lds_bytes() {
-  constexpr int C = kBlock<IOT>, E = IOT == 0 ? 4 : 2;
-  return (C * ((FILL ? 1 : 2) * DK + 16 * NC * WAVES) + (FILL ? 0 : C * C)) * E + (3 * C + 16) * 4;
+  constexpr int C = kBlock<IOT>, E = IOT == 0 ? 4 : 2, TILES = C / 16 * (C / 16 + 1) / 2;
+  return (C * ((FILL ? 1 : 2) * DK + 16 * NC * WAVES) + (FILL ? 0 : TILES * 256 * kFactors<IOT>)) * E + (3 * C + 16) * 4;
 }
 
 // FILL: the state behind a segment alone, from nothing, for all but the last segment (LinArgs.fill).
 template <int IOT, int DK, int WAVES, int NC, bool FILL, bool EVEN, bool OUT32>
 __global__ __launch_bounds__(64 * WAVES, DK >= 256 || NC == 2 || (DK >= 128 && WAVES == 4 && !FILL) ? 2 : 4) void k_lin(LinArgs a, int first_pass) {
-  constexpr int C = kBlock<IOT>, IT = C / 16, JJ = C / 32, KT = DK / 16, DVT = 16 * NC * WAVES, NP = kParts<IOT>;
+  constexpr int C = kBlock<IOT>, IT = C / 16, JJ = C / 32, KT = DK / 16, DVT = 16 * NC * WAVES, NP = kParts<IOT>, NF = kFactors<IOT>;
   constexpr int HELD = 4;                              // tiles of k's rows at a time
   typedef Lds<IOT, DK> MK;
   typedef Lds<IOT, DVT> MV;
@@ -341,7 +351,7 @@ __global__ __launch_bounds__(64 * WAVES, DK >= 256 || NC == 2 || (DK >= 128 && W
   T* const lk = reinterpret_cast<T*>(apart + C + 16);
   T* const lv = lk + C * DK;
   T* const lq = lv + C * DVT;
-  T* const lp = lq + C * DK;   // tiles (i, j) of 16 x 16 at i IT + j, 4 values to a lane
+  T* const lp = lq + C * DK;   // tiles (i, j) of 16 x 16 at (i (i + 1) / 2 + j) NF + part, 4 values to a lane
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = lane & 15, g = lane >> 4;
 
   const int tiles = (p.DV + DVT - 1) / DVT, segs = FILL ? a.segs - 1 : a.segs;
@@ -438,8 +448,10 @@ __global__ __launch_bounds__(64 * WAVES, DK >= 256 || NC == 2 || (DK >= 128 && W
 #pragma unroll
             for (int r = 0; r < 4; ++r) acc[r] = l >= 4 * g + r ? acc[r] : 0.f;
           }
-          // bf16: a pair's weight is rounded once, as an output is
-          *reinterpret_cast<Four*>(lp + ((i * IT + j) * 64 + lane) * 4) = as_operand<IOT>(acc);
+          Frag<IOT> w[NF];
+          parts_of(acc, acc, w);
+#pragma unroll
+          for (int f = 0; f < NF; ++f) *reinterpret_cast<Four*>(lp + ((k * NF + f) * 64 + lane) * 4) = w[f].a;
         }
         __syncthreads();
       }
@@ -450,14 +462,10 @@ __global__ __launch_bounds__(64 * WAVES, DK >= 256 || NC == 2 || (DK >= 128 && W
         return Frag<IOT>{MV::column(lv + 32 * j * DVT, at, 16 * c), MV::column(lv + (32 * j + 16) * DVT, at, 16 * c)};
       };
       if constexpr (!FILL) {
-        // bf16: the state is rounded once for its product with q, and stays fp32
-        Frag<IOT> sf[KT / 2][NC];
-#pragma unroll
-        for (int k = 0; k < KT / 2; ++k)
-#pragma unroll
-          for (int c = 0; c < NC; ++c) sf[k][c] = {as_operand<IOT>(S[2 * k][c]), as_operand<IOT>(S[2 * k + 1][c])};
         const T* const pt = lp + lane * 4;
-        const auto weights = [&](int i, int j) { return *reinterpret_cast<const Four*>(pt + (i * IT + j) * 256); };
+        const auto weights = [&](int i, int j, int f) {
+          return *reinterpret_cast<const Four*>(pt + ((i * (i + 1) / 2 + j) * NF + f) * 256);
+        };
         const auto put = [&](int i, int c, f32x4v o) {
           if (16 * i + l < count) {
             if (OUT32) st4n<0>(out + 16 * i * out_step, 16 * c, o, p.DV - d0 - 16 * c);
@@ -471,13 +479,17 @@ __global__ __launch_bounds__(64 * WAVES, DK >= 256 || NC == 2 || (DK >= 128 && W
           for (int c = 0; c < NC; ++c) acc[i][c] = f32x4v{0.f, 0.f, 0.f, 0.f};
         const int at = here(MK::base(l) ^ (8 * g));
 #pragma unroll
-        for (int k = 0; k < KT / 2; ++k)
+        for (int k = 0; k < KT / 2; ++k) {
+          Frag<IOT> sf[NC];
+#pragma unroll
+          for (int c = 0; c < NC; ++c) sf[c] = {as_operand<IOT>(S[2 * k][c]), as_operand<IOT>(S[2 * k + 1][c])};
 #pragma unroll
           for (int i = 0; i < IT; ++i) {
             const Frag<IOT> q = MK::row(lq + 16 * i * DK, at, 32 * k);
 #pragma unroll
-            for (int c = 0; c < NC; ++c) acc[i][c] = mma(sf[k][c], q, acc[i][c]);
+            for (int c = 0; c < NC; ++c) acc[i][c] = mma(sf[c], q, acc[i][c]);
           }
+        }
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
           const float w = through[16 * i + l];
@@ -491,11 +503,15 @@ __global__ __launch_bounds__(64 * WAVES, DK >= 256 || NC == 2 || (DK >= 128 && W
           for (int c = 0; c < NC; ++c) vt[c] = values(j, c);
 #pragma unroll
           for (int i = 2 * j; i < IT; ++i) {
-            Frag<IOT> w;
-            w.a = weights(i, 2 * j);
-            if (i > 2 * j) w.b = weights(i, 2 * j + 1);
 #pragma unroll
-            for (int c = 0; c < NC; ++c) acc[i][c] = i == 2 * j ? mma_half(vt[c], w.a, acc[i][c]) : mma(vt[c], w, acc[i][c]);
+            for (int f = NF - 1; f >= 0; --f) {
+              Frag<IOT> w;
+              w.a = weights(i, 2 * j, f);
+              if (i > 2 * j) w.b = weights(i, 2 * j + 1, f);
+#pragma unroll
+              for (int c = 0; c < NC; ++c)
+                acc[i][c] = i == 2 * j ? mma_half(vt[c], w.a, acc[i][c]) : mma(vt[c], w, acc[i][c]);
+            }
           }
         }
         float bad = 0.f;
@@ -526,18 +542,22 @@ __global__ __launch_bounds__(64 * WAVES, DK >= 256 || NC == 2 || (DK >= 128 && W
               if (!__any(from < 16)) continue;
               f32x4v o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-              for (int k = 0; k < KT / 2; ++k) o = mma(sf[k][c], MK::row(lq + 16 * i * DK, at, 32 * k), o);
+              for (int k = 0; k < KT / 2; ++k)
+                o = mma(Frag<IOT>{as_operand<IOT>(S[2 * k][c]), as_operand<IOT>(S[2 * k + 1][c])},
+                        MK::row(lq + 16 * i * DK, at, 32 * k), o);
               o *= through[16 * i + l];
 #pragma unroll
               for (int j = 0; j < JJ; ++j)
-                if (2 * j + 1 < i) o = mma(values(j, c), Frag<IOT>{weights(i, 2 * j), weights(i, 2 * j + 1)}, o);
-              if (i & 1) {
-                clear_bad(own.b);
-                o = mma(own, Frag<IOT>{weights(i, i - 1), weights(i, i)}, o);
-              } else {
-                clear_bad(own.a);
-                o = mma_half(own, weights(i, i), o);
-              }
+                if (2 * j + 1 < i) {
+#pragma unroll
+                  for (int f = NF - 1; f >= 0; --f)
+                    o = mma(values(j, c), Frag<IOT>{weights(i, 2 * j, f), weights(i, 2 * j + 1, f)}, o);
+                }
+              if (i & 1) clear_bad(own.b);
+              else clear_bad(own.a);
+#pragma unroll
+              for (int f = NF - 1; f >= 0; --f)
+                o = i & 1 ? mma(own, Frag<IOT>{weights(i, i - 1, f), weights(i, i, f)}, o) : mma_half(own, weights(i, i, f), o);
 #pragma unroll
               for (int r = 0; r < 4; ++r) {
                 const int behind = __shfl(from, 4 * g + r);
