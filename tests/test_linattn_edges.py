@@ -341,3 +341,44 @@ def test_entry_points_refuse_shapes():
     wide = x[:1].expand(2, -1, -1, -1)
     with pytest.raises(H.HyenaError):
         H.rotary(wide, freq, out=wide)                  # one memory for two sequences
+
+
+# ------------------------------------------------------ the caller's own memory
+
+def test_rotary_positions_for_a_whole_batch():
+    """No positions, one row of them for all sequences, and one for each give the same bits where they say the same."""
+    x = dev(gen(17)(3, 21, 2, 32))
+    freq, _ = H.rotary_frequencies(16, device=DEV)
+    row = torch.arange(21, device=DEV, dtype=torch.int32)
+    want = H.rotary(x, freq)
+    same(H.rotary(x, freq, row), want, "one row")
+    same(H.rotary(x, freq, row.expand(3, -1).contiguous()), want, "a row each")
+    same(H.rotary(x, freq, row + 7)[2], H.rotary(x[2:], freq, row + 7)[0], "the last sequence")
+
+
+@pytest.mark.parametrize("io", ["fp32", "bf16"])
+def test_outputs_and_workspaces_of_the_caller(io):
+    """A workspace that holds anything, larger than asked for and used again, and outputs that are given."""
+    t, r = TYPES[io], gen(18)
+    B, L, N, D = 1, 2000, 2, 64
+    q, k, v, go = (dev(r(B, L, h, D).to(t)) for h in (N, 1, N, N))
+    want, last = H.linear_attention(q, k, v, return_state=True)
+    grads = H.linear_attention_backward(q, k, v, go)
+    need = max(H.linear_attention_workspace_bytes(B, L, N, D, D), H.linear_attention_backward_workspace_bytes(B, L, N, N, 1, N, D, D))
+    assert H.linear_attention_workspace_bytes(B, L, N, D, D) > 0
+    ws = torch.full((need + 4096,), 255, dtype=torch.uint8, device=DEV)
+    o, s = torch.empty_like(want), torch.empty_like(last)
+    for _ in range(2):
+        got = H.linear_attention(q, k, v, return_state=True, out=o, state_out=s, workspace=ws)
+        assert got[0] is o and got[1] is s
+        same(o, want, "o")
+        same(s, last, "state")
+        for name, x in H.linear_attention_backward(q, k, v, go, workspace=ws).items():
+            same(x, grads[name], name)
+    with pytest.raises(H.HyenaError):
+        H.linear_attention(q, k, v, workspace=ws[:16])
+    x, w = dev(r(50, 96).to(t)), dev(r(96))
+    a, b = H.group_norm_backward(x, 3, x, w), H.group_norm_backward(x, 3, x, w, workspace=torch.full(
+        (H.group_norm_backward_workspace_bytes(50, 96, 3),), 255, dtype=torch.uint8, device=DEV))
+    for name in a:
+        same(a[name], b[name], name)
