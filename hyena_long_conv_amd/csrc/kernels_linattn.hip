@@ -168,11 +168,12 @@ __device__ __forceinline__ int here(int v) {
   return v;
 }
 
-__device__ __forceinline__ u32x2v narrow4(f32x4v v) { return u32x2v{bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3])}; }
-template <int IOT> __device__ __forceinline__ auto as_operand(f32x4v v) {
-  if constexpr (IOT == 0) return v;
-  else return narrow4(v);
+__device__ __forceinline__ f32x4v here(f32x4v v) {
+  asm volatile("" : "+v"(v));
+  return v;
 }
+
+__device__ __forceinline__ u32x2v narrow4(f32x4v v) { return u32x2v{bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3])}; }
 __device__ __forceinline__ f32x4v widen4(f32x4v v) { return v; }
 __device__ __forceinline__ f32x4v widen4(u32x2v v) {
   return f32x4v{__uint_as_float(v[0] << 16), __uint_as_float(v[0] & 0xffff0000u), __uint_as_float(v[1] << 16),
@@ -199,17 +200,20 @@ __device__ __forceinline__ void clear_bad(u32x2v& f) {
 }
 
 // fp32 values as operands: themselves in fp32, and in bf16 as a sum of bf16
-// parts, each rounded from what the ones before leave: after two parts 2^-18
-// of a value, after three less than its own last place.  The state's addends
-// go in three, since their sum is an fp32 output (two would leave it off by
-// 2.7e-6 of its norm and take 5 to 9% off the time); a pair's weight in two, which
-// costs 1 to 3 us of 70 and 176 in a forward and 6 of 97 in a backward; the state in its product
-// with q is rounded once, as the output is, since a second part of it costs 7
-// us there and, in spilled registers, 60 of 110 at 128 x 128.  So an output's
-// error is its own rounding's where its block's tokens make it up, and 1.4
-// times that where the tokens before them do.
+// parts, each rounded from what the ones before leave: at most 2^-8 of a value
+// after one part, 2^-17 after two, 2^-26, less than its last place, after three.
+// The state's addends go in three, since their sum is an fp32 output (two would
+// leave it off by 2.7e-6 of its norm and take 5 to 9% off the time).  A pair's
+// weight and the state in its product with q go in two: at most 2^-17 of the
+// sizes of an output's terms, |w| |v| and |q| |S|, are lost, which shows beside
+// the output's own rounding only where the terms cancel to 2^-9 of their sizes
+// or less.  One part of the state left 2^-8 of |q| |S|: 1.4 times the error of
+// outputs of random values, 4 times where the keys share a direction that the
+// queries lack.  Its second part costs 1 us of 45 in the main pass of 64 x 128
+// heads and of 25 in that of 64 x 64, 16 of 113 at 128 x 128, 8 of 74 at 256 x 256.
 template <int IOT> constexpr int kParts = IOT == 1 ? 3 : 1;     // of the state's addends
 template <int IOT> constexpr int kFactors = IOT == 1 ? 2 : 1;   // of the pairs' weights
+template <int IOT> constexpr int kStates = IOT == 1 ? 2 : 1;    // of the state where q meets it
 template <int N>
 __device__ __forceinline__ void parts_of(f32x4v a, f32x4v b, Frag<0> (&o)[N]) { o[0] = {a, b}; }
 template <int N>
@@ -337,7 +341,7 @@ constexpr int lin_lds_bytes() {
 // FILL: the state behind a segment alone, from nothing, for all but the last segment (LinArgs.fill).
 template <int IOT, int DK, int WAVES, int NC, bool FILL, bool EVEN, bool OUT32>
 __global__ __launch_bounds__(64 * WAVES, DK >= 256 || NC == 2 || (DK >= 128 && WAVES == 4 && !FILL) ? 2 : 4) void k_lin(LinArgs a, int first_pass) {
-  constexpr int C = kBlock<IOT>, IT = C / 16, JJ = C / 32, KT = DK / 16, DVT = 16 * NC * WAVES, NP = kParts<IOT>, NF = kFactors<IOT>;
+  constexpr int C = kBlock<IOT>, IT = C / 16, JJ = C / 32, KT = DK / 16, DVT = 16 * NC * WAVES, NP = kParts<IOT>, NF = kFactors<IOT>, NS = kStates<IOT>;
   constexpr int HELD = 4;                              // tiles of k's rows at a time
   typedef Lds<IOT, DK> MK;
   typedef Lds<IOT, DVT> MV;
@@ -480,14 +484,16 @@ __global__ __launch_bounds__(64 * WAVES, DK >= 256 || NC == 2 || (DK >= 128 && W
         const int at = here(MK::base(l) ^ (8 * g));
 #pragma unroll
         for (int k = 0; k < KT / 2; ++k) {
-          Frag<IOT> sf[NC];
+          Frag<IOT> sf[NC][NS];
 #pragma unroll
-          for (int c = 0; c < NC; ++c) sf[c] = {as_operand<IOT>(S[2 * k][c]), as_operand<IOT>(S[2 * k + 1][c])};
+          for (int c = 0; c < NC; ++c) parts_of(S[2 * k][c], S[2 * k + 1][c], sf[c]);
 #pragma unroll
           for (int i = 0; i < IT; ++i) {
             const Frag<IOT> q = MK::row(lq + 16 * i * DK, at, 32 * k);
 #pragma unroll
-            for (int c = 0; c < NC; ++c) acc[i][c] = mma(sf[c], q, acc[i][c]);
+            for (int f = NS - 1; f >= 0; --f)
+#pragma unroll
+              for (int c = 0; c < NC; ++c) acc[i][c] = mma(sf[c][f], q, acc[i][c]);
           }
         }
 #pragma unroll
@@ -542,9 +548,13 @@ __global__ __launch_bounds__(64 * WAVES, DK >= 256 || NC == 2 || (DK >= 128 && W
               if (!__any(from < 16)) continue;
               f32x4v o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-              for (int k = 0; k < KT / 2; ++k)
-                o = mma(Frag<IOT>{as_operand<IOT>(S[2 * k][c]), as_operand<IOT>(S[2 * k + 1][c])},
-                        MK::row(lq + 16 * i * DK, at, 32 * k), o);
+              for (int k = 0; k < KT / 2; ++k) {
+                const Frag<IOT> q = MK::row(lq + 16 * i * DK, at, 32 * k);
+                Frag<IOT> sf[NS];
+                parts_of(here(S[2 * k][c]), here(S[2 * k + 1][c]), sf);   // not kept from above: 35 spilled registers at 128 x 128
+#pragma unroll
+                for (int f = NS - 1; f >= 0; --f) o = mma(sf[f], q, o);
+              }
               o *= through[16 * i + l];
 #pragma unroll
               for (int j = 0; j < JJ; ++j)

@@ -601,9 +601,11 @@ hyena_status hyena_scaled_matmul(const void* q, const float* scales, const void*
  * positive one grows the state, exp(log_decay t) not to overflow.  It is a
  * constant of the head: the backward forms no gradient of it.
  *
- * Sums and states are fp32.  With bf16 activations the state is rounded to
- * bf16 in its product with q (it is kept, and handed on, in fp32), and so are
- * the states and their gradients in the backward's products.  A value that is
+ * Sums and states are fp32.  With bf16 activations the state where q meets
+ * it, the weight of a pair of tokens where v does, and the states and their
+ * gradients in the backward's products are taken to 2^-17 of themselves: an
+ * output is off by its own rounding and at most 2^-17 of the summed sizes of
+ * its terms (states are kept, and handed on, in fp32).  A value that is
  * not finite reaches what the formulas say and no earlier token; an infinity
  * may become NaN on its way.
  * workspace: hyena_linear_attention_workspace_bytes() (0 where the time axis
