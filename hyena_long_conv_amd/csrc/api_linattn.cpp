@@ -48,7 +48,8 @@ int64_t seg_bytes(const LinPlan& p, int64_t B, int64_t H, int64_t Dk, int64_t Dv
 }
 
 // The backward's workspace: states before and behind the segments, and fp32
-// gradients of every head where heads share one.
+// gradients of every head where heads share one.  For sizes that a launch
+// takes (kMaxGroups), so B H < 2^24 and the sum stays below 2^58.
 struct BackwardLayout {
   int64_t before, behind, part[3], total;
 };
@@ -84,7 +85,8 @@ static hyena_status lin_args(const hyena_linear_attention_params* p, hyena_dtype
 
 int64_t hyena_linear_attention_workspace_bytes(int64_t B, int64_t L, int32_t H, int32_t Dk, int32_t Dv) {
   if (!heads_ok(B, L, H, H, H, H, Dk, Dv)) return -1;
-  return seg_bytes(lin_plan(B, L, H, Dk, Dv), B, H, Dk, Dv);
+  const LinPlan plan = lin_plan(B, L, H, Dk, Dv);
+  return lin_groups(plan, B, H) > kMaxGroups ? -1 : seg_bytes(plan, B, H, Dk, Dv);
 }
 
 hyena_status hyena_linear_attention(const hyena_linear_attention_params* p, void* o, float* state_out, hyena_dtype io,
@@ -159,7 +161,8 @@ hyena_status hyena_linear_attention_step(const hyena_linear_attention_params* p,
 int64_t hyena_linear_attention_backward_workspace_bytes(int64_t B, int64_t L, int32_t H, int32_t Hq, int32_t Hk,
                                                         int32_t Hv, int32_t Dk, int32_t Dv) {
   if (!heads_ok(B, L, H, Hq, Hk, Hv, Dk, Dv)) return -1;
-  return backward_layout(lin_backward_plan(B, L, H, Dk, Dv), B, L, H, {Hq, Hk, Hv}, Dk, Dv).total;
+  const LinPlan plan = lin_backward_plan(B, L, H, Dk, Dv);
+  return lin_groups(plan, B, H) > kMaxGroups ? -1 : backward_layout(plan, B, L, H, {Hq, Hk, Hv}, Dk, Dv).total;
 }
 
 hyena_status hyena_linear_attention_backward(const hyena_linear_attention_params* p, const void* go,
@@ -300,12 +303,16 @@ static bool group_sizes_ok(int64_t rows, int64_t D, int64_t G) {
   return rows >= 1 && rows <= ((int64_t)1 << 31) && D >= 1 && D <= kMaxDim && G >= 1 && G <= D && D % G == 0;
 }
 
+static bool group_launch_ok(int64_t rows, int64_t D, int64_t G) {   // a group wider than a workgroup's registers is a workgroup's
+  return group_norm_plan(G, D / G).words || rows * G <= kMaxGroups;
+}
+
 static hyena_status group_args(const hyena_group_norm_params* p, hyena_dtype io, GroupNormArgs* a) {
   if (!p || !p->x) return HYENA_ERR_NULL;
   if (!group_sizes_ok(p->rows, p->D, p->G)) return HYENA_ERR_SHAPE;
   if ((p->silu != 0 && p->silu != 1) || (p->silu && p->z) || !io_ok(io) || !(p->eps >= 0.f) || !std::isfinite(p->eps))
     return HYENA_ERR_UNSUPPORTED;
-  if (!group_norm_plan(p->G, p->D / p->G).words && p->rows * p->G > kMaxGroups) return HYENA_ERR_UNSUPPORTED;
+  if (!group_launch_ok(p->rows, p->D, p->G)) return HYENA_ERR_UNSUPPORTED;
   *a = GroupNormArgs{};
   a->x = p->x;
   a->z = p->z;
@@ -333,7 +340,7 @@ hyena_status hyena_group_norm(const hyena_group_norm_params* p, void* y, hyena_d
 }
 
 int64_t hyena_group_norm_backward_workspace_bytes(int64_t rows, int32_t D, int32_t G) {
-  if (!group_sizes_ok(rows, D, G)) return -1;
+  if (!group_sizes_ok(rows, D, G) || !group_launch_ok(rows, D, G)) return -1;
   return group_norm_backward_parts(rows, G, D / G) * 2 * D * 4;
 }
 

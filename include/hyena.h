@@ -609,7 +609,8 @@ hyena_status hyena_scaled_matmul(const void* q, const float* scales, const void*
  * not finite reaches what the formulas say and no earlier token; an infinity
  * may become NaN on its way.
  * workspace: hyena_linear_attention_workspace_bytes() (0 where the time axis
- * is not split).
+ * is not split; this block's sizes of workspaces are -1 for sizes that the
+ * call refuses).
  */
 #define HYENA_MAX_HEAD 256
 

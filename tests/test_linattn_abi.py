@@ -90,6 +90,18 @@ def test_workspace_sizes_refuse_what_the_calls_refuse():
     assert 0 < f(1, 1 << 22, 1, 256, 256) <= 256 * 256 * 256 * 4 and f(64, 4096, 64, 64, 64) == 0
 
 
+def test_workspace_sizes_of_calls_too_large_to_launch():
+    """Sizes whose launches a call refuses (UNSUPPORTED): -1, where sums of their bytes pass 63 bits too."""
+    f, g, n = H.linear_attention_workspace_bytes, H.linear_attention_backward_workspace_bytes, H.group_norm_backward_workspace_bytes
+    for heads in ((1, 1, 1), (1, 1, 1024), (1024, 1024, 1024)):
+        assert g(1 << 20, 1 << 22, 1024, *heads, 256, 256) == -1
+    assert f(1 << 20, 1 << 22, 1024, 256, 256) == -1 and f(1 << 20, 1, 16, 16, 16) == -1
+    assert attention("hyena_linear_attention", B=1 << 20, H=16, L=1, Dk=16, Dv=16) == UNSUP
+    assert attention("hyena_linear_attention_backward", B=1 << 20, H=1024, L=1 << 22, Hq=1, Hk=1, Hv=1, Dk=256, Dv=256) == UNSUP
+    assert n(1 << 24, 10000, 1) == -1 and norm(back=True, rows=1 << 24, D=10000, G=1) == UNSUP
+    assert n((1 << 24) - 1, 10000, 1) > 0
+
+
 def rotary(x=P[0], out=P[1], io=0, null=False, **k):
     B, L, N, D = k.get("B", 2), k.get("L", 8), k.get("H", 4), k.get("D", 64)
     p = linattn.RotaryParams(B, L, N, D, k.get("R", 32), k.get("il", 0), k.get("inv", 0), k.get("scale", 1.0),
