@@ -86,7 +86,7 @@ static hyena_status lin_args(const hyena_linear_attention_params* p, hyena_dtype
 int64_t hyena_linear_attention_workspace_bytes(int64_t B, int64_t L, int32_t H, int32_t Dk, int32_t Dv) {
   if (!heads_ok(B, L, H, H, H, H, Dk, Dv)) return -1;
   const LinPlan plan = lin_plan(B, L, H, Dk, Dv);
-  return lin_groups(plan, B, H) > kMaxGroups ? -1 : seg_bytes(plan, B, H, Dk, Dv);
+  return lin_groups(plan, B, H, Dv) > kMaxGroups ? -1 : seg_bytes(plan, B, H, Dk, Dv);
 }
 
 hyena_status hyena_linear_attention(const hyena_linear_attention_params* p, void* o, float* state_out, hyena_dtype io,
@@ -96,7 +96,7 @@ hyena_status hyena_linear_attention(const hyena_linear_attention_params* p, void
   if (!o) return HYENA_ERR_NULL;
   const int64_t e = size_of(io), st = p->B * p->H * p->Dk * p->Dv * 4;
   const LinPlan plan = lin_plan(p->B, p->L, p->H, p->Dk, p->Dv);
-  if (lin_groups(plan, p->B, p->H) > kMaxGroups) return HYENA_ERR_UNSUPPORTED;
+  if (lin_groups(plan, p->B, p->H, p->Dv) > kMaxGroups) return HYENA_ERR_UNSUPPORTED;
   const int64_t need = seg_bytes(plan, p->B, p->H, p->Dk, p->Dv);
   if (need && (!workspace || workspace_bytes < need)) return HYENA_ERR_WORKSPACE;
   const Span out[] = {{o, p->B * p->L * p->H * p->Dv * e, 16}, {state_out, st, 16}, {need ? workspace : nullptr, need, 16}};
@@ -137,7 +137,7 @@ hyena_status hyena_linear_attention_step(const hyena_linear_attention_params* p,
   int64_t ext[3];
   if (const hyena_status s = lin_args(p, io, 1, ext)) return s;
   if (!o || !state) return HYENA_ERR_NULL;
-  if (p->B * p->H * 4 > kMaxGroups) return HYENA_ERR_UNSUPPORTED;   // at most 4 workgroups to a head
+  if (p->B * p->H * lin_step_plan(p->Dv).tiles > kMaxGroups) return HYENA_ERR_UNSUPPORTED;
   const int64_t e = size_of(io), st = p->B * p->H * p->Dk * p->Dv * 4;
   const Span out[] = {{o, p->B * p->H * p->Dv * e, 16}, {state, st, 16}};
   const Span in[] = {{p->q, ext[0] * e, e}, {p->k, ext[1] * e, e}, {p->v, ext[2] * e, e}, {p->log_decay, p->H * 4, 4}};
@@ -162,7 +162,7 @@ int64_t hyena_linear_attention_backward_workspace_bytes(int64_t B, int64_t L, in
                                                         int32_t Hv, int32_t Dk, int32_t Dv) {
   if (!heads_ok(B, L, H, Hq, Hk, Hv, Dk, Dv)) return -1;
   const LinPlan plan = lin_backward_plan(B, L, H, Dk, Dv);
-  return lin_groups(plan, B, H) > kMaxGroups ? -1 : backward_layout(plan, B, L, H, {Hq, Hk, Hv}, Dk, Dv).total;
+  return lin_groups(plan, B, H, Dk > Dv ? Dk : Dv) > kMaxGroups ? -1 : backward_layout(plan, B, L, H, {Hq, Hk, Hv}, Dk, Dv).total;
 }
 
 hyena_status hyena_linear_attention_backward(const hyena_linear_attention_params* p, const void* go,
@@ -173,7 +173,7 @@ hyena_status hyena_linear_attention_backward(const hyena_linear_attention_params
   if (!go || !g || !g->gq || !g->gk || !g->gv) return HYENA_ERR_NULL;
   const int64_t e = size_of(io), st = p->B * p->H * p->Dk * p->Dv * 4, tokens = p->B * p->L;
   const LinPlan plan = lin_backward_plan(p->B, p->L, p->H, p->Dk, p->Dv);
-  if (lin_groups(plan, p->B, p->H) > kMaxGroups) return HYENA_ERR_UNSUPPORTED;
+  if (lin_groups(plan, p->B, p->H, p->Dk > p->Dv ? p->Dk : p->Dv) > kMaxGroups) return HYENA_ERR_UNSUPPORTED;
   const int64_t heads[3] = {p->Hq, p->Hk, p->Hv};
   const BackwardLayout w = backward_layout(plan, p->B, p->L, p->H, heads, p->Dk, p->Dv);
   if (w.total && (!workspace || workspace_bytes < w.total)) return HYENA_ERR_WORKSPACE;

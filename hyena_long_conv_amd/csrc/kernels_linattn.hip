@@ -858,16 +858,14 @@ __global__ __launch_bounds__(256) void k_fold(FoldArgs a) {
 hipError_t linear_attention(const LinArgs& a, hipStream_t s) { return a.io ? launch<1>(a, s) : launch<0>(a, s); }
 
 hipError_t linear_attention_step(const LinStepArgs& a, hipStream_t s) {
-  const int vec = a.Dv % 4 ? 1 : 4, words = a.Dv / vec;
-  int cols = 1;
-  while (cols < words && cols < 64) cols *= 2;
-  const dim3 grid((unsigned)((words + cols - 1) / cols * ((int64_t)a.B * a.H)));
+  const LinStepPlan p = lin_step_plan(a.Dv);
+  const dim3 grid((unsigned)(p.tiles * ((int64_t)a.B * a.H)));
   if (a.io) {
-    if (vec == 4) k_lin_step<1, 4><<<grid, 256, 0, s>>>(a, cols);
-    else k_lin_step<1, 1><<<grid, 256, 0, s>>>(a, cols);
+    if (p.vec == 4) k_lin_step<1, 4><<<grid, 256, 0, s>>>(a, p.cols);
+    else k_lin_step<1, 1><<<grid, 256, 0, s>>>(a, p.cols);
   } else {
-    if (vec == 4) k_lin_step<0, 4><<<grid, 256, 0, s>>>(a, cols);
-    else k_lin_step<0, 1><<<grid, 256, 0, s>>>(a, cols);
+    if (p.vec == 4) k_lin_step<0, 4><<<grid, 256, 0, s>>>(a, p.cols);
+    else k_lin_step<0, 1><<<grid, 256, 0, s>>>(a, p.cols);
   }
   return hipGetLastError();
 }

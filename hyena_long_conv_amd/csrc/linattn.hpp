@@ -78,8 +78,11 @@ inline LinPlan lin_plan(int64_t B, int64_t L, int64_t H, int64_t DK, int64_t DV)
 inline LinPlan lin_backward_plan(int64_t B, int64_t L, int64_t H, int64_t Dk, int64_t Dv) {
   return lin_plan(Dk > 64 || Dv > 64 ? 2 * B : B, L, H, Dk, Dv);
 }
-// The most workgroups of a launch of one pass.
-inline int64_t lin_groups(const LinPlan& p, int64_t B, int64_t H) { return B * H * p.segs * 4; }
+// The most workgroups of a launch of one pass with DV columns, counted by
+// their 256 threads (128 columns may take 512).
+inline int64_t lin_groups(const LinPlan& p, int64_t B, int64_t H, int64_t DV) {
+  return B * H * p.segs * (DV <= 64 ? 1 : DV <= 128 ? 2 : 4);
+}
 
 struct LinStepArgs {
   HeadView q, k, v;        // token strides unused
@@ -89,6 +92,18 @@ struct LinStepArgs {
   int B, H, Dk, Dv, io;
   float scale;
 };
+
+// A token's launch: words of 4 columns (1 where Dv is no multiple) of a head's
+// state, `cols` of them (a power of two) to a workgroup.
+struct LinStepPlan {
+  int vec, cols, tiles;
+};
+inline LinStepPlan lin_step_plan(int Dv) {
+  const int vec = Dv % 4 ? 1 : 4, words = Dv / vec;
+  int cols = 1;
+  while (cols < words && cols < 64) cols *= 2;
+  return LinStepPlan{vec, cols, (words + cols - 1) / cols};
+}
 
 // Sums over the heads that share one: out[t][j][d] = sum of x[t][j share ..][d].
 struct FoldArgs {
