@@ -161,7 +161,7 @@ hyena_status hyena_linear_attention_step(const hyena_linear_attention_params* p,
 int64_t hyena_linear_attention_backward_workspace_bytes(int64_t B, int64_t L, int32_t H, int32_t Hq, int32_t Hk,
                                                         int32_t Hv, int32_t Dk, int32_t Dv) {
   if (!heads_ok(B, L, H, Hq, Hk, Hv, Dk, Dv)) return -1;
-  const LinPlan plan = lin_backward_plan(B, L, H, Dk, Dv);
+  const LinPlan plan = lin_backward_plan(B, L, H, Dk, Dv, 0);   // no fewer segments than bf16's
   return lin_groups(plan, B, H, Dk > Dv ? Dk : Dv) > kMaxGroups ? -1 : backward_layout(plan, B, L, H, {Hq, Hk, Hv}, Dk, Dv).total;
 }
 
@@ -172,7 +172,7 @@ hyena_status hyena_linear_attention_backward(const hyena_linear_attention_params
   if (const hyena_status s = lin_args(p, io, p ? p->L : 1, ext)) return s;
   if (!go || !g || !g->gq || !g->gk || !g->gv) return HYENA_ERR_NULL;
   const int64_t e = size_of(io), st = p->B * p->H * p->Dk * p->Dv * 4, tokens = p->B * p->L;
-  const LinPlan plan = lin_backward_plan(p->B, p->L, p->H, p->Dk, p->Dv);
+  const LinPlan plan = lin_backward_plan(p->B, p->L, p->H, p->Dk, p->Dv, io == HYENA_BF16);
   if (lin_groups(plan, p->B, p->H, p->Dk > p->Dv ? p->Dk : p->Dv) > kMaxGroups) return HYENA_ERR_UNSUPPORTED;
   const int64_t heads[3] = {p->Hq, p->Hk, p->Hv};
   const BackwardLayout w = backward_layout(plan, p->B, p->L, p->H, heads, p->Dk, p->Dv);

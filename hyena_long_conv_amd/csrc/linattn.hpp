@@ -70,13 +70,17 @@ inline LinPlan lin_plan(int64_t B, int64_t L, int64_t H, int64_t DK, int64_t DV)
   seg = (seg + 63) / 64 * 64;
   return LinPlan{(int)((L + seg - 1) / seg), seg};
 }
-// The backward's passes for gq and gk share a launch, so that half as many
-// segments fill the chip: 32768 tokens of 6 heads 128 x 128 bf16 253 us (279
-// with as many as in the forward), 4 x 2048 of 12 heads 64 x 128 107 (111).
-// Narrow heads keep the forward's number (2 x 8192 of 12 heads 64 x 64 fp32
-// 228 us, 239 with half of them).
-inline LinPlan lin_backward_plan(int64_t B, int64_t L, int64_t H, int64_t Dk, int64_t Dv) {
-  return lin_plan(Dk > 64 || Dv > 64 ? 2 * B : B, L, H, Dk, Dv);
+// The backward's passes for gq and gk share a launch where both or neither are
+// summed over shared heads.  In bf16 half as many segments as in the forward
+// fill the chip: 4 x 2048 tokens of 12 heads 64 x 128 112 us (116 with as many
+// as in the forward), 32768 of 6 heads 128 x 128 260 (274), of 12 heads 64 x 64
+// 205 (210).  With k and v on fewer heads, where those passes share no launch:
+// 32768 of 6 heads 128 x 128 on 2 344 (363), 4 x 2048 of 12 heads 64 x 64 on 4
+// 91 and 91, of 64 x 128 154 (148), the one that half as many cost.  In fp32
+// they cost: 16384 of 6 heads 128 x 128 352 us, 400 with half of them, on 2
+// heads 388 and 433, 2 x 8192 of 12 heads 64 x 64 226 and 245.
+inline LinPlan lin_backward_plan(int64_t B, int64_t L, int64_t H, int64_t Dk, int64_t Dv, int io) {
+  return lin_plan(io ? 2 * B : B, L, H, Dk, Dv);
 }
 // The most workgroups of a launch of one pass with DV columns, counted by
 // their 256 threads (128 columns may take 512).

@@ -39,3 +39,21 @@ def test_four_million_heads():
     one = H.linear_attention_step(q[:, 0], k[:, 0], v[:, 0], state, decay)
     near(one, ref["o"][0][:, 0], ref["o"][1][:, 0], 2 * D + 16, 0, "o of a token")
     near(state, *ref["state"], 16, 0, "state of a token")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("io", ["fp32", "bf16"])
+@pytest.mark.parametrize("heads,Dk,Dv", [((3, 1, 3), 128, 100), ((2, 2, 2), 64, 128), ((2, 1, 1), 40, 64)])
+def test_backward_workspace_as_large_as_asked_for(heads, Dk, Dv, io):
+    """One size serves both types, whose splits of the time axis differ; nothing behind it is written."""
+    L, N = 5000, max(heads)
+    g = torch.Generator(device=DEV).manual_seed(2)
+    t = torch.bfloat16 if io == "bf16" else torch.float32
+    q, k, v, go = (torch.randn(1, L, h, d, generator=g, device=DEV).to(t) for h, d in ((heads[0], Dk), (heads[1], Dk), (heads[2], Dv), (N, Dv)))
+    need = H.linear_attention_backward_workspace_bytes(1, L, N, *heads, Dk, Dv)
+    room = torch.full((need + 4096,), 85, dtype=torch.uint8, device=DEV)
+    want = H.linear_attention_backward(q, k, v, go)
+    got = H.linear_attention_backward(q, k, v, go, workspace=room[:need])
+    for name in ("gq", "gk", "gv"):
+        assert torch.equal(got[name], want[name]), name
+    assert bool((room[need:] == 85).all())
