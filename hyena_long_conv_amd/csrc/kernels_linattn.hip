@@ -13,11 +13,11 @@
 // 65536 tokens of 6 heads 128 x 128, 161 us for 65536 of 12 heads 64 x 64 in
 // fp32.  So few heads do not fill the chip one token after the other; the time
 // axis is split, and k and v are read twice, once for the states behind the
-// segments (k_lin with FILL, then k_lin_join) and once for the outputs: 43 +
-// 23 + 4, 110 + 55 + 6 and 205 + 100 + 4 us.  The main passes lose to their
+// segments (k_lin with FILL, then k_lin_join) and once for the outputs: 46 +
+// 23 + 5, 128 + 54 + 14 and 214 + 100 + 13 us.  The main passes lose to their
 // memory what the barriers between a block's phases leave idle (vector units
-// 41% and matrix units 26% busy at 128 x 128; in fp32, whose matrix
-// instructions take 16 times as long, 66% of those).
+// 47% and matrix units 29% busy at 128 x 128; in fp32, whose matrix
+// instructions take 16 times as long, 65% of those).
 #include <hip/hip_runtime.h>
 
 #include "linattn.hpp"
@@ -731,9 +731,10 @@ hipError_t launch_tiles(const LinArgs& a, int first, int count, hipStream_t s) {
 // Columns of the state to a workgroup: 64 in 4 waves, or 128.  Those in 8
 // waves of 16, four of which a SIMD holds, or in 4 of 32, which read the rows
 // of q and k half as often but leave two to a SIMD.  bf16, 8 x 2048 tokens of 12 heads
-// 64 x 128: 43 us in 8 waves, 46 in 4 (the fill 23 and 25); 65536 tokens of 6 heads
-// 128 x 128: 107 in 4, 145 in 8, whose registers spill there (the fill, which
-// needs fewer: 60 in 8, 63 in 4).
+// 64 x 128: 46 us in 8 waves, 52 in 4 (the fill 23 and 25); 65536 tokens of 6 heads
+// 128 x 128: 128 in 4, 131 in 8, whose registers spill there (the fill, which
+// needs fewer: 54 in 8, 59 in 4).  Heads of 129 to 256 values of k with up to 64
+// of v spill 12 to 16 registers in 4 waves, which stay.
 template <int IOT, bool FILL, bool EVEN>
 hipError_t launch_sizes(const LinArgs& a, int first, int count, hipStream_t s) {
   const LinPass& p = FILL ? a.fill[0] : a.pass[first];

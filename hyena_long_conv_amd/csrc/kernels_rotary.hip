@@ -18,7 +18,10 @@ namespace {
 // The cosine and sine of position * freq, freq in radians.  In fp32 the
 // product of a position of 2^20 would be off by 2^-4 radians; in fp64 the
 // turns are off by 2^-52 of their number, and what is left of them after the
-// whole ones, at most half a turn, loses 2^-25 of itself when it is rounded.
+// whole ones, at most half a turn, loses 2^-25 of itself when it is rounded.  The
+// sines and cosines are fp32's and are rounded again with the scale: outputs in
+// fp32 are off by 4.7e-8 of their norm where half of each head is turned, 3.6e-8
+// with fp64's sines rounded once; in bf16 neither shows.
 __device__ __forceinline__ void turn(double position, double freq, float scale, float sine, float& c, float& s) {
   const double turns = position * freq * 0.15915494309189535;
   float sn, cs;

@@ -172,7 +172,8 @@ hipError_t group_norm_backward(const GroupNormArgs& a, hipStream_t s);
 // How a launch covers rows of G groups of Dg values: `lanes` threads (a power
 // of two up to 256) to a group, `words` words of 8 values to a thread; a
 // workgroup of 256 threads takes `per` neighbouring groups of `rows` rows at
-// a time.  Groups beyond 256 x 4 words are read twice (`words` 0).
+// a time.  Groups beyond 256 x 4 words (`words` 0) are not held: x is read three
+// times, by the backward four times, and gy and z twice.
 struct GroupNormPlan {
   int lanes, words, per, rows;
   int64_t blocks;              // workgroups across a row's groups

@@ -209,8 +209,10 @@ def rotary_frequencies(dim: int, base: float = 10000.0, scaling: str = "none", f
     (positions interpolated); "ntk" raises the base to base factor^(dim/(dim-2)),
     which divides the slowest by factor and keeps the fastest; "yarn" keeps
     pairs that turn at least turns[1] times within `context`, divides those
-    that turn at most turns[0] times, blends linearly in between, and gives
-    the scale 0.1 log(factor) + 1 (to queries and keys alike)."""
+    that turn at most turns[0] times, and gives the scale 0.1 log(factor) + 1
+    (to queries and keys alike).  Between them it blends the two linearly in
+    the number of turns; a model that was trained with a blend linear in the
+    pair's index needs frequencies of its own, which rotary takes as they are."""
     torch = _torch()
     if dim < 2 or dim % 2:
         raise ValueError(f"dim must be even and at least 2, not {dim}")

@@ -641,7 +641,7 @@ hyena_status hyena_linear_attention(const hyena_linear_attention_params* p, void
                                     hyena_dtype io, void* workspace, int64_t workspace_bytes, void* stream);
 
 /* One token for each sequence: q, k, v [B][..][D] (the strides between tokens
- * are not used), o [B][H][Dv]; state [B][H][Dk][Dv] is moved on by one in
+ * move nothing, but are checked as the others are), o [B][H][Dv]; state [B][H][Dk][Dv] is moved on by one in
  * place.  p->L, p->state and p->lengths are not used. */
 hyena_status hyena_linear_attention_step(const hyena_linear_attention_params* p, float* state, void* o,
                                          hyena_dtype io, void* stream);
