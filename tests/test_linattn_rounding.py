@@ -27,8 +27,8 @@ def off_by_its_rounding(got, ref, size, c, what):
 
 
 def inputs(B, L, heads, Dk, Dv, kind, t, seed):
-    """random: no mean anywhere; keys: a direction that keys share and queries lack; values: the same of v and go, so that
-    the gradients of k and v meet it; means: all of them off zero, go without the mean of v."""
+    """random: no mean anywhere; keys, queries: a direction that the one share and the other lack, so that the terms of o and gv
+    cancel; values: one that v shares and go lacks, for gq and gk; means: all of them off zero, but for go."""
     r = gen(seed)
     Hq, Hk, Hv = heads
     q, k, v, go = r(B, L, Hq, Dk), r(B, L, Hk, Dk), r(B, L, Hv, Dv), r(B, L, max(heads), Dv)
